@@ -14,3 +14,8 @@ from .binding import SPEC_ERR_SCRATCH_LIMIT, spec_verify_attn_noalloc  # noqa: F
 from .binding import SPEC_DEBUG_NO_LOADS  # noqa: F401,E402
 from .binding import SPEC_COMMIT_CHAIN, SPEC_COMMIT_TREE, SpecCommitArgs, spec_commit  # noqa: F401,E402
 from .binding import SpecLmheadArgs, spec_lmhead_sample, spec_lmhead_sample_workspace  # noqa: F401,E402
+from .serving import (  # noqa: F401,E402
+    SPEC_STATUS_BAD_PAGE, SPEC_STATUS_BAD_RANGE, SpecLogprobArgs, SpecPagedArgs, SpecPrefillArgs, spec_paged_attn,
+    spec_paged_attn_workspace, spec_prefill_attn, spec_prefill_attn_workspace, spec_token_logprobs,
+    spec_token_logprobs_workspace,
+)

@@ -22,9 +22,10 @@ LIBNAME = "libspecverify.so"
 LIBPATH = os.path.join(LIBDIR, LIBNAME)
 
 SOURCES = ["attn.cu", "attn_tc.cu", "attn_tc_pair.cu", "sample.cu", "sample_tree.cu", "lmhead.cu", "commit.cu",
-           "api.cpp", "noalloc.cu", "launch_cache.cpp"]
+           "api.cpp", "noalloc.cu", "launch_cache.cpp", "serve_api.cpp", "paged_mma.cu", "chunk_plan.cu", "chunk_f32.cu",
+           "logprobs.cu"]
 HEADERS = ["common.cuh", "attn_common.cuh", "tcgen05.cuh", "ff.cuh", "attn_internal.h", "sample_internal.h",
-           "commit_internal.h", "lmhead_internal.h", "launch_cache.h"]
+           "commit_internal.h", "lmhead_internal.h", "launch_cache.h", "serve_internal.h", "serve_common.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -37,7 +38,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "spec_verify.h"))
+    files += [os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_serve.h")]
     files.append(os.path.abspath(__file__))
     return files
 

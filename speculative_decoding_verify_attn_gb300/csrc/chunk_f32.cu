@@ -1,0 +1,200 @@
+// Chunk attention on the CUDA cores: the fp32 form of the paged and packed operators.
+//
+// A CTA takes the pieces of the plan in turn: 32 query rows against 64-key tiles.  Thread (ty, tx)
+// of 16 x 16 holds the scores of rows 2 ty, 2 ty + 1 and keys tx + 16 j, and the output columns
+// 4 tx + 64 j of those rows.  fp32 throughout: scores by fp32 FMA, 2^x of the fused difference
+// s * scale - m (the rounding of m is the same for the whole row and cancels in the normalisation),
+// running maximum, sum and output in fp32.  Bound: the FMA pipes for long chunks (the tensor cores
+// have no fp32 type), HBM for few rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch_cache.h"
+#include "serve_common.cuh"
+#include "serve_internal.h"
+
+namespace specv {
+
+constexpr int kF32Threads = 256;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* src) {
+  if (sizeof(T) == 4) return *reinterpret_cast<const float4*>(src);
+  const uint2 u = *reinterpret_cast<const uint2*>(src);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+
+template <int D>
+constexpr size_t f32_smem_bytes() {
+  return sizeof(float) * (kF32Rows * (D + 4) + kF32Keys * (D + 4) + kF32Keys * D + kF32Rows * (kF32Keys + 4));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_constant__ ServeAttnParams p) {
+  pdl_launch_dependents();
+  extern __shared__ __align__(16) float sm[];
+  float* qs = sm;                                // [32][D + 4]
+  float* ks = qs + kF32Rows * (D + 4);           // [64][D + 4]
+  float* vs = ks + kF32Keys * (D + 4);           // [64][D]
+  float* ps = vs + kF32Keys * D;                 // [32][64 + 4]
+  constexpr int C4 = D / 4, OC = D / 64;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const T* q = reinterpret_cast<const T*>(p.q);
+  const T* k = reinterpret_cast<const T*>(p.k);
+  const T* v = reinterpret_cast<const T*>(p.v);
+  pdl_wait();  // the plan, and appended rows
+  const int n_items = __ldcg(&p.plan->n_items) * p.Hkv;
+  for (int round = 0;; ++round) {
+    const int idx = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (round * (int)gridDim.x >= n_items) break;
+    if (idx >= n_items) continue;
+    const int g = idx % p.Hkv;
+    const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p.items + idx / p.Hkv));
+    const int slot = __ldcg(&p.items[idx / p.Hkv].slot);
+    const int b = w0.x, row0 = w0.y, u0 = w0.z, u1 = w0.w;
+    const SeqInfo s = seq_info(p, b);
+    const int rows = min(kF32Rows, s.n * p.G - row0);
+    __syncthreads();
+    for (int i = tid; i < kF32Rows * C4; i += kF32Threads) {
+      const int r = i / C4, c = i % C4;
+      const float4 x = r < rows ? load4(q + q_offset(p, s, g, row0 + r) + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(qs + r * (D + 4) + c * 4) = x;
+    }
+    float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};
+    float4 o[2][OC];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < OC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = u0; u < u1; ++u) {
+      const int key0 = u * kF32Keys;
+      __syncthreads();
+      for (int i = tid; i < kF32Keys * C4; i += kF32Threads) {
+        const int r = i / C4, c = i % C4, t = key0 + r;
+        const bool in = t >= s.lo && t < s.len;
+        const int64_t off = in ? key_offset(p, s, b, g, t) : -1;
+        if (in && off < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+        *reinterpret_cast<float4*>(ks + r * (D + 4) + c * 4) = off >= 0 ? load4(k + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(vs + r * D + c * 4) = off >= 0 ? load4(v + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      __syncthreads();
+      float x[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[r][j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < C4; ++c) {
+        const float4 q0 = *reinterpret_cast<const float4*>(qs + (2 * ty) * (D + 4) + c * 4);
+        const float4 q1 = *reinterpret_cast<const float4*>(qs + (2 * ty + 1) * (D + 4) + c * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 kk = *reinterpret_cast<const float4*>(ks + (tx + 16 * j) * (D + 4) + c * 4);
+          x[0][j] = fmaf(q0.x, kk.x, fmaf(q0.y, kk.y, fmaf(q0.z, kk.z, fmaf(q0.w, kk.w, x[0][j]))));
+          x[1][j] = fmaf(q1.x, kk.x, fmaf(q1.y, kk.y, fmaf(q1.z, kk.z, fmaf(q1.w, kk.w, x[1][j]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int pos = s.len - s.n + (row0 + 2 * ty + r) / p.G;
+        float mx = neg_inf();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = key0 + tx + 16 * j;
+          const bool vis = t <= pos && t < s.len && (p.window <= 0 || t > pos - p.window);
+          if (!vis) x[r][j] = neg_inf();
+          mx = fmaxf(mx, x[r][j]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        // m in scaled log2 units; scale > 0 keeps the order (a negative or zero scale is refused)
+        const float mn = fmaxf(m[r], mx == neg_inf() ? mx : mx * p.scale_log2);
+        const float ref = mn == neg_inf() ? 0.f : mn;
+        const float a = m[r] == neg_inf() ? 0.f : exp2f(m[r] - mn);
+        m[r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = x[r][j] == neg_inf() ? 0.f : exp2f(fmaf(x[r][j], p.scale_log2, -ref));
+          ps[(2 * ty + r) * (kF32Keys + 4) + tx + 16 * j] = e;
+          sum += e;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[r] = l[r] * a + sum;
+#pragma unroll
+        for (int c = 0; c < OC; ++c) {
+          o[r][c].x *= a;
+          o[r][c].y *= a;
+          o[r][c].z *= a;
+          o[r][c].w *= a;
+        }
+      }
+      __syncwarp();  // a row's probabilities are written and read by the same half-warp
+#pragma unroll 4
+      for (int t = 0; t < kF32Keys; ++t) {
+        const float p0 = ps[(2 * ty) * (kF32Keys + 4) + t], p1 = ps[(2 * ty + 1) * (kF32Keys + 4) + t];
+#pragma unroll
+        for (int c = 0; c < OC; ++c) {
+          const float4 vv = *reinterpret_cast<const float4*>(vs + t * D + tx * 4 + 64 * c);
+          o[0][c].x = fmaf(p0, vv.x, o[0][c].x);
+          o[0][c].y = fmaf(p0, vv.y, o[0][c].y);
+          o[0][c].z = fmaf(p0, vv.z, o[0][c].z);
+          o[0][c].w = fmaf(p0, vv.w, o[0][c].w);
+          o[1][c].x = fmaf(p1, vv.x, o[1][c].x);
+          o[1][c].y = fmaf(p1, vv.y, o[1][c].y);
+          o[1][c].z = fmaf(p1, vv.z, o[1][c].z);
+          o[1][c].w = fmaf(p1, vv.w, o[1][c].w);
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int mrow = 2 * ty + r;
+      if (slot >= 0) {
+        const int64_t rec = (int64_t)slot * p.Hkv + g;
+        if (tx == 0) p.part_ml[rec * kF32Rows + mrow] = make_float2(m[r], l[r]);
+        float* dst = p.part_o + rec * D * kF32Rows + mrow;
+#pragma unroll
+        for (int c = 0; c < OC; ++c) {
+          dst[(tx * 4 + 64 * c) * kF32Rows] = o[r][c].x;
+          dst[(tx * 4 + 64 * c + 1) * kF32Rows] = o[r][c].y;
+          dst[(tx * 4 + 64 * c + 2) * kF32Rows] = o[r][c].z;
+          dst[(tx * 4 + 64 * c + 3) * kF32Rows] = o[r][c].w;
+        }
+      } else if (mrow < rows) {
+        const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+        const int64_t off = o_offset(p, s, g, row0 + mrow);
+#pragma unroll
+        for (int c = 0; c < OC; ++c) {
+          const float out[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t at = off + tx * 4 + 64 * c + e;
+            if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(out[e]);
+            else reinterpret_cast<float*>(p.o)[at] = out[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+static cudaError_t launch_f32(const ServeAttnParams& p, cudaStream_t stream) {
+  auto kern = chunk_attn_f32<T, D>;
+  const size_t smem = f32_smem_bytes<D>();
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(p.grid), dim3(kF32Threads), smem, stream, 0u, p);
+}
+
+cudaError_t launch_chunk_f32(const ServeAttnParams& p, int bf16, cudaStream_t stream) {
+  if (bf16) return p.D == 128 ? launch_f32<__nv_bfloat16, 128>(p, stream) : launch_f32<__nv_bfloat16, 64>(p, stream);
+  return p.D == 128 ? launch_f32<float, 128>(p, stream) : launch_f32<float, 64>(p, stream);
+}
+
+}  // namespace specv

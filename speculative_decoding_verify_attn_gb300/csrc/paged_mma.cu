@@ -1,0 +1,544 @@
+// Attention of small chunks (up to kMmaMaxRows query rows per sequence and kv head: decode, chain
+// verify) over a paged bf16 cache.
+//
+// Bound: HBM, one read of every visible key's K and V; a group's query rows share it.  Work is cut
+// into units of 128 keys, laid end to end over all (sequence, kv head) segments; CTA c takes units
+// [c * per, (c + 1) * per), so ragged lengths balance.  A warp owns 16 keys of every unit and runs
+// its own pipeline: a private 3-stage ring filled by its own cp.async (16-byte chunks at
+// XOR-swizzled places, zeros for slots outside [lo, len)), mma.sync m16n8k16 for Q K^T and P V, and
+// its own running (m, l, O), so no barrier of any kind stands between a warp and its data; the page
+// ids of a unit are looked up one unit ahead.  About 128 KB per SM stay in flight.  The eight warps'
+// states are joined through shared memory when a segment's part ends.  A part that is the whole
+// segment writes o; others leave a record for the merge kernel (a programmatic dependent).
+// Short segments (direct mode) are one CTA each and need no merge launch.
+// cp.async rather than TMA: a page may be any number of tokens in any layout, and the copies of an
+// SM's tensor-memory-access unit complete at a rate set by their number, which small pages multiply.
+//
+// Append: a new token's row is read from k_new / v_new and also stored into its slot by the warp
+// that owns the key; no CTA reads that slot in this call, so nothing has to be ordered.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch_cache.h"
+#include "serve_common.cuh"
+#include "serve_internal.h"
+
+namespace specv {
+
+constexpr int kMmaWarps = 8;
+constexpr int kMmaThreads = kMmaWarps * 32;
+constexpr int kMmaStages = 3;
+constexpr int kMmaCmbStride = 40;  // floats per row of the 32-column join buffer (conflict-free)
+
+__host__ __device__ constexpr int mma_stage_bytes(int D) { return 16 * D * 2 * 2; }  // a warp's K and V
+constexpr int kMmaCmbBytes = kMmaWarps * 16 * kMmaCmbStride * 4;
+__host__ __device__ constexpr size_t mma_smem_bytes(int D) {
+  return (size_t)kMmaWarps * kMmaStages * mma_stage_bytes(D) + kMmaCmbBytes;
+}
+
+// Units of a segment of sequence s; its first unit starts at key lo rounded down to 16.
+__device__ __forceinline__ int mma_units(const SeqInfo& s) {
+  return s.len > 0 ? (s.len - (s.lo & ~15) + kMmaUnit - 1) / kMmaUnit : 0;
+}
+
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sm) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) sm[warp] = v;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < kMmaWarps; ++w) t += sm[w];
+  return t;
+}
+
+__device__ __forceinline__ int64_t mma_per_cta(int64_t total, int grid) {
+  const int64_t per = (total + grid - 1) / grid;
+  return per < 1 ? 1 : per;
+}
+
+// Position in the walk over a CTA's units: unit u of nu of segment (b, g), `left` units to go.
+struct MmaWalk {
+  int b, g, u, nu;
+  int64_t left;
+  SeqInfo s;
+  __device__ __forceinline__ void step(const ServeAttnParams& p) {
+    if (--left <= 0) return;
+    if (++u < nu) return;
+    u = 0;
+    if (++g < p.Hkv) return;
+    g = 0;
+    do {
+      s = seq_info(p, ++b);
+      nu = mma_units(s);
+    } while (nu == 0);
+  }
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constant__ ServeAttnParams p) {
+  pdl_launch_dependents();
+  constexpr int KS = D / 16;        // k steps of Q K^T
+  constexpr int NT = D / 8;         // n tiles of P V
+  constexpr int CH = D / 8;         // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;      // rows one cp.async instruction of the warp covers
+  constexpr int STAGE = mma_stage_bytes(D);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scan[kMmaWarps];
+  __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
+  __shared__ int s_b;
+  __shared__ int64_t s_cum;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  float* cmb = reinterpret_cast<float*>(smem + (size_t)kMmaWarps * kMmaStages * STAGE);
+  if (cta == 0 && tid == 0) status_clear_for_launch(p.status);
+
+  // ---- this CTA's units
+  MmaWalk ld;
+  int64_t begin = 0;
+  if (p.direct) {
+    ld.b = cta / p.Hkv;
+    ld.g = cta % p.Hkv;
+    ld.u = 0;
+    ld.s = seq_info(p, ld.b);
+    ld.nu = mma_units(ld.s);
+    ld.left = ld.nu;
+    if (ld.s.bad && ld.g == 0 && tid == 0) status_report(p.status, ld.s.bad);
+    if (ld.nu == 0) {  // no keys: zeros for the rows of a bad length
+      for (int i = tid; i < ld.s.n * p.G * D; i += kMmaThreads) {
+        const int64_t off = o_offset(p, ld.s, ld.g, i / D) + i % D;
+        if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(0.f);
+        else reinterpret_cast<float*>(p.o)[off] = 0.f;
+      }
+      return;
+    }
+  } else {
+    int64_t mine = 0;
+    for (int b = tid; b < p.B; b += kMmaThreads) {
+      const SeqInfo s = seq_info(p, b);
+      mine += mma_units(s);
+      if (s.bad && cta == 0) status_report(p.status, s.bad);
+    }
+    const int64_t total = block_sum(mine, s_scan) * p.Hkv;
+    const int64_t per = mma_per_cta(total, p.grid);
+    begin = (int64_t)cta * per;
+    if (begin >= total) return;
+    ld.left = min(per, total - begin);
+    // the sequence whose units hold `begin`
+    int64_t run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kMmaThreads) {
+      const int b = b0 + tid;
+      const int64_t n = b < p.B ? (int64_t)mma_units(seq_info(p, b)) * p.Hkv : 0;
+      int64_t x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      int64_t pre = run, all = 0;
+#pragma unroll
+      for (int w = 0; w < kMmaWarps; ++w) {
+        if (w < warp) pre += s_scan[w];
+        all += s_scan[w];
+      }
+      const int64_t excl = pre + x - n;
+      if (n > 0 && begin >= excl && begin < excl + n) {
+        s_b = b;
+        s_cum = excl;
+      }
+      run += all;
+      if (begin < run) break;  // the same for all threads
+    }
+    __syncthreads();
+    ld.b = s_b;
+    ld.s = seq_info(p, ld.b);
+    ld.nu = mma_units(ld.s);
+    const int64_t rel = begin - s_cum;
+    ld.g = (int)(rel / ld.nu);
+    ld.u = (int)(rel % ld.nu);
+  }
+
+  // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
+  uint8_t* ring = smem + (size_t)warp * kMmaStages * STAGE;
+  const uint32_t ring_u32 = smem_u32(ring);
+  const __nv_bfloat16* kb = reinterpret_cast<const __nv_bfloat16*>(p.k);
+  const __nv_bfloat16* vb = reinterpret_cast<const __nv_bfloat16*>(p.v);
+  const __nv_bfloat16* knew = reinterpret_cast<const __nv_bfloat16*>(p.k_new);
+  const __nv_bfloat16* vnew = reinterpret_cast<const __nv_bfloat16*>(p.v_new);
+  MmaWalk cw = ld;  // the unit in compute
+  int page = -1;
+  auto look_up = [&]() {  // page id of this lane's key (lanes 16-31 repeat lanes 0-15)
+    const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
+    page = -1;
+    if (ld.left > 0 && t >= ld.s.lo && t < ld.s.len)
+      page = __ldg(p.table + (int64_t)ld.b * p.table_stride + t / p.page_size);
+  };
+  auto issue = [&](int stage) {
+    if (ld.left > 0) {
+      const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
+      const bool in = t >= ld.s.lo && t < ld.s.len;
+      const bool good = in && page >= 0 && page < p.num_pages;
+      const int64_t slot = good ? (int64_t)page * p.kv_sp + (int64_t)(t % p.page_size) * p.kv_st + (int64_t)ld.g * p.kv_sh : 0;
+      const int first_new = ld.s.len - ld.s.n;
+      const bool fresh = knew != nullptr && in && t >= first_new;
+      const int64_t src = fresh ? (int64_t)(ld.s.q0 + t - first_new) * p.new_st + (int64_t)ld.g * p.new_sh : slot;
+      const int kind = fresh ? 2 : (good ? 1 : 0);
+      if (__any_sync(0xffffffffu, in && !good)) {
+        if (in && !good) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+      }
+      const bool any_new = __any_sync(0xffffffffu, fresh);
+      const uint32_t dst = ring_u32 + stage * STAGE;
+      const int c = lane % CH;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + lane / CH;
+        const int64_t so = __shfl_sync(0xffffffffu, src, r);
+        const int sk = __shfl_sync(0xffffffffu, kind, r);
+        const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
+        cp_async16(at, (sk == 2 ? knew : kb) + so + c * 8, sk != 0);
+        cp_async16(at + 16 * D * 2, (sk == 2 ? vnew : vb) + so + c * 8, sk != 0);
+      }
+      if (any_new) {  // store the new rows into their slots
+#pragma unroll 1
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = i * RPI + lane / CH;
+          const int64_t so = __shfl_sync(0xffffffffu, src, r);
+          const int64_t to = __shfl_sync(0xffffffffu, slot, r);
+          const bool st = __shfl_sync(0xffffffffu, (int)(fresh && good), r) != 0;
+          if (st) {
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.k) + to + c * 8) =
+                __ldg(reinterpret_cast<const uint4*>(knew + so + c * 8));
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.v) + to + c * 8) =
+                __ldg(reinterpret_cast<const uint4*>(vnew + so + c * 8));
+          }
+        }
+      }
+      ld.step(p);
+      look_up();
+    }
+    cp_async_commit();
+  };
+  look_up();
+  issue(0);
+  issue(1);
+
+  // ---- compute
+  const int gid = lane >> 2, tq = lane & 3;
+  const float sc = p.scale_log2;
+  uint32_t qf[MT][KS][4];
+  float o[MT][NT][4];
+  float m_run[MT][2], l_run[MT][2];
+  int stage = 0;
+  bool fresh_part = true;
+  bool starts_at_begin = true;  // the current part starts where the CTA's range starts
+  int part_u0 = cw.u;
+  while (true) {
+    const int rows = cw.s.n * p.G;
+    if (fresh_part) {
+      fresh_part = false;
+      part_u0 = cw.u;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = mt * 16 + gid + h * 8;
+          const bool real = r < rows;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                                  (real ? q_offset(p, cw.s, cw.g, r) : 0));
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            qf[mt][ks][h] = real ? __ldg(src + ks * 8 + tq) : 0u;
+            qf[mt][ks][2 + h] = real ? __ldg(src + ks * 8 + 4 + tq) : 0u;
+          }
+          m_run[mt][h] = neg_inf();
+          l_run[mt][h] = 0.f;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+      }
+    }
+    issue(stage == 0 ? 2 : stage - 1);  // two units ahead
+    cp_async_wait<2>();
+    __syncwarp();
+    const uint32_t ks_u32 = ring_u32 + stage * STAGE, vs_u32 = ks_u32 + 16 * D * 2;
+    const int key0 = (cw.s.lo & ~15) + cw.u * kMmaUnit + warp * 16;
+
+    float s[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+    {
+      const int r = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4(ks_u32 + r * (D * 2) + (((ks * 2 + hc) ^ (r & 7)) << 4), b0, b1, b2, b3);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(s[mt][0], qf[mt][ks], b0, b1);
+          mma_bf16_16816(s[mt][1], qf[mt][ks], b2, b3);
+        }
+      }
+    }
+    // keys some row must not see: past the first new token, below the last row's window, or slots
+    // outside [lo, len)
+    const int first_new = cw.s.len - cw.s.n;
+    const bool edge = key0 + 16 > first_new || key0 < cw.s.lo || (p.window > 0 && key0 < cw.s.len - p.window);
+    uint32_t pf[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float mx[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int pos = first_new + (mt * 16 + gid + h * 8) / p.G;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = s[mt][nt][h * 2 + e] * sc;
+            if (edge) {
+              const int t = key0 + nt * 8 + tq * 2 + e;
+              const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
+              x = vis ? x : neg_inf();
+            }
+            s[mt][nt][h * 2 + e] = x;
+          }
+        mx[h] = fmaxf(fmaxf(s[mt][0][h * 2], s[mt][0][h * 2 + 1]), fmaxf(s[mt][1][h * 2], s[mt][1][h * 2 + 1]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      }
+      if (__any_sync(0xffffffffu, mx[0] > m_run[mt][0] || mx[1] > m_run[mt][1])) {
+        float a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(m_run[mt][h], mx[h]);
+          a[h] = m_run[mt][h] == neg_inf() ? 0.f : ex2_approx(m_run[mt][h] - mn);
+          m_run[mt][h] = mn;
+          l_run[mt][h] *= a[h];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[mt][nt][0] *= a[0];
+          o[mt][nt][1] *= a[0];
+          o[mt][nt][2] *= a[1];
+          o[mt][nt][3] *= a[1];
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float ref = m_run[mt][h] == neg_inf() ? 0.f : m_run[mt][h];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float p0 = ex2_approx(s[mt][nt][h * 2] - ref), p1 = ex2_approx(s[mt][nt][h * 2 + 1] - ref);
+          l_run[mt][h] += p0 + p1;
+          pf[mt][nt * 2 + h] = pack_bf16(p0, p1);
+        }
+      }
+    }
+    {
+      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hc = lane >> 4;
+#pragma unroll
+      for (int nn = 0; nn < NT / 2; ++nn) {
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4_trans(vs_u32 + r * (D * 2) + (((nn * 2 + hc) ^ (r & 7)) << 4), b0, b1, b2, b3);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(o[mt][nn * 2], pf[mt], b0, b1);
+          mma_bf16_16816(o[mt][nn * 2 + 1], pf[mt], b2, b3);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage before it is refilled
+    stage = stage == kMmaStages - 1 ? 0 : stage + 1;
+
+    // ---- end of the part: join the warps' states
+    const bool last = cw.left == 1;
+    if (cw.u + 1 == cw.nu || last) {
+      const bool whole = part_u0 == 0 && cw.u + 1 == cw.nu;
+      const int64_t rec = 2 * (int64_t)cta + (starts_at_begin ? 0 : 1);
+      starts_at_begin = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float l = l_run[mt][h];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          if (tq == 0) s_ml[warp][mt * 16 + gid + h * 8] = make_float2(m_run[mt][h], l);
+        }
+      __syncthreads();
+#pragma unroll 1
+      for (int mt = 0; mt < MT; ++mt) {
+        if (mt * 16 >= rows) break;
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = mt * 16 + gid + h * 8;
+          float M = neg_inf();
+#pragma unroll
+          for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+          const float own = s_ml[warp][r].x;
+          f[h] = own == neg_inf() ? 0.f : ex2_approx(own - M);
+        }
+        const int row = tid >> 4, col = (tid & 15) * 2;  // 16 rows x 32 columns by 256 threads
+        const int r = mt * 16 + row;
+        float M = neg_inf(), L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) {
+          const float2 v = s_ml[w][r];
+          L += v.x == neg_inf() ? 0.f : ex2_approx(v.x - M) * v.y;
+        }
+        const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+        if (!whole && r < rows && (tid & 15) == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M, L);
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float* dst = cmb + (warp * 16 + gid) * kMmaCmbStride + x * 8 + tq * 2;
+            const float* v = MT == 1 ? o[0][c4 * 4 + x] : (mt == 0 ? o[0][c4 * 4 + x] : o[MT - 1][c4 * 4 + x]);
+            *reinterpret_cast<float2*>(dst) = make_float2(v[0] * f[0], v[1] * f[0]);
+            *reinterpret_cast<float2*>(dst + 8 * kMmaCmbStride) = make_float2(v[2] * f[1], v[3] * f[1]);
+          }
+          __syncthreads();
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kMmaWarps; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(cmb + (w * 16 + row) * kMmaCmbStride + col);
+            sum.x += v.x;
+            sum.y += v.y;
+          }
+          if (r < rows) {
+            if (whole) {
+              const int64_t off = o_offset(p, cw.s, cw.g, r) + c4 * 32 + col;
+              if (p.o_bf16) {
+                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off;
+                const uint32_t v = pack_bf16(sum.x * inv, sum.y * inv);
+                if ((reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+                  *reinterpret_cast<uint32_t*>(dst) = v;
+                } else {
+                  reinterpret_cast<uint16_t*>(dst)[0] = (uint16_t)v;
+                  reinterpret_cast<uint16_t*>(dst)[1] = (uint16_t)(v >> 16);
+                }
+              } else {
+                float* dst = reinterpret_cast<float*>(p.o) + off;
+                dst[0] = sum.x * inv;
+                dst[1] = sum.y * inv;
+              }
+            } else {
+              *reinterpret_cast<float2*>(p.part_o + (rec * kMmaMaxRows + r) * D + c4 * 32 + col) = sum;
+            }
+          }
+          __syncthreads();
+        }
+      }
+      fresh_part = true;
+    }
+    if (last) break;
+    cw.step(p);
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the records of the segments that were split over CTAs; zeros for rows of a bad length.
+// One CTA per segment, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_constant__ ServeAttnParams p) {
+  __shared__ int64_t s_scan[kMmaWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
+  int64_t before = 0, all = 0;
+  for (int i = tid; i < p.B; i += kMmaThreads) {
+    const int u = mma_units(seq_info(p, i));
+    all += u;
+    if (i < b) before += u;
+  }
+  const int64_t total = block_sum(all, s_scan) * p.Hkv;
+  before = block_sum(before, s_scan) * p.Hkv;
+  const SeqInfo s = seq_info(p, b);
+  const int nu = mma_units(s), rows = s.n * p.G;
+  const int64_t per = mma_per_cta(total, p.grid);
+  const int64_t start = before + (int64_t)g * nu;
+  const int64_t c0 = start / per, c1 = nu > 0 ? (start + nu - 1) / per : c0;
+  pdl_wait();
+  if (nu > 0 && c0 == c1) return;  // written by its CTA
+  constexpr int E = D / 32;
+  for (int r = warp; r < rows; r += kMmaWarps) {
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float L = 0.f;
+    if (nu > 0) {
+      // the first record is its CTA's second unless the segment starts where that CTA starts
+      const int64_t first = 2 * c0 + (start % per == 0 ? 0 : 1);
+      float M = neg_inf();
+      for (int64_t c = c0 + lane; c <= c1; c += 32) {
+        const int64_t rec = c == c0 ? first : 2 * c;
+        M = fmaxf(M, __ldcg(&p.part_ml[rec * kMmaMaxRows + r]).x);
+      }
+      M = warp_max(M);
+      if (M != neg_inf()) {
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+          const int64_t rec = c == c0 ? first : 2 * c;
+          const float2 ml = __ldcg(&p.part_ml[rec * kMmaMaxRows + r]);
+          const float w = ml.x == neg_inf() ? 0.f : exp2f(ml.x - M);
+          L += w * ml.y;
+          const float* src = p.part_o + (rec * kMmaMaxRows + r) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __ldcg(src + e), acc[e]);
+        }
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int64_t off = o_offset(p, s, g, r) + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off + e] = __float2bfloat16_rn(acc[e] * inv);
+      else reinterpret_cast<float*>(p.o)[off + e] = acc[e] * inv;
+    }
+  }
+}
+
+size_t mma_workspace_bytes(int D) {
+  const size_t recs = 2 * (size_t)kServeMaxGrid * kMmaMaxRows;
+  return 256 + recs * (sizeof(float2) + (size_t)D * sizeof(float));
+}
+void mma_workspace_carve(void* ws, ServeAttnParams* p) {
+  char* b = reinterpret_cast<char*>(ws);
+  p->status = reinterpret_cast<uint32_t*>(b);
+  p->part_ml = reinterpret_cast<float2*>(b + 256);
+  p->part_o = reinterpret_cast<float*>(b + 256 + 2 * (size_t)kServeMaxGrid * kMmaMaxRows * sizeof(float2));
+}
+
+template <int D, int MT>
+static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
+  const size_t smem = mma_smem_bytes(D);
+  auto kern = paged_mma<D, MT>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.direct) return e;
+  return launch_dependent(paged_mma_merge<D>, dim3(p.B * p.Hkv), dim3(kMmaThreads), 0, stream, 0u, p);
+}
+
+cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream) {
+  const bool two = p.max_q * p.G > 16;
+  if (p.D == 128) return two ? launch_mma<128, 2>(p, stream) : launch_mma<128, 1>(p, stream);
+  return two ? launch_mma<64, 2>(p, stream) : launch_mma<64, 1>(p, stream);
+}
+
+}  // namespace specv

@@ -1,0 +1,232 @@
+// C ABI of the serving operators (include/spec_serve.h): argument validation, workspace sizing and
+// kernel launches.  As in api.cpp nothing here allocates memory or keeps state between calls.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "serve_internal.h"
+#include "spec_serve.h"
+
+namespace {
+
+using specv::LogprobParams;
+using specv::ServeAttnParams;
+
+constexpr int64_t kMaxTokens = 1 << 22;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int elem_bytes(int dtype) { return dtype == SPEC_BF16 ? 2 : 4; }
+
+struct Shape {
+  int B, Hq, Hkv, D, T, max_q, window, q_dtype, kv_dtype, o_dtype;
+};
+
+int check_shape(const Shape& s) {
+  if (s.B < 1 || s.B > 4096 || s.Hq < 1 || s.Hq > 4096 || s.Hkv < 1 || s.Hq % s.Hkv != 0) return SPEC_ERR_INVALID_ARG;
+  if (s.T < 0 || s.window < 0) return SPEC_ERR_INVALID_ARG;
+  if (s.max_q < 1) return SPEC_ERR_INVALID_ARG;
+  if (s.kv_dtype != SPEC_F32 && s.kv_dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (s.o_dtype != SPEC_F32 && s.o_dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (s.q_dtype != SPEC_F32 && s.q_dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (s.q_dtype != s.kv_dtype) return SPEC_ERR_UNSUPPORTED;
+  if (s.D != 64 && s.D != 128) return SPEC_ERR_UNSUPPORTED;
+  if (s.Hq / s.Hkv > 32 || s.T > kMaxTokens) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+// a 16-byte aligned base whose strides are multiples of 16 bytes
+bool vector_layout(const void* p, int dtype, int64_t s0, int64_t s1, int64_t s2 = 0) {
+  const int64_t per = 16 / elem_bytes(dtype);
+  return p && aligned(p, 16) && s0 >= 0 && s1 >= 0 && s2 >= 0 && s0 % per == 0 && s1 % per == 0 && s2 % per == 0;
+}
+bool o_layout(const void* o, int dtype, int64_t st, int64_t sh) {
+  return o && st >= 0 && sh >= 0 && aligned(o, elem_bytes(dtype));
+}
+bool int_layout(const int32_t* p) { return p && aligned(p, 4); }
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SPEC_ERR_INVALID_ARG;
+  return !ws || have < need || !aligned(ws, 256) ? SPEC_ERR_WORKSPACE : SPEC_OK;
+}
+
+int serve_grid() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  return sms < specv::kServeMaxGrid ? sms : specv::kServeMaxGrid;
+}
+
+// Few query rows per kv head: the mma.sync kernel reads the cache at the HBM rate; more rows need
+// the tensor cores' larger tiles.
+bool use_mma(int kv_dtype, int max_q, int G) {
+  return kv_dtype == SPEC_BF16 && (int64_t)max_q * G <= specv::kMmaMaxRows;
+}
+int chunk_row_tile(int kv_dtype) { (void)kv_dtype; return specv::kF32Rows; }
+
+ServeAttnParams base_params(const Shape& s, float scale) {
+  ServeAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.B = s.B; p.Hq = s.Hq; p.Hkv = s.Hkv; p.G = s.Hq / s.Hkv; p.D = s.D; p.T = s.T; p.max_q = s.max_q;
+  p.window = s.window;
+  p.o_bf16 = s.o_dtype == SPEC_BF16;
+  p.scale_log2 = (scale != 0.f ? scale : 1.0f / sqrtf((float)s.D)) * 1.4426950408889634f;
+  return p;
+}
+
+int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream) {
+  const int bf16 = kv_dtype == SPEC_BF16;
+  p.row_tile = chunk_row_tile(kv_dtype);
+  p.unit_keys = specv::kF32Keys;
+  specv::chunk_workspace_carve(ws, &p);
+  if (specv::launch_chunk_plan(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (p.k_new && specv::launch_chunk_append(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (specv::launch_chunk_f32(p, bf16, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  return specv::launch_chunk_merge(p, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_serve_struct_size(int which) {
+  switch (which) {
+    case 0: return sizeof(spec_paged_args);
+    case 1: return sizeof(spec_prefill_args);
+    case 2: return sizeof(spec_logprob_args);
+    default: return 0;
+  }
+}
+
+// ------------------------------------------------------------------ spec_paged_attn
+static Shape paged_shape(const spec_paged_args* a) {
+  // no chunk is longer than all rows together
+  const int max_q = a->max_q > a->T && a->T > 0 ? a->T : a->max_q;
+  return Shape{a->B, a->Hq, a->Hkv, a->D, a->T, max_q, a->window, a->q_dtype, a->kv_dtype, a->o_dtype};
+}
+
+size_t spec_paged_attn_workspace(const spec_paged_args* a) {
+  if (!a || check_shape(paged_shape(a)) != SPEC_OK) return 0;
+  const int G = a->Hq / a->Hkv;
+  return use_mma(a->kv_dtype, paged_shape(a).max_q, G)
+             ? specv::mma_workspace_bytes(a->D)
+             : specv::chunk_workspace_bytes(a->T, G, a->B, a->Hkv, a->D, chunk_row_tile(a->kv_dtype));
+}
+
+int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_ERR_INVALID_ARG;
+  const Shape s = paged_shape(a);
+  int st = check_shape(s);
+  if (st != SPEC_OK) return st;
+  if (a->page_size < 1 || a->page_size > 65536 || a->num_pages < 1 || a->table_cols < 1 || a->table_stride < 0 ||
+      (int64_t)a->table_cols * a->page_size > 0x7fffffff)
+    return SPEC_ERR_INVALID_ARG;
+  if (!isfinite(a->scale) || a->scale < 0.f) return SPEC_ERR_INVALID_ARG;
+  if ((a->k_new == nullptr) != (a->v_new == nullptr)) return SPEC_ERR_INVALID_ARG;
+  if (a->T == 0) return SPEC_OK;
+  if (!vector_layout(a->q, a->q_dtype, a->q_stride_t, a->q_stride_h) ||
+      !vector_layout(a->k_pages, a->kv_dtype, a->kv_stride_p, a->kv_stride_h, a->kv_stride_t) ||
+      !vector_layout(a->v_pages, a->kv_dtype, 0, 0) || !o_layout(a->o, a->o_dtype, a->o_stride_t, a->o_stride_h))
+    return SPEC_ERR_INVALID_ARG;
+  if (a->k_new && (!vector_layout(a->k_new, a->kv_dtype, a->new_stride_t, a->new_stride_h) ||
+                   !vector_layout(a->v_new, a->kv_dtype, 0, 0)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!int_layout(a->page_table) || !int_layout(a->q_start) || !int_layout(a->kv_len)) return SPEC_ERR_INVALID_ARG;
+  if ((st = check_workspace(a->workspace, a->workspace_bytes, spec_paged_attn_workspace(a))) != SPEC_OK) return st;
+
+  ServeAttnParams p = base_params(s, a->scale);
+  p.paged = 1;
+  p.page_size = a->page_size; p.num_pages = a->num_pages; p.table_cols = a->table_cols;
+  p.table = a->page_table; p.table_stride = a->table_stride;
+  p.q_start = a->q_start; p.kv_len = a->kv_len;
+  p.q = a->q; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;
+  p.k = a->k_pages; p.v = a->v_pages;
+  p.kv_sp = a->kv_stride_p; p.kv_sh = a->kv_stride_h; p.kv_st = a->kv_stride_t;
+  p.k_new = a->k_new; p.v_new = a->v_new; p.new_st = a->new_stride_t; p.new_sh = a->new_stride_h;
+  p.o = a->o; p.o_st = a->o_stride_t; p.o_sh = a->o_stride_h;
+  if ((p.grid = serve_grid()) < 1) return SPEC_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (!use_mma(a->kv_dtype, s.max_q, p.G)) return launch_chunk(p, a->kv_dtype, a->workspace, cs);
+  // the longest segment a sequence can have: the table's capacity, or its window
+  int64_t keys = (int64_t)a->table_cols * a->page_size;
+  if (a->window > 0 && keys > (int64_t)a->window + s.max_q + 15) keys = (int64_t)a->window + s.max_q + 15;
+  p.direct = keys <= specv::kMmaDirectKeys;
+  specv::mma_workspace_carve(a->workspace, &p);
+  return specv::launch_paged_mma(p, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ spec_prefill_attn
+static Shape prefill_shape(const spec_prefill_args* a) {
+  return Shape{a->B, a->Hq, a->Hkv, a->D, a->T, a->T > 1 ? a->T : 1, a->window, a->q_dtype, a->kv_dtype, a->o_dtype};
+}
+
+size_t spec_prefill_attn_workspace(const spec_prefill_args* a) {
+  if (!a || check_shape(prefill_shape(a)) != SPEC_OK) return 0;
+  return specv::chunk_workspace_bytes(a->T, a->Hq / a->Hkv, a->B, a->Hkv, a->D, chunk_row_tile(a->kv_dtype));
+}
+
+int spec_prefill_attn(const spec_prefill_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_ERR_INVALID_ARG;
+  const Shape s = prefill_shape(a);
+  int st = check_shape(s);
+  if (st != SPEC_OK) return st;
+  if (!isfinite(a->scale) || a->scale < 0.f) return SPEC_ERR_INVALID_ARG;
+  if (a->T == 0) return SPEC_OK;
+  if (!vector_layout(a->q, a->q_dtype, a->q_stride_t, a->q_stride_h) ||
+      !vector_layout(a->k, a->kv_dtype, a->kv_stride_t, a->kv_stride_h) || !vector_layout(a->v, a->kv_dtype, 0, 0) ||
+      !o_layout(a->o, a->o_dtype, a->o_stride_t, a->o_stride_h) || !int_layout(a->seq_start))
+    return SPEC_ERR_INVALID_ARG;
+  if ((st = check_workspace(a->workspace, a->workspace_bytes, spec_prefill_attn_workspace(a))) != SPEC_OK) return st;
+
+  ServeAttnParams p = base_params(s, a->scale);
+  p.q_start = a->seq_start;
+  p.q = a->q; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;
+  p.k = const_cast<void*>(a->k); p.v = const_cast<void*>(a->v);
+  p.kv_st = a->kv_stride_t; p.kv_sh = a->kv_stride_h;
+  p.o = a->o; p.o_st = a->o_stride_t; p.o_sh = a->o_stride_h;
+  if ((p.grid = serve_grid()) < 1) return SPEC_ERR_CUDA;
+  return launch_chunk(p, a->kv_dtype, a->workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ spec_token_logprobs
+static int check_logprobs(const spec_logprob_args* a) {
+  if (a->N < 0 || a->N > (1 << 24) || a->V < 1 || a->V > (1 << 24)) return SPEC_ERR_INVALID_ARG;
+  if (a->K < 0 || a->K > a->V) return SPEC_ERR_INVALID_ARG;
+  if (a->K > 32) return SPEC_ERR_UNSUPPORTED;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+size_t spec_token_logprobs_workspace(const spec_logprob_args* a) {
+  if (!a || check_logprobs(a) != SPEC_OK) return 0;
+  return specv::logprob_workspace_bytes(a->N, a->V, a->K);
+}
+
+int spec_token_logprobs(const spec_logprob_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_ERR_INVALID_ARG;
+  int st = check_logprobs(a);
+  if (st != SPEC_OK) return st;
+  if (a->N == 0) return SPEC_OK;
+  if (!a->logits || !aligned(a->logits, elem_bytes(a->dtype)) || a->logits_stride < a->V) return SPEC_ERR_INVALID_ARG;
+  if ((a->tokens == nullptr) != (a->logprobs == nullptr)) return SPEC_ERR_INVALID_ARG;
+  if ((a->top_ids == nullptr) != (a->K == 0) || (a->top_logprobs == nullptr) != (a->K == 0)) return SPEC_ERR_INVALID_ARG;
+  if (!a->logprobs && !a->entropy && a->K == 0) return SPEC_ERR_INVALID_ARG;
+  const void* words[5] = {a->tokens, a->logprobs, a->entropy, a->top_ids, a->top_logprobs};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return SPEC_ERR_INVALID_ARG;
+  if ((st = check_workspace(a->workspace, a->workspace_bytes, spec_token_logprobs_workspace(a))) != SPEC_OK) return st;
+  LogprobParams p;
+  memset(&p, 0, sizeof(p));
+  p.N = a->N; p.V = a->V; p.K = a->K;
+  p.bf16 = a->dtype == SPEC_BF16;
+  p.slices = specv::logprob_slices(a->N, a->V);
+  p.logits = a->logits; p.stride = a->logits_stride;
+  p.tokens = a->tokens; p.logprobs = a->logprobs; p.entropy = a->entropy;
+  p.top_ids = a->top_ids; p.top_lp = a->top_logprobs;
+  specv::logprob_workspace_carve(a->workspace, &p);
+  return specv::launch_token_logprobs(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK
+                                                                                               : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"

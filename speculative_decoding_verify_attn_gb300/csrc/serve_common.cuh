@@ -1,0 +1,68 @@
+// Shared by the attention kernels of the serving operators: what a sequence of the ragged batch is,
+// where its rows and keys lie, and cp.async.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "serve_internal.h"
+#include "spec_serve.h"
+
+namespace specv {
+
+// Sequence b of the batch: chunk rows q0 .. q0 + n - 1, `len` keys of which [lo, len) are seen by
+// some row.  len == 0: no keys to attend to (n == 0, or bad data: `bad` holds the status flag; with
+// n > 0 the rows' output is zero).
+struct SeqInfo {
+  int q0, n, len, lo;
+  uint32_t bad;
+};
+__device__ __forceinline__ SeqInfo seq_info(const ServeAttnParams& p, int b) {
+  SeqInfo s{0, 0, 0, 0, 0u};
+  const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
+  if (a < 0 || e < a || e > p.T || e - a > p.max_q) {
+    s.bad = (uint32_t)SPEC_STATUS_BAD_RANGE;
+    return s;
+  }
+  s.q0 = a;
+  s.n = e - a;
+  if (s.n == 0) return s;
+  const int len = p.kv_len ? __ldg(p.kv_len + b) : s.n;
+  if (len < s.n || (p.paged && (int64_t)len > (int64_t)p.table_cols * p.page_size)) {
+    s.bad = (uint32_t)SPEC_STATUS_BAD_KV_LEN;
+    return s;
+  }
+  s.len = len;
+  s.lo = p.window > 0 ? max(0, len - s.n + 1 - min(p.window, len)) : 0;
+  return s;
+}
+
+// 16-byte asynchronous copy to shared memory; zeros instead when `valid` is false (nothing is read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Element offset of token t's row of kv head g, or -1 for a page id out of range.
+__device__ __forceinline__ int64_t key_offset(const ServeAttnParams& p, const SeqInfo& s, int b, int g, int t) {
+  if (!p.paged) return (int64_t)(s.q0 + t) * p.kv_st + (int64_t)g * p.kv_sh;
+  const int page = __ldg(p.table + (int64_t)b * p.table_stride + t / p.page_size);
+  if (page < 0 || page >= p.num_pages) return -1;
+  return (int64_t)page * p.kv_sp + (int64_t)(t % p.page_size) * p.kv_st + (int64_t)g * p.kv_sh;
+}
+
+// Element offset of chunk row r (token r / G of the chunk, head r % G of kv head g's group).
+__device__ __forceinline__ int64_t q_offset(const ServeAttnParams& p, const SeqInfo& s, int g, int r) {
+  return (int64_t)(s.q0 + r / p.G) * p.q_st + (int64_t)(g * p.G + r % p.G) * p.q_sh;
+}
+__device__ __forceinline__ int64_t o_offset(const ServeAttnParams& p, const SeqInfo& s, int g, int r) {
+  return (int64_t)(s.q0 + r / p.G) * p.o_st + (int64_t)(g * p.G + r % p.G) * p.o_sh;
+}
+
+}  // namespace specv

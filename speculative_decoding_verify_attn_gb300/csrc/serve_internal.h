@@ -1,0 +1,108 @@
+// Internal interface between serve_api.cpp and the kernels of the serving operators (paged_mma.cu,
+// chunk_tc.cu, chunk_f32.cu, logprobs.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace specv {
+
+// CTAs a chunk kernel's work is split over at most (one per SM); the workspace is sized for it.
+constexpr int kServeMaxGrid = 160;
+// Query rows (tokens x heads of a group) per sequence and kv head up to which the mma.sync kernel
+// runs.
+constexpr int kMmaMaxRows = 32;
+constexpr int kMmaUnit = 128;   // keys per unit of work of the mma.sync kernel (16 per warp)
+// Segments of at most this many keys are one CTA of the mma.sync kernel each (no merge launch).
+constexpr int kMmaDirectKeys = 4 * kMmaUnit;
+constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
+constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
+constexpr int kF32Rows = 32;    // query rows per tile of the fp32 kernel
+constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
+
+// One piece of work of a chunk kernel, for every kv head: the row tile starting at row `row0` of
+// sequence b (row r: token r / G of the chunk, head r % G of the group), key units [u0, u1).
+// slot < 0: the piece is the whole tile and writes o; else its record is slot * Hkv + g.
+struct ChunkItem {
+  int32_t b, row0, u0, u1, slot, pad0, pad1, pad2;
+};
+// A tile whose pieces were split: records slot .. slot + pieces - 1.
+struct ChunkSplit {
+  int32_t b, row0, slot, pieces;
+};
+// Head of the plan in the workspace, after the status block.
+struct ChunkPlan {
+  int32_t n_items, n_splits, pad0, pad1;
+};
+
+struct ServeAttnParams {
+  int B, Hq, Hkv, G, D, T, max_q, window;
+  int paged, page_size, num_pages, table_cols;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* q_start;
+  const int32_t* kv_len;  // null for packed prompts: the length is the chunk's own
+  const void* q;
+  int64_t q_st, q_sh;
+  void* k;                // pages, or the packed rows
+  void* v;
+  int64_t kv_sp, kv_sh, kv_st;
+  const void* k_new;
+  const void* v_new;
+  int64_t new_st, new_sh;
+  void* o;
+  int64_t o_st, o_sh;
+  int o_bf16;
+  float scale_log2;       // scale * log2(e)
+  int grid;               // CTAs of the attention kernel
+  int direct;             // mma.sync kernel: a CTA per segment, no records
+  int row_tile, unit_keys;  // chunk kernels: rows per tile, keys per unit
+  int use_tma;            // tcgen05 kernel: the tensor maps are valid
+  int tma_page_keys;      // keys one copy brings (min(page_size, kTcKeys); packed: kTcKeys)
+  int max_tiles;          // chunk kernels: tiles (per kv head) the plan has room for
+  uint32_t* status;
+  ChunkPlan* plan;
+  ChunkItem* items;
+  ChunkSplit* splits;
+  float2* part_ml;        // chunk kernels [slot * Hkv + g][row_tile]; mma: [2 * cta + s][kMmaMaxRows]
+  float* part_o;          // chunk kernels [slot * Hkv + g][D][row_tile]; mma: [..][kMmaMaxRows][D]
+};
+
+// Upper bounds on what the plan can hold.
+inline int64_t chunk_max_tiles(int64_t T, int G, int B, int row_tile) { return T * G / row_tile + B; }
+
+size_t mma_workspace_bytes(int D);
+size_t chunk_workspace_bytes(int64_t T, int G, int B, int Hkv, int D, int row_tile);
+void mma_workspace_carve(void* ws, ServeAttnParams* p);
+void chunk_workspace_carve(void* ws, ServeAttnParams* p);
+
+cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream);
+// plan, [append], attention, merge
+cudaError_t launch_chunk_plan(const ServeAttnParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_append(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                            cudaStream_t stream);
+cudaError_t launch_chunk_f32(const ServeAttnParams& p, int bf16, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ServeAttnParams& p, cudaStream_t stream);
+
+struct LogprobParams {
+  int N, V, K, bf16, slices;
+  const void* logits;
+  int64_t stride;
+  const int32_t* tokens;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_lp;
+  uint32_t* status;
+  float4* part_stat;               // [N][slices]: max, sum, weighted sum
+  unsigned long long* part_keys;   // [N][slices][K]
+};
+int logprob_slices(int N, int V);
+size_t logprob_workspace_bytes(int N, int V, int K);
+void logprob_workspace_carve(void* ws, LogprobParams* p);
+cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t stream);
+
+}  // namespace specv

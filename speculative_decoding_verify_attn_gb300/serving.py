@@ -1,0 +1,283 @@
+"""ctypes binding of the serving operators (include/spec_serve.h): attention of new-token chunks over a
+paged KV cache, attention over packed prompts, and token log probabilities.
+
+Same names as the C ABI and the same manner as ``binding``: every function checks its tensors,
+marshals them into the argument struct and calls the library on the current stream of the tensors'
+device (or on ``stream``).  There is no fallback.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from ctypes import POINTER, Structure, byref, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+
+from .binding import SPEC_BF16, SPEC_ERR_INVALID_ARG, SPEC_F32, SPEC_OK, SpecError, lib
+
+SPEC_STATUS_BAD_RANGE = 16
+SPEC_STATUS_BAD_PAGE = 32
+
+
+class SpecPagedArgs(Structure):
+    _fields_ = [
+        ("B", c_int32), ("Hq", c_int32), ("Hkv", c_int32), ("D", c_int32), ("T", c_int32), ("max_q", c_int32),
+        ("q_dtype", c_int32), ("kv_dtype", c_int32), ("o_dtype", c_int32),
+        ("page_size", c_int32), ("num_pages", c_int32), ("table_cols", c_int32),
+        ("window", c_int32), ("scale", c_float),
+        ("q", c_void_p), ("q_stride_t", c_int64), ("q_stride_h", c_int64),
+        ("k_pages", c_void_p), ("v_pages", c_void_p),
+        ("kv_stride_p", c_int64), ("kv_stride_h", c_int64), ("kv_stride_t", c_int64),
+        ("page_table", c_void_p), ("table_stride", c_int64), ("q_start", c_void_p), ("kv_len", c_void_p),
+        ("k_new", c_void_p), ("v_new", c_void_p), ("new_stride_t", c_int64), ("new_stride_h", c_int64),
+        ("o", c_void_p), ("o_stride_t", c_int64), ("o_stride_h", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class SpecPrefillArgs(Structure):
+    _fields_ = [
+        ("B", c_int32), ("Hq", c_int32), ("Hkv", c_int32), ("D", c_int32), ("T", c_int32), ("window", c_int32),
+        ("q_dtype", c_int32), ("kv_dtype", c_int32), ("o_dtype", c_int32), ("scale", c_float),
+        ("q", c_void_p), ("q_stride_t", c_int64), ("q_stride_h", c_int64),
+        ("k", c_void_p), ("v", c_void_p), ("kv_stride_t", c_int64), ("kv_stride_h", c_int64),
+        ("seq_start", c_void_p),
+        ("o", c_void_p), ("o_stride_t", c_int64), ("o_stride_h", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class SpecLogprobArgs(Structure):
+    _fields_ = [
+        ("N", c_int32), ("V", c_int32), ("K", c_int32), ("dtype", c_int32),
+        ("logits", c_void_p), ("logits_stride", c_int64), ("tokens", c_void_p),
+        ("logprobs", c_void_p), ("entropy", c_void_p), ("top_ids", c_void_p), ("top_logprobs", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+_lib = None
+
+
+def _serve_lib():
+    """The loaded library with this header's prototypes set (once)."""
+    global _lib
+    if _lib is None:
+        L = lib()
+        for name, cls in (("spec_paged_attn", SpecPagedArgs), ("spec_prefill_attn", SpecPrefillArgs),
+                          ("spec_token_logprobs", SpecLogprobArgs)):
+            fn, ws = getattr(L, name), getattr(L, name + "_workspace")
+            fn.argtypes, fn.restype = [POINTER(cls), c_void_p], c_int
+            ws.argtypes, ws.restype = [POINTER(cls)], c_size_t
+        L.spec_serve_struct_size.argtypes, L.spec_serve_struct_size.restype = [c_int], c_size_t
+        for i, cls in enumerate((SpecPagedArgs, SpecPrefillArgs, SpecLogprobArgs)):
+            if L.spec_serve_struct_size(i) != ctypes.sizeof(cls):
+                raise RuntimeError(f"ABI mismatch for {cls.__name__}: library {L.spec_serve_struct_size(i)} bytes, "
+                                   f"binding {ctypes.sizeof(cls)}")
+        _lib = L
+    return _lib
+
+
+# ---------------------------------------------------------------------------- helpers
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return SPEC_BF16
+    if t.dtype == torch.float32:
+        return SPEC_F32
+    raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _check(device, **tensors):
+    """All on one CUDA device, with a contiguous innermost dimension."""
+    if device.type != "cuda":
+        raise ValueError("all tensors must be CUDA tensors (host buffers: copy them to the device first)")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+            raise ValueError(f"{name}: innermost dimension must be contiguous")
+
+
+def _int32(shapes, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shapes[name]):
+            raise ValueError(f"{name} must be int32 of shape {shapes[name]}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _call(name, args, device, workspace, stream):
+    """Sizes the workspace, fills it in and makes the call on the tensors' device."""
+    import torch
+    L = _serve_lib()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, args, device, workspace, stream)
+    need = getattr(L, name + "_workspace")(byref(args))
+    if need == 0:
+        # the call itself says why the sizes are refused
+        raise SpecError(getattr(L, name)(byref(args), None) or SPEC_ERR_INVALID_ARG, name)
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        stream = current
+    elif not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream != current:
+            workspace.record_stream(stream)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        if workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace too small: need {need} bytes")
+    args.workspace = workspace.data_ptr()
+    args.workspace_bytes = workspace.numel() * workspace.element_size()
+    st = getattr(L, name)(byref(args), stream.cuda_stream)
+    if st != SPEC_OK:
+        raise SpecError(st, name)
+
+
+def _workspace_bytes(name, args) -> int:
+    need = getattr(_serve_lib(), name + "_workspace")(byref(args))
+    if need == 0:
+        raise SpecError(SPEC_ERR_INVALID_ARG, name + "_workspace")
+    return need
+
+
+# ---------------------------------------------------------------------------- paged attention
+def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_q, k_new=None, v_new=None,
+                    window: int = 0, scale: float = 0.0) -> SpecPagedArgs:
+    """Fill SpecPagedArgs from tensors (no workspace yet)."""
+    T, Hq, D = q.shape
+    pages, Hkv, page_size, D2 = k_pages.shape
+    B, cols = page_table.shape
+    if D2 != D or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with q's D and equal strides")
+    if v_pages.dtype != k_pages.dtype:
+        raise TypeError("k_pages and v_pages must share a dtype")
+    if o.shape != q.shape:
+        raise ValueError("o must have q's shape")
+    _int32({"page_table": (B, cols), "q_start": (B + 1,), "kv_len": (B,)}, page_table=page_table, q_start=q_start,
+           kv_len=kv_len)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        if tuple(k_new.shape) != (T, Hkv, D) or v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
+            raise ValueError("k_new, v_new must be [T, Hkv, D] with equal strides")
+        if k_new.dtype != k_pages.dtype or v_new.dtype != k_pages.dtype:
+            raise TypeError("k_new, v_new must have the cache's dtype")
+    return SpecPagedArgs(
+        B, Hq, Hkv, D, T, int(max_q), _dtype_code(q), _dtype_code(k_pages), _dtype_code(o), page_size, pages, cols,
+        int(window), scale, q.data_ptr(), q.stride(0), q.stride(1), k_pages.data_ptr(), v_pages.data_ptr(),
+        k_pages.stride(0), k_pages.stride(1), k_pages.stride(2), page_table.data_ptr(), page_table.stride(0),
+        q_start.data_ptr(), kv_len.data_ptr(), None if k_new is None else k_new.data_ptr(),
+        None if v_new is None else v_new.data_ptr(), 0 if k_new is None else k_new.stride(0),
+        0 if k_new is None else k_new.stride(1), o.data_ptr(), o.stride(0), o.stride(1), None, 0)
+
+
+def spec_paged_attn_workspace(q, k_pages, page_table, o, *, max_q) -> int:
+    """Bytes of workspace spec_paged_attn needs for tensors of these shapes."""
+    T, Hq, D = q.shape
+    a = SpecPagedArgs(B=page_table.shape[0], Hq=Hq, Hkv=k_pages.shape[1], D=D, T=T, max_q=int(max_q),
+                      q_dtype=_dtype_code(q), kv_dtype=_dtype_code(k_pages), o_dtype=_dtype_code(o))
+    return _workspace_bytes("spec_paged_attn", a)
+
+
+def spec_paged_attn(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_q, k_new=None, v_new=None,
+                    window: int = 0, scale: float = 0.0, workspace=None, stream=None):
+    """Attention of a ragged batch of new-token chunks over a paged cache.
+
+    q, o [T, Hq, D]; k_pages, v_pages [pages, Hkv, page_size, D] (any strides, so a permuted view of
+    another page layout serves too); page_table [B, cols] int32; q_start [B + 1] int32, the rows of
+    sequence b being q_start[b] .. q_start[b + 1] - 1; kv_len [B] int32, the new tokens included.
+    max_q: an upper bound on the chunk lengths.  With k_new, v_new [T, Hkv, D] the call also writes
+    them into the new tokens' slots.  window > 0: rows see the last `window` tokens only.  Writes o
+    and returns it."""
+    _check(q.device, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, q_start=q_start, kv_len=kv_len,
+           o=o, k_new=k_new, v_new=v_new)
+    a = paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, max_q=max_q, k_new=k_new, v_new=v_new,
+                        window=window, scale=scale)
+    _call("spec_paged_attn", a, q.device, workspace, stream)
+    return o
+
+
+# ---------------------------------------------------------------------------- packed prompts
+def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 0.0) -> SpecPrefillArgs:
+    """Fill SpecPrefillArgs from tensors (no workspace yet)."""
+    T, Hq, D = q.shape
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k, v must be [T, Hkv, D] with equal strides")
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must share a dtype")
+    if o.shape != q.shape:
+        raise ValueError("o must have q's shape")
+    B = seq_start.shape[0] - 1
+    _int32({"seq_start": (B + 1,)}, seq_start=seq_start)
+    return SpecPrefillArgs(
+        B, Hq, k.shape[1], D, T, int(window), _dtype_code(q), _dtype_code(k), _dtype_code(o), scale,
+        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+        seq_start.data_ptr(), o.data_ptr(), o.stride(0), o.stride(1), None, 0)
+
+
+def spec_prefill_attn_workspace(q, k, seq_start, o) -> int:
+    """Bytes of workspace spec_prefill_attn needs for tensors of these shapes."""
+    T, Hq, D = q.shape
+    a = SpecPrefillArgs(B=seq_start.shape[0] - 1, Hq=Hq, Hkv=k.shape[1], D=D, T=T, q_dtype=_dtype_code(q),
+                        kv_dtype=_dtype_code(k), o_dtype=_dtype_code(o))
+    return _workspace_bytes("spec_prefill_attn", a)
+
+
+def spec_prefill_attn(q, k, v, seq_start, o, *, window: int = 0, scale: float = 0.0, workspace=None, stream=None):
+    """Causal attention over whole prompts packed one after the other.
+
+    q, o [T, Hq, D]; k, v [T, Hkv, D]; seq_start [B + 1] int32, sequence b being rows seq_start[b] ..
+    seq_start[b + 1] - 1.  window > 0: rows see the last `window` tokens only.  Writes o and returns
+    it."""
+    _check(q.device, q=q, k=k, v=v, seq_start=seq_start, o=o)
+    a = prefill_attn_args(q, k, v, seq_start, o, window=window, scale=scale)
+    _call("spec_prefill_attn", a, q.device, workspace, stream)
+    return o
+
+
+# ---------------------------------------------------------------------------- log probabilities
+def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None) -> SpecLogprobArgs:
+    """Fill SpecLogprobArgs from tensors (no workspace yet)."""
+    import torch
+    N, V = logits.shape
+    if (tokens is None) != (logprobs is None):
+        raise ValueError("tokens and logprobs go together")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    K = 0 if top_ids is None else top_ids.shape[1]
+    _int32({"tokens": (N,), "top_ids": (N, K)}, tokens=tokens, top_ids=top_ids)
+    for name, t, shape in (("logprobs", logprobs, (N,)), ("entropy", entropy, (N,)), ("top_logprobs", top_logprobs, (N, K))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be float32 of shape {shape}")
+    for t in (tokens, logprobs, entropy, top_ids, top_logprobs):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tokens and the outputs must be contiguous")
+    ptr = [None if t is None or t.numel() == 0 else t.data_ptr() for t in (tokens, logprobs, entropy, top_ids, top_logprobs)]
+    # the stride of a single row may be anything
+    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), logits.stride(0) if N > 1 else V, *ptr,
+                           None, 0)
+
+
+def spec_token_logprobs_workspace(logits, K: int = 0) -> int:
+    """Bytes of workspace spec_token_logprobs needs for these logits and K alternatives."""
+    return _workspace_bytes("spec_token_logprobs", SpecLogprobArgs(N=logits.shape[0], V=logits.shape[1], K=K,
+                                                                   dtype=_dtype_code(logits)))
+
+
+def spec_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None, workspace=None,
+                        stream=None):
+    """Log probabilities of given tokens, with the rows' entropies and top alternatives.
+
+    logits [N, V] fp32 or bf16; tokens [N] int32 and logprobs [N] fp32 (both or neither); entropy [N]
+    fp32; top_ids [N, K] int32 and top_logprobs [N, K] fp32 (K <= 32, descending, lower ids first
+    among equals).  Outputs not wanted are None.  Writes them and returns logprobs."""
+    _check(logits.device, logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_ids=top_ids,
+           top_logprobs=top_logprobs)
+    a = token_logprobs_args(logits, tokens, logprobs, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs)
+    _call("spec_token_logprobs", a, logits.device, workspace, stream)
+    return logprobs
