@@ -23,9 +23,10 @@ LIBPATH = os.path.join(LIBDIR, LIBNAME)
 
 SOURCES = ["attn.cu", "attn_tc.cu", "attn_tc_pair.cu", "sample.cu", "sample_tree.cu", "lmhead.cu", "commit.cu",
            "api.cpp", "noalloc.cu", "launch_cache.cpp", "serve_api.cpp", "paged_mma.cu", "chunk_plan.cu", "chunk_f32.cu",
-           "logprobs.cu"]
+           "chunk_tc.cu", "logprobs.cu"]
 HEADERS = ["common.cuh", "attn_common.cuh", "tcgen05.cuh", "ff.cuh", "attn_internal.h", "sample_internal.h",
-           "commit_internal.h", "lmhead_internal.h", "launch_cache.h", "serve_internal.h", "serve_common.cuh"]
+           "commit_internal.h", "lmhead_internal.h", "launch_cache.h", "serve_internal.h", "serve_common.cuh",
+           "tensor_map.h"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

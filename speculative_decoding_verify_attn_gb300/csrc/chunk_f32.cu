@@ -18,20 +18,12 @@ namespace specv {
 
 constexpr int kF32Threads = 256;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* src) {
-  if (sizeof(T) == 4) return *reinterpret_cast<const float4*>(src);
-  const uint2 u = *reinterpret_cast<const uint2*>(src);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
-
 template <int D>
 constexpr size_t f32_smem_bytes() {
   return sizeof(float) * (kF32Rows * (D + 4) + kF32Keys * (D + 4) + kF32Keys * D + kF32Rows * (kF32Keys + 4));
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_constant__ ServeAttnParams p) {
   pdl_launch_dependents();
   extern __shared__ __align__(16) float sm[];
@@ -41,9 +33,9 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
   float* ps = vs + kF32Keys * D;                 // [32][64 + 4]
   constexpr int C4 = D / 4, OC = D / 64;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const T* q = reinterpret_cast<const T*>(p.q);
-  const T* k = reinterpret_cast<const T*>(p.k);
-  const T* v = reinterpret_cast<const T*>(p.v);
+  const float* q = reinterpret_cast<const float*>(p.q);
+  const float* k = reinterpret_cast<const float*>(p.k);
+  const float* v = reinterpret_cast<const float*>(p.v);
   pdl_wait();  // the plan, and appended rows
   const int n_items = __ldcg(&p.plan->n_items) * p.Hkv;
   for (int round = 0;; ++round) {
@@ -59,7 +51,7 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
     __syncthreads();
     for (int i = tid; i < kF32Rows * C4; i += kF32Threads) {
       const int r = i / C4, c = i % C4;
-      const float4 x = r < rows ? load4(q + q_offset(p, s, g, row0 + r) + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 x = r < rows ? *reinterpret_cast<const float4*>(q + q_offset(p, s, g, row0 + r) + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       *reinterpret_cast<float4*>(qs + r * (D + 4) + c * 4) = x;
     }
     float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};
@@ -76,8 +68,8 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
         const bool in = t >= s.lo && t < s.len;
         const int64_t off = in ? key_offset(p, s, b, g, t) : -1;
         if (in && off < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
-        *reinterpret_cast<float4*>(ks + r * (D + 4) + c * 4) = off >= 0 ? load4(k + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(vs + r * D + c * 4) = off >= 0 ? load4(v + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(ks + r * (D + 4) + c * 4) = off >= 0 ? *reinterpret_cast<const float4*>(k + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(vs + r * D + c * 4) = off >= 0 ? *reinterpret_cast<const float4*>(v + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       __syncthreads();
       float x[2][4];
@@ -183,18 +175,17 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
   }
 }
 
-template <typename T, int D>
+template <int D>
 static cudaError_t launch_f32(const ServeAttnParams& p, cudaStream_t stream) {
-  auto kern = chunk_attn_f32<T, D>;
+  auto kern = chunk_attn_f32<D>;
   const size_t smem = f32_smem_bytes<D>();
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.grid), dim3(kF32Threads), smem, stream, 0u, p);
 }
 
-cudaError_t launch_chunk_f32(const ServeAttnParams& p, int bf16, cudaStream_t stream) {
-  if (bf16) return p.D == 128 ? launch_f32<__nv_bfloat16, 128>(p, stream) : launch_f32<__nv_bfloat16, 64>(p, stream);
-  return p.D == 128 ? launch_f32<float, 128>(p, stream) : launch_f32<float, 64>(p, stream);
+cudaError_t launch_chunk_f32(const ServeAttnParams& p, cudaStream_t stream) {
+  return p.D == 128 ? launch_f32<128>(p, stream) : launch_f32<64>(p, stream);
 }
 
 }  // namespace specv

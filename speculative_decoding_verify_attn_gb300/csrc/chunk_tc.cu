@@ -1,0 +1,548 @@
+// Chunk attention on the 5th-generation tensor core: bf16 chunks of more than kMmaMaxRows query rows
+// per sequence and kv head over a paged cache, and packed prompts.
+//
+// One CTA per SM takes the pieces of the plan (chunk_plan.cu) in turn: 256 query rows (tokens x heads
+// of one kv head's group, two blocks of 128) against 128-key tiles.  Flash attention with the scores
+// of a tile in TMEM: S_w = Q_w K^T (M = N = 128, both operands in shared memory), then the row maximum,
+// P_w = 2^(s * scale - mu) rounded to bf16 over S_w's first 64 columns, then O_w += P_w V (P from TMEM,
+// V as an MN-major operand).  mu moves only when a tile's maximum exceeds it by more than 2^8 (O is
+// then rescaled in TMEM), which keeps every P below 2^8 and the result exact after normalisation.
+//   warps 0, 1    loaders: K and V tiles into a ring of 32 KB stages (D = 128).  A tile that lies
+//                 wholly inside the sequence comes by TMA; edges (the sequence's end, tokens before the
+//                 window, bad page ids) and pages too small for TMA by cp.async with zeros in the gaps,
+//                 so nothing outside [lo, len) reaches the tensor core, NaN or not.
+//   warps 2, 3    MMA issuers, one per block; each walks the stages in order (K: Q K^T, V: P V), so
+//                 while one block's warps compute probabilities the other block's products run.
+//   warps 4-11    two warpgroups, a thread per query row.
+// Why 128-key tiles: an operand in shared memory is read anew by every instruction; per pair of blocks
+// and 128 keys that is 192 KB of reads with 128-key scores and 256 KB with 64-key ones, against 2048
+// cycles of products at 128 B per cycle.
+// TMEM columns (512): block w at 256 w: S [0, 128), P over [0, 64), O [128, 128 + D).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch_cache.h"
+#include "serve_common.cuh"
+#include "serve_internal.h"
+#include "tcgen05.cuh"
+
+namespace specv {
+
+constexpr int kCtThreads = 128 + 2 * 128;
+constexpr uint32_t kCtTmemCols = 512;
+constexpr int kCtHalf = 128 * 128;  // 128 rows of one 64-column half: 16 KB
+constexpr float kCtRescaleLog2 = 8.0f;
+constexpr int kCtLag = 2;           // steps a loader's cp.async tiles may be in flight
+
+template <int D>
+struct Ct {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * kCtHalf;       // a K or V tile, or a Q block
+  static constexpr int kStages = D == 128 ? 5 : 10;     // 160 KB
+  static constexpr size_t kSmem = 1024 + 2 * (size_t)kTile + (size_t)kStages * kTile;
+  static constexpr uint32_t kIdescQK = tc::idesc_bf16(128, 128, 0, 0);
+  static constexpr uint32_t kIdescPV = tc::idesc_bf16(128, D, 0, 1);
+};
+
+__device__ __forceinline__ uint32_t ct_col_s(int w) { return 256u * w; }
+__device__ __forceinline__ uint32_t ct_col_o(int w) { return 256u * w + 128u; }
+
+struct CtItem {
+  int b, g, row0, u0, u1, slot;
+  SeqInfo s;
+};
+// The round's piece of this CTA (pieces sorted by size: forth and back over the CTAs).
+__device__ __forceinline__ bool ct_item(const ServeAttnParams& p, int n_items, int round, CtItem& it) {
+  const int grid = gridDim.x, cta = blockIdx.x;
+  const int64_t idx = (int64_t)round * grid + ((round & 1) ? grid - 1 - cta : cta);
+  if (idx >= n_items) return false;
+  const ChunkItem* src = p.items + idx / p.Hkv;
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(src));
+  it.b = a.x;
+  it.row0 = a.y;
+  it.u0 = a.z;
+  it.u1 = a.w;
+  it.slot = __ldcg(&src->slot);
+  it.g = (int)(idx % p.Hkv);
+  it.s = seq_info(p, it.b);
+  return true;
+}
+__device__ __forceinline__ int ct_rounds(int n_items) { return (n_items + (int)gridDim.x - 1) / (int)gridDim.x; }
+
+// Units of the piece that block w's rows see: [b0, b1), empty for a block without rows.
+__device__ __forceinline__ void ct_block_units(const ServeAttnParams& p, const CtItem& it, int w, int& b0, int& b1) {
+  const int rows = it.s.n * p.G, r0 = it.row0 + w * 128;
+  b0 = b1 = it.u0;
+  if (r0 >= rows) return;
+  const int rl = min(r0 + 128, rows) - 1, base = it.s.len - it.s.n;
+  const int first = p.window > 0 ? max(0, base + r0 / p.G + 1 - min(p.window, it.s.len)) : 0;
+  b0 = max(it.u0, first / kTcKeys);
+  b1 = max(b0, min(it.u1, (base + rl / p.G) / kTcKeys + 1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCtThreads, 1)
+    chunk_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ ServeAttnParams p) {
+  using C = Ct<D>;
+  constexpr int NS = C::kStages;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_abort;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* qs = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // [block][half][128 rows][128 B]
+  uint8_t* stages = qs + 2 * C::kTile;
+  const uint32_t qs_u32 = smem_u32(qs), stages_u32 = smem_u32(stages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 2);   // one arrival per loader warp
+      mbar_init(&empty[i], 2);  // one per issuer
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sfull[w], 1);
+      mbar_init(&pfull[w], 4);
+      mbar_init(&pvdone[w], 1);
+      mbar_init(&ofree[w], 4);
+      mbar_init(&qfull[w], 4);
+      mbar_init(&drain[w], 1);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tc::alloc(&tmem_base, kCtTmemCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();  // the plan, and appended rows
+  const int n_items = __ldcg(&p.plan->n_items) * p.Hkv;
+  const int rounds = ct_rounds(n_items);
+
+  auto fail = [&]() {
+    s_abort = 1;
+    atomicOr(p.status, (uint32_t)SPEC_STATUS_TIMEOUT);
+  };
+
+  // registers: 128 x 88 + 256 x 208 = 384 x 168, what the block was launched with
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+
+  if (warp < 2) {
+    // ------------------------------------------------------------------ loaders
+    constexpr int CH = D / 8, RPI = 32 / CH;
+    const __nv_bfloat16* kv[2] = {reinterpret_cast<const __nv_bfloat16*>(p.k),
+                                  reinterpret_cast<const __nv_bfloat16*>(p.v)};
+    int step = 0;
+    uint32_t by_copy = 0;  // bit i: the step i + 1 before the current one was filled by cp.async
+    bool ok = true;
+    // the step kCtLag before has landed: hand its stage over if it was filled by cp.async
+    auto hand_over = [&](int done) {
+      tc::fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[done % NS]);
+    };
+    for (int round = 0; ok && round < rounds; ++round) {
+      CtItem it;
+      if (!ct_item(p, n_items, round, it)) continue;
+      for (int u = it.u0; ok && u < it.u1; ++u) {
+        const int key0 = u * kTcKeys;
+        // rows of the tile: offsets of this lane's two of the warp's 64 keys, -1 where zeros go
+        bool tma = p.use_tma && key0 >= it.s.lo && key0 + kTcKeys <= it.s.len;
+        int64_t off[2] = {-1, -1};
+        int page = 0, in_page = 0;
+        if (tma) {
+          if (!p.paged) {
+            in_page = it.s.q0 + key0;
+          } else {
+            const int t = key0 + (lane * p.tma_page_keys) % kTcKeys;
+            page = __ldg(p.table + (int64_t)it.b * p.table_stride + t / p.page_size);
+            in_page = t % p.page_size;
+            tma = __all_sync(0xffffffffu, page >= 0 && page < p.num_pages);
+          }
+        }
+        if (!tma) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = key0 + warp * 64 + i * 32 + lane;
+            if (t >= it.s.lo && t < it.s.len) {
+              off[i] = key_offset(p, it.s, it.b, it.g, t);
+              if (off[i] < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+            }
+          }
+        }
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x, ++step) {
+          const int s = step % NS;
+          const bool got = mbar_wait_bounded(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
+          if (!__all_sync(0xffffffffu, got)) {
+            fail();
+            ok = false;
+            break;
+          }
+          const uint32_t dst = stages_u32 + s * C::kTile;
+          if (tma) {
+            if (warp == 1) {
+              if (lane == 0) mbar_arrive(&full[s]);
+            } else {
+              if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)C::kTile);
+              __syncwarp();
+              // whole tiles in one copy; pages below a tile in one copy per page and half
+              const int n = p.tma_page_keys == kTcKeys ? 1 : kTcKeys / p.tma_page_keys * C::kHalves;
+              const int src_lane = n == 1 ? 0 : lane / C::kHalves;
+              const int pg = __shfl_sync(0xffffffffu, page, src_lane), ip = __shfl_sync(0xffffffffu, in_page, src_lane);
+              if (lane < n) {
+                const int half = n == 1 ? 0 : lane % C::kHalves;
+                const uint32_t at = dst + half * kCtHalf + src_lane * p.tma_page_keys * 128;
+                asm volatile(
+                    "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                    " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(at),
+                    "l"(reinterpret_cast<uint64_t>(x == 0 ? &tmK : &tmV)), "r"(0), "r"(ip), "r"(half), "r"(it.g),
+                    "r"(pg), "r"(smem_u32(&full[s]))
+                    : "memory");
+              }
+            }
+          } else {
+            const int c = lane % CH;
+#pragma unroll 4
+            for (int i = 0; i < 64 / RPI; ++i) {
+              const int r = i * RPI + lane / CH;  // of the warp's 64 rows
+              const int64_t o0 = __shfl_sync(0xffffffffu, off[0], r & 31), o1 = __shfl_sync(0xffffffffu, off[1], r & 31);
+              const int64_t so = r < 32 ? o0 : o1;
+              const int row = warp * 64 + r;
+              cp_async16(dst + (c >> 3) * kCtHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                         kv[x] + (so < 0 ? 0 : so) + c * 8, so >= 0);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<kCtLag>();
+          if ((by_copy >> (kCtLag - 1)) & 1u) hand_over(step - kCtLag);
+          by_copy = (by_copy << 1) | (tma ? 0u : 1u);
+        }
+      }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = kCtLag; i >= 1; --i)
+      if ((by_copy >> (i - 1)) & 1u) hand_over(step - i);
+    if (!ok || s_abort) {
+      // copies still in flight into this CTA
+      for (int i = 1; i <= min(step, NS); ++i) mbar_wait_bounded(&full[(step - i) % NS], ((step - i) / NS) & 1, nullptr);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ MMA issuer of block w
+    const int w = warp - 2;
+    if (lane == 0) {
+      const uint32_t qa = qs_u32 + w * C::kTile, sd = tmem + ct_col_s(w), od = tmem + ct_col_o(w);
+      int step = 0, t = 0, part = 0;  // t: tiles of this block so far, part: pieces it had tiles of
+      bool ok = true;
+      for (int round = 0; ok && round < rounds; ++round) {
+        CtItem it;
+        if (!ct_item(p, n_items, round, it)) continue;
+        int b0, b1;
+        ct_block_units(p, it, w, b0, b1);
+        for (int u = it.u0; ok && u < it.u1; ++u) {
+          const bool in = u >= b0 && u < b1;
+          // K: S = Q K^T (behind P V of the tile before, whose P it overwrites)
+          {
+            const int s = step % NS;
+            if (in && u == b0 && !mbar_wait_bounded(&qfull[w], part & 1, &s_abort)) { ok = false; break; }
+            if (!mbar_wait_bounded(&full[s], (step / NS) & 1, &s_abort)) { ok = false; break; }
+            if (in) {
+              tc::fence_after();
+              const uint32_t kb = stages_u32 + s * C::kTile;
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t koff = (ks >> 2) * kCtHalf + (ks & 3) * 32;
+                tc::mma_ss(sd, tc::smem_desc(qa + koff, 16, 1024), tc::smem_desc(kb + koff, 16, 1024), C::kIdescQK,
+                           ks > 0 ? 1u : 0u);
+              }
+              tc::commit(&sfull[w]);
+              tc::commit(&empty[s]);
+            } else {
+              mbar_arrive(&empty[s]);
+            }
+            ++step;
+          }
+          // V: O += P V
+          {
+            const int s = step % NS;
+            if (!mbar_wait_bounded(&full[s], (step / NS) & 1, &s_abort)) { ok = false; break; }
+            if (in) {
+              if (u == b0 && part >= 1 && !mbar_wait_bounded(&ofree[w], (part - 1) & 1, &s_abort)) { ok = false; break; }
+              if (!mbar_wait_bounded(&pfull[w], t & 1, &s_abort)) { ok = false; break; }
+              tc::fence_after();
+              const uint32_t vb = stages_u32 + s * C::kTile;
+#pragma unroll
+              for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                tc::mma_ts(od, sd + ks * 8, tc::smem_desc(vb + ks * 2048, kCtHalf, 1024), C::kIdescPV,
+                           (ks > 0 || u > b0) ? 1u : 0u);
+              tc::commit(&pvdone[w]);
+              tc::commit(&empty[s]);
+              ++t;
+            } else {
+              mbar_arrive(&empty[s]);
+            }
+            ++step;
+          }
+        }
+        if (b1 > b0) ++part;
+      }
+      if (!ok) {
+        fail();
+        tc::commit(&drain[w]);  // every MMA issued so far has finished before TMEM is released
+        mbar_wait_bounded(&drain[w], 0, nullptr);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warpgroups
+    const int w = (warp - 4) >> 2;
+    const int sub = warp & 3;        // TMEM sub-partition of this warp
+    const int m = sub * 32 + lane;   // TMEM lane = row of the block
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+    const uint32_t sbuf = tl + ct_col_s(w), obuf = tl + ct_col_o(w);
+    uint8_t* qblock = qs + w * C::kTile;
+    const float sc = p.scale_log2;
+
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool got = mbar_wait_bounded(bar, parity, &s_abort);
+      return __all_sync(0xffffffffu, got);
+    };
+    // the next piece in which this block has tiles, its rows into shared memory (K-major, 128-byte
+    // swizzle; zeros for padding rows); pieces without tiles leave an empty record
+    CtItem it;
+    int b0 = 0, b1 = 0, round = 0;
+    auto next_piece = [&](CtItem& n, int& nb0, int& nb1) -> bool {
+      for (; round < rounds; ++round) {
+        if (!ct_item(p, n_items, round, n)) continue;
+        ct_block_units(p, n, w, nb0, nb1);
+        if (nb1 > nb0) {
+          ++round;
+          return true;
+        }
+        if (n.slot >= 0)
+          p.part_ml[((int64_t)n.slot * p.Hkv + n.g) * kTcRows + w * 128 + m] = make_float2(neg_inf(), 0.f);
+      }
+      return false;
+    };
+    auto load_q = [&](const CtItem& n) {
+      const int r = n.row0 + w * 128 + m;
+      const bool real = r < n.s.n * p.G;
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                        (real ? q_offset(p, n.s, n.g, r) : 0));
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h) {
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = real ? __ldg(src + h * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(qblock + h * kCtHalf + m * 128 + ((c ^ (m & 7)) << 4)) = v[c];
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[w]);
+    };
+
+    bool have = next_piece(it, b0, b1), ok = true;
+    if (have) load_q(it);
+    int t = 0;
+    while (have && ok) {
+      CtItem nx;
+      int nb0 = 0, nb1 = 0;
+      const bool have_next = next_piece(nx, nb0, nb1);
+      const int r = it.row0 + w * 128 + m;
+      const bool real = r < it.s.n * p.G;
+      // position of the row's token; padding rows see what the last row sees
+      const int pos = it.s.len - it.s.n + (real ? r / p.G : it.s.n - 1);
+      const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      float m_run = neg_inf(), l = 0.f;
+      for (int u = b0; u < b1; ++u, ++t) {
+        if (!warp_wait(&sfull[w], t & 1)) { ok = false; break; }
+        tc::fence_after();
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tc::ld32(sbuf, s0);
+        tc::ld32(sbuf + 32, s1);
+        tc::ld32(sbuf + 64, s2);
+        tc::ld32(sbuf + 96, s3);
+        const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
+        const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
+        tc::ld_wait(s0);
+        tc::ld_wait(s1);
+        tc::ld_wait(s2);
+        tc::ld_wait(s3);
+        if (edge) {
+          auto hide = [&](uint32_t(&v)[32], int c0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e > hi || c0 + e < lo) v[e] = 0xff800000u;
+          };
+          hide(s0, 0);
+          hide(s1, 32);
+          hide(s2, 64);
+          hide(s3, 96);
+        }
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          mx[0] = fmax3(mx[0], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+          mx[1] = fmax3(mx[1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+          mx[2] = fmax3(mx[2], __uint_as_float(s2[e]), __uint_as_float(s2[e + 1]));
+          mx[3] = fmax3(mx[3], __uint_as_float(s3[e]), __uint_as_float(s3[e + 1]));
+        }
+        const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float tmax = raw_max == neg_inf() ? raw_max : raw_max * sc;
+        // ---- reference maximum: the first tile's, moved when a tile exceeds it by more than 2^8
+        if (u == b0) {
+          m_run = tmax;
+        } else {
+          const bool need = tmax > m_run + kCtRescaleLog2 || (m_run == neg_inf() && tmax > neg_inf());
+          if (__any_sync(0xffffffffu, need)) {
+            // O may be touched once the P V before has completed
+            if (!warp_wait(&pvdone[w], (t - 1) & 1)) { ok = false; break; }
+            tc::fence_after();
+            float alpha = 1.f;
+            if (need) {
+              alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - tmax);
+              l *= alpha;
+              m_run = tmax;
+            }
+            uint32_t v[32];
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tc::ld32(obuf + c * 32, v);
+              tc::ld_wait(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tc::st32(obuf + c * 32, v);
+            }
+            tc::st_wait();
+          }
+        }
+        // ---- P = 2^(s * scale - mu) as bf16 pairs over S's first 64 columns
+        const float mu = m_run == neg_inf() ? 0.f : m_run;
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
+        auto chunk = [&](const uint32_t(&v)[32], int c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), sc, -mu, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            add2(sums[(e >> 1) & 1], sums[2 + ((e >> 1) & 1)], p0, p1);
+            pk[e / 2] = pack_bf16(p0, p1);
+          }
+          __syncwarp();
+          tc::st16(sbuf + c * 16, pk);
+        };
+        chunk(s0, 0);
+        chunk(s1, 1);
+        chunk(s2, 2);
+        chunk(s3, 3);
+        tc::st_wait();
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[w]);
+      }
+      if (!ok) break;
+      if (have_next) load_q(nx);  // the piece's last Q K^T has read its rows
+      // ---- epilogue, once the piece's last P V is done
+      if (!warp_wait(&pvdone[w], (t - 1) & 1)) { ok = false; break; }
+      tc::fence_after();
+      if (it.slot >= 0) {
+        const int64_t rec = (int64_t)it.slot * p.Hkv + it.g;
+        float* dst = p.part_o + rec * D * kTcRows + w * 128 + m;
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          __syncwarp();
+          tc::ld32(obuf + c * 32, v);
+          tc::ld_wait(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) dst[(c * 32 + e) * kTcRows] = __uint_as_float(v[e]);
+        }
+        p.part_ml[rec * kTcRows + w * 128 + m] = make_float2(m_run, l);
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t off = real ? o_offset(p, it.s, it.g, r) : 0;
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          __syncwarp();
+          tc::ld32(obuf + c * 32, v);
+          tc::ld_wait(v);
+          if (real) {
+            if (p.o_bf16) {
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off + c * 32;
+              if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  uint4 x;
+                  x.x = pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+                  x.y = pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+                  x.z = pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+                  x.w = pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+                  *reinterpret_cast<uint4*>(dst + e) = x;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) dst[e] = __float2bfloat16_rn(__uint_as_float(v[e]) * inv);
+              }
+            } else {
+              float* dst = reinterpret_cast<float*>(p.o) + off + c * 32;
+              if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(dst + e) =
+                      make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
+                                  __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) dst[e] = __uint_as_float(v[e]) * inv;
+              }
+            }
+          }
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ofree[w]);
+      have = have_next;
+      it = nx;
+      b0 = nb0;
+      b1 = nb1;
+    }
+    if (!ok) fail();
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    __syncwarp();
+    tc::fence_after();
+    tc::dealloc(tmem, kCtTmemCols);
+  }
+}
+
+template <int D>
+static cudaError_t launch_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                             cudaStream_t stream) {
+  auto kern = chunk_attn_tc<D>;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)Ct<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(p.grid), dim3(kCtThreads), Ct<D>::kSmem, stream, 0u, *tmK, *tmV, p);
+}
+
+cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                            cudaStream_t stream) {
+  return p.D == 128 ? launch_tc<128>(p, tmK, tmV, stream) : launch_tc<64>(p, tmK, tmV, stream);
+}
+
+}  // namespace specv

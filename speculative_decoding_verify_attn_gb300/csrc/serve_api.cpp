@@ -8,6 +8,7 @@
 
 #include "serve_internal.h"
 #include "spec_serve.h"
+#include "tensor_map.h"
 
 namespace {
 
@@ -63,7 +64,7 @@ int serve_grid() {
 bool use_mma(int kv_dtype, int max_q, int G) {
   return kv_dtype == SPEC_BF16 && (int64_t)max_q * G <= specv::kMmaMaxRows;
 }
-int chunk_row_tile(int kv_dtype) { (void)kv_dtype; return specv::kF32Rows; }
+int chunk_row_tile(int kv_dtype) { return kv_dtype == SPEC_BF16 ? specv::kTcRows : specv::kF32Rows; }
 
 ServeAttnParams base_params(const Shape& s, float scale) {
   ServeAttnParams p;
@@ -75,14 +76,43 @@ ServeAttnParams base_params(const Shape& s, float scale) {
   return p;
 }
 
+// K or V as (column in half, token, half of D, kv head, page): one box is a page's rows, or a tile's
+// 128 where pages are larger; packed rows are one page.  False where the layout does not suit a map.
+bool encode_kv(CUtensorMap* m, const void* base, const ServeAttnParams& p) {
+  specv::EncodeTiledFn fn = specv::encode_fn();
+  if (!fn) return false;
+  const int64_t tokens = p.paged ? p.page_size : p.T, pages = p.paged ? p.num_pages : 1;
+  const int64_t sp = p.paged ? p.kv_sp : p.kv_st * p.T;
+  cuuint64_t dims[5] = {64, (cuuint64_t)tokens, (cuuint64_t)p.D / 64, (cuuint64_t)p.Hkv, (cuuint64_t)pages};
+  cuuint64_t strides[4] = {(cuuint64_t)p.kv_st * 2, 128, (cuuint64_t)p.kv_sh * 2, (cuuint64_t)sp * 2};
+  for (cuuint64_t s : strides)
+    if (s == 0 || s >= ((cuuint64_t)1 << 40)) return false;
+  const bool whole = p.tma_page_keys == specv::kTcKeys;
+  cuuint32_t box[5] = {64, (cuuint32_t)p.tma_page_keys, whole ? (cuuint32_t)p.D / 64 : 1u, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream) {
-  const int bf16 = kv_dtype == SPEC_BF16;
+  const bool bf16 = kv_dtype == SPEC_BF16;
   p.row_tile = chunk_row_tile(kv_dtype);
-  p.unit_keys = specv::kF32Keys;
+  p.unit_keys = bf16 ? specv::kTcKeys : specv::kF32Keys;
   specv::chunk_workspace_carve(ws, &p);
+  CUtensorMap tm[2];
+  if (bf16) {
+    memset(tm, 0, sizeof(tm));
+    // whole tiles per copy, or pages of at least kTmaMinPage tokens that divide a tile
+    if (!p.paged || p.page_size % specv::kTcKeys == 0) p.tma_page_keys = specv::kTcKeys;
+    else if (specv::kTcKeys % p.page_size == 0 && p.page_size >= specv::kTmaMinPage) p.tma_page_keys = p.page_size;
+    // a copy of a packed tile is never issued where T < kTcKeys
+    p.use_tma = p.tma_page_keys > 0 && encode_kv(&tm[0], p.k, p) && encode_kv(&tm[1], p.v, p);
+  }
   if (specv::launch_chunk_plan(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
   if (p.k_new && specv::launch_chunk_append(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (specv::launch_chunk_f32(p, bf16, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  const cudaError_t e = bf16 ? specv::launch_chunk_tc(p, &tm[0], &tm[1], stream) : specv::launch_chunk_f32(p, stream);
+  if (e != cudaSuccess) return SPEC_ERR_CUDA;
   return specv::launch_chunk_merge(p, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

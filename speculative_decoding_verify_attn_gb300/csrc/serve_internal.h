@@ -19,6 +19,7 @@ constexpr int kMmaUnit = 128;   // keys per unit of work of the mma.sync kernel 
 constexpr int kMmaDirectKeys = 4 * kMmaUnit;
 constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
 constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
+constexpr int kTmaMinPage = 64; // tokens per page from which the tcgen05 kernel copies pages by TMA
 constexpr int kF32Rows = 32;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 
@@ -84,7 +85,7 @@ cudaError_t launch_chunk_plan(const ServeAttnParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_append(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             cudaStream_t stream);
-cudaError_t launch_chunk_f32(const ServeAttnParams& p, int bf16, cudaStream_t stream);
+cudaError_t launch_chunk_f32(const ServeAttnParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ServeAttnParams& p, cudaStream_t stream);
 
 struct LogprobParams {

@@ -101,7 +101,7 @@ def test_empty_calls_launch_nothing(L):
 def test_workspace_sizes(L):
     assert L.spec_paged_attn_workspace(ctypes.byref(paged(D=96))) == 0
     assert L.spec_paged_attn_workspace(ctypes.byref(paged(T=0, max_q=1))) > 0
-    assert L.spec_prefill_attn_workspace(ctypes.byref(prefill())) > L.spec_prefill_attn_workspace(
+    assert L.spec_prefill_attn_workspace(ctypes.byref(prefill(T=100000))) > L.spec_prefill_attn_workspace(
         ctypes.byref(prefill(T=1)))
     assert L.spec_token_logprobs_workspace(ctypes.byref(logp(N=2, V=128256, K=20))) > 256
 
