@@ -72,6 +72,23 @@ __device__ __forceinline__ void fma2(float a0, float a1, float b, float c, float
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(bb), "l"(cc));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
 }
+// (a0 * b, a1 * b)
+__device__ __forceinline__ void mul2(float a0, float a1, float b, float& d0, float& d1) {
+  unsigned long long a, bb, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(bb));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+// (s0, s1) += (a0 * b0, a1 * b1)
+__device__ __forceinline__ void fma2_acc(float& s0, float& s1, float a0, float a1, float b0, float b1) {
+  unsigned long long s, a, b, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(s0), "f"(s1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(d));
+}
 // (s0, s1) += (a0, a1)
 __device__ __forceinline__ void add2(float& s0, float& s1, float a0, float a1) {
   unsigned long long s, a, d;

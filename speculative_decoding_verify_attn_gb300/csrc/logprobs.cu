@@ -9,8 +9,10 @@
 //
 // Top alternatives: an id's key is (order of its logit, lower id first) as one 64-bit number; each
 // warp keeps its K best keys sorted over its lanes.  A batch of vectors is looked at one by one only
-// if its maximum, which the softmax needs anyway, reaches the warp's K-th value or the CTA's best
-// K-th value so far (shared), so the list costs about K log(n / K) insertions per warp.
+// if its maximum, which the softmax needs anyway, reaches a floor that the CTA's warps share: the
+// least of the warps' ceil(K / 8)-th best values, at or above which K ids exist.  The first floor comes
+// from the lanes' maxima of the first batch, before anything is inserted, so a row of n ids costs
+// about K log(n / 8192) insertions in all.
 //
 // Bound: HBM, one read of the logits.  A row is one CTA when there are enough rows to fill the GPU,
 // else kSliceTarget / N slices whose records a second kernel joins (launched as a programmatic
@@ -27,6 +29,7 @@ namespace specv {
 constexpr int kLpWarps = 8;
 constexpr int kLpThreads = kLpWarps * 32;
 constexpr int kLpVecs = 4;            // 16-byte vectors per lane and batch
+constexpr int kLpCtasPerSm = 3;
 constexpr int kSliceTarget = 608;     // CTAs wanted (four per SM) before rows are no longer sliced
 constexpr int kMinSlice = 4096;       // elements of a slice at least (one fp32 batch of a CTA)
 
@@ -57,15 +60,16 @@ __device__ __forceinline__ Stat warp_stat(Stat v) {
 }
 
 typedef unsigned long long Key;
-__device__ __forceinline__ Key make_key(float x, uint32_t id) {
+__device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 as 0: equal logits compare equal
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((Key)o << 32) | (uint32_t)~id;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(Key k) {
-  const uint32_t o = (uint32_t)(k >> 32);
+__device__ __forceinline__ float order_value(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+__device__ __forceinline__ Key make_key(float x, uint32_t id) { return ((Key)order_of(x) << 32) | (uint32_t)~id; }
+__device__ __forceinline__ float key_value(Key k) { return order_value((uint32_t)(k >> 32)); }
+constexpr uint32_t kOrderNegInf = 0x007fffffu;  // order_of(-inf): no id is below it
 
 // The K best keys seen, sorted descending over the lanes of a warp (0: none yet).
 struct TopList {
@@ -77,10 +81,10 @@ struct TopList {
     if (lane >= pos) mine = lane == pos ? nk : up;
     thr = __shfl_sync(0xffffffffu, mine, K - 1);
   }
-  // all lanes offer one key each (0: none); those above `floor` and the K-th enter
-  __device__ __forceinline__ void offer(Key k, Key floor, int K) {
+  // all lanes offer one key each (0: none); those above the K-th enter
+  __device__ __forceinline__ void offer(Key k, int K) {
     for (;;) {
-      const unsigned hit = __ballot_sync(0xffffffffu, k > thr && k > floor);
+      const unsigned hit = __ballot_sync(0xffffffffu, k > thr);
       if (!hit) return;
       const int src = __ffs(hit) - 1;
       insert(__shfl_sync(0xffffffffu, k, src), K);
@@ -97,6 +101,12 @@ struct Vec {
     const uint32_t w = BF16 ? (&v.x)[e >> 1] : (&v.x)[e];
     if (!BF16) return __uint_as_float(w);
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+  __device__ __forceinline__ float max() const {
+    if (!BF16) return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
 template <bool BF16>
@@ -134,12 +144,13 @@ __device__ __forceinline__ float given_logit(const LogprobParams& p, const void*
 }
 
 template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_stats(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_stats(const __grid_constant__ LogprobParams p) {
   pdl_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) status_clear_for_launch(p.status);
   __shared__ Key s_keys[kLpWarps][32];
   __shared__ Stat s_stat[kLpWarps];
-  __shared__ Key s_floor;  // the best K-th key of the CTA's warps: lower keys are not among the K best
+  __shared__ uint32_t s_rank[kLpWarps];  // order of each warp's ceil(K / 8)-th best value (or below it)
+  __shared__ uint32_t s_floor;
   constexpr int VN = Vec<BF16>::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
@@ -150,15 +161,14 @@ __global__ void __launch_bounds__(kLpThreads) logprob_stats(const __grid_constan
   const uint4* body = reinterpret_cast<const uint4*>(row_ptr + (int64_t)head * (BF16 ? 2 : 4));
   const int per = (nvec + p.slices - 1) / p.slices;
   const int v0 = min(nvec, slice * per), v1 = min(nvec, v0 + per);
-  if (TOP && threadIdx.x == 0) s_floor = 0;
-  if (TOP) __syncthreads();
+  const int rank = (p.K + kLpWarps - 1) / kLpWarps;
 
   Stat st{neg_inf(), 0.f, 0.f};
   TopList top;
   auto single = [&](int i, bool in) {  // one element per lane, outside the vectors
     const float x = in ? load_elem<BF16>(row_ptr, i) : neg_inf();
     if (in) st = stat_join(st, Stat{x, x == neg_inf() ? 0.f : 1.f, 0.f});
-    if (TOP) top.offer(in ? make_key(x, (uint32_t)i) : 0, 0, p.K);
+    if (TOP) top.offer(in ? make_key(x, (uint32_t)i) : 0, p.K);
   };
   // a warp meets its ids in ascending order (the head here, the tail at the end)
   if (slice == 0 && warp == 0 && head > 0) single(lane, lane < head);
@@ -174,17 +184,30 @@ __global__ void __launch_bounds__(kLpThreads) logprob_stats(const __grid_constan
     }
   };
   int base = v0 + warp * 32 * kLpVecs;
-  if (base < v1) fetch(cur, base);
-  for (; base < v1; base += kStep) {
-    if (base + kStep < v1) fetch(nxt, base + kStep);
-    float vm[kLpVecs], bm = neg_inf();
+  fetch(cur, base);
+  if (TOP) {
+    // the first floor: the least of the warps' rank-th largest lane maxima
+    float x = cur[0].max();
 #pragma unroll
-    for (int u = 0; u < kLpVecs; ++u) {
-      vm[u] = cur[u].get(0);
-#pragma unroll
-      for (int e = 1; e < VN; ++e) vm[u] = fmaxf(vm[u], cur[u].get(e));
-      bm = fmaxf(bm, vm[u]);
+    for (int u = 1; u < kLpVecs; ++u) x = fmaxf(x, cur[u].max());
+    uint32_t o = order_of(x), best = kOrderNegInf;
+    for (int i = 0; i < rank; ++i) {
+      best = __reduce_max_sync(0xffffffffu, o);
+      const unsigned who = __ballot_sync(0xffffffffu, o == best);
+      if (lane == __ffs(who) - 1) o = 0;
     }
+    best = max(best, kOrderNegInf);
+    if (lane == 0) s_rank[warp] = best;
+    __syncthreads();
+    const uint32_t f = __reduce_min_sync(0xffffffffu, s_rank[lane % kLpWarps]);
+    if (threadIdx.x == 0) s_floor = f;
+    __syncthreads();
+  }
+  for (; base < v1; base += kStep) {
+    fetch(nxt, base + kStep);
+    float bm = cur[0].max();
+#pragma unroll
+    for (int u = 1; u < kLpVecs; ++u) bm = fmaxf(bm, cur[u].max());
     if (bm > st.m) {
       const float d = fmaxf(st.m - bm, -256.f);
       const float a = ex2_approx(d * kLog2e);
@@ -192,35 +215,58 @@ __global__ void __launch_bounds__(kLpThreads) logprob_stats(const __grid_constan
       st.s *= a;
       st.m = bm;
     }
-    const float ref = st.m == neg_inf() ? 0.f : st.m;
-    float s2[2] = {0.f, 0.f}, w2[2] = {0.f, 0.f};
+    const float nref = st.m == neg_inf() ? 0.f : -st.m;
+    float s0 = 0.f, s1 = 0.f, w0 = 0.f, w1 = 0.f;
 #pragma unroll
     for (int u = 0; u < kLpVecs; ++u)
 #pragma unroll
-      for (int e = 0; e < VN; ++e) {
-        const float d = fmaxf(cur[u].get(e) - ref, -256.f);  // -inf: e^-256 is 0 in fp32
-        const float x = ex2_approx(d * kLog2e);
-        s2[e & 1] += x;
-        w2[e & 1] = fmaf(d, x, w2[e & 1]);
+      for (int i = 0; i < VN / 2; ++i) {
+        float d0 = cur[u].get(2 * i), d1 = cur[u].get(2 * i + 1), t0, t1;
+        add2(d0, d1, nref, nref);
+        d0 = fmaxf(d0, -256.f);  // -inf, and differences past fp32: e^-256 is 0 in fp32
+        d1 = fmaxf(d1, -256.f);
+        mul2(d0, d1, kLog2e, t0, t1);
+        const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+        add2(s0, s1, e0, e1);
+        fma2_acc(w0, w1, d0, d1, e0, e1);
       }
-    st.s += s2[0] + s2[1];
-    st.w += w2[0] + w2[1];
+    st.s += s0 + s1;
+    st.w += w0 + w1;
     if (TOP) {
-      const Key floor = *reinterpret_cast<volatile Key*>(&s_floor);
-      // within the warp later ids lose ties, so the K-th value must be exceeded; against the other
-      // warps' floor a tie may still win
-      const bool full = top.thr != 0;
-      const float tf = key_value(top.thr), ff = floor ? key_value(floor) : neg_inf();
-      if (__any_sync(0xffffffffu, (!full || bm > tf) && bm >= ff)) {
+      // a value counts from the floor on; within the warp, where later ids lose ties, from above the
+      // K-th value on
+      const uint32_t lim = max(*reinterpret_cast<volatile uint32_t*>(&s_floor), top.thr ? (uint32_t)(top.thr >> 32) + 1u : 0u);
+      const float lf = order_value(lim);
+      if (__any_sync(0xffffffffu, bm >= lf)) {
+        uint32_t todo = 0;  // bit u * VN + e: element e of vector u of this lane
 #pragma unroll
-        for (int u = 0; u < kLpVecs; ++u) {
-          const int i = base + u * 32 + lane;
-          if (!__any_sync(0xffffffffu, (top.thr == 0 || vm[u] >= key_value(top.thr)) && vm[u] >= ff)) continue;
+        for (int u = 0; u < kLpVecs; ++u)
 #pragma unroll
-          for (int e = 0; e < VN; ++e)
-            top.offer(i < v1 ? make_key(cur[u].get(e), (uint32_t)(head + i * VN + e)) : 0, floor, p.K);
+          for (int e = 0; e < VN; ++e) todo |= cur[u].get(e) >= lf ? 1u << (u * VN + e) : 0u;
+#pragma unroll
+        for (int u = 0; u < kLpVecs; ++u)
+          if (base + u * 32 + lane >= v1) todo &= ~(((1u << VN) - 1u) << (u * VN));
+        // few: read again rather than picked out of registers by a run-time index
+        while (__any_sync(0xffffffffu, todo != 0)) {
+          Key k = 0;
+          if (todo) {
+            const int j = __ffs(todo) - 1;
+            const int id = head + (base + j / VN * 32 + lane) * VN + j % VN;
+            k = make_key(load_elem<BF16>(row_ptr, id), (uint32_t)id);
+            todo &= todo - 1;
+          }
+          top.offer(k, p.K);
         }
-        if (lane == 0 && top.thr > floor) atomicMax(&s_floor, top.thr);
+        // a better floor
+        const uint32_t o = (uint32_t)(__shfl_sync(0xffffffffu, top.mine, rank - 1) >> 32);
+        const uint32_t old = *reinterpret_cast<volatile uint32_t*>(&s_rank[warp]);
+        __syncwarp();
+        if (o > old) {
+          if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&s_rank[warp]) = o;
+          __syncwarp();
+          const uint32_t f = __reduce_min_sync(0xffffffffu, reinterpret_cast<volatile uint32_t*>(s_rank)[lane % kLpWarps]);
+          if (lane == 0) atomicMax(&s_floor, f);
+        }
       }
     }
 #pragma unroll
@@ -238,7 +284,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_stats(const __grid_constan
 #pragma unroll
   for (int w = 1; w < kLpWarps; ++w) {
     st = stat_join(st, s_stat[w]);
-    if (TOP) top.offer(lane < p.K ? s_keys[w][lane] : 0, 0, p.K);
+    if (TOP) top.offer(lane < p.K ? s_keys[w][lane] : 0, p.K);
   }
   if (p.slices == 1) {
     int state;
@@ -269,7 +315,7 @@ __global__ void __launch_bounds__(32) logprob_join(const __grid_constant__ Logpr
   const int nk = p.slices * p.K;
   for (int i0 = 0; i0 < nk; i0 += 32) {
     const int i = i0 + lane;
-    top.offer(i < nk ? __ldcg(p.part_keys + (int64_t)row * nk + i) : 0, 0, p.K);
+    top.offer(i < nk ? __ldcg(p.part_keys + (int64_t)row * nk + i) : 0, p.K);
   }
   if (state < 0 && lane == 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_TOKEN);
   write_row(p, row, st, top.mine, given, state);

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   constexpr int CH = D / 8;         // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows one cp.async instruction of the warp covers
   constexpr int STAGE = mma_stage_bytes(D);
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int64_t s_scan[kMmaWarps];
   __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
   __shared__ int s_b;
@@ -177,45 +177,59 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
     const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
     page = -1;
     if (ld.left > 0 && t >= ld.s.lo && t < ld.s.len)
-      page = __ldg(p.table + (int64_t)ld.b * p.table_stride + t / p.page_size);
+      page = __ldg(p.table + (int64_t)ld.b * p.table_stride + page_of(p, t));
   };
+  // chunk c of row r at chunk c ^ (r & 7): for r = i * RPI + lane / CH the lane's part of the place
+  // is constant and i changes address bits by XOR and row offset
+  const int c = lane % CH, rl = lane / CH;
+  const uint32_t lane_at = rl * (D * 2) + ((c ^ rl) << 4);
   auto issue = [&](int stage) {
     if (ld.left > 0) {
-      const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
-      const bool in = t >= ld.s.lo && t < ld.s.len;
-      const bool good = in && page >= 0 && page < p.num_pages;
-      const int64_t slot = good ? (int64_t)page * p.kv_sp + (int64_t)(t % p.page_size) * p.kv_st + (int64_t)ld.g * p.kv_sh : 0;
+      const int t0 = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16;
       const int first_new = ld.s.len - ld.s.n;
-      const bool fresh = knew != nullptr && in && t >= first_new;
-      const int64_t src = fresh ? (int64_t)(ld.s.q0 + t - first_new) * p.new_st + (int64_t)ld.g * p.new_sh : slot;
-      const int kind = fresh ? 2 : (good ? 1 : 0);
-      if (__any_sync(0xffffffffu, in && !good)) {
-        if (in && !good) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
-      }
-      const bool any_new = __any_sync(0xffffffffu, fresh);
       const uint32_t dst = ring_u32 + stage * STAGE;
-      const int c = lane % CH;
+      const int64_t head = (int64_t)ld.g * p.kv_sh;
+      // the usual case: 16 cached tokens of one page
+      if ((p.page_size & 15) == 0 && t0 >= ld.s.lo && t0 + 16 <= (knew ? first_new : ld.s.len) && page >= 0 &&
+          page < p.num_pages) {
+        const int64_t off = (int64_t)page * p.kv_sp + (int64_t)(t0 - page_of(p, t0) * p.page_size + rl) * p.kv_st + head + c * 8;
+        const __nv_bfloat16 *ks = kb + off, *vs = vb + off;
+        const int64_t step = p.kv_st * RPI;
 #pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = i * RPI + lane / CH;
-        const int64_t so = __shfl_sync(0xffffffffu, src, r);
-        const int sk = __shfl_sync(0xffffffffu, kind, r);
-        const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
-        cp_async16(at, (sk == 2 ? knew : kb) + so + c * 8, sk != 0);
-        cp_async16(at + 16 * D * 2, (sk == 2 ? vnew : vb) + so + c * 8, sk != 0);
-      }
-      if (any_new) {  // store the new rows into their slots
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const uint32_t at = dst + ((lane_at + i * RPI * (D * 2)) ^ (((i * RPI) & 7) << 4));
+          cp_async16(at, ks);
+          cp_async16(at + 16 * D * 2, vs);
+          ks += step;
+          vs += step;
+        }
+      } else {
+        const int t = t0 + (lane & 15);
+        const bool in = t >= ld.s.lo && t < ld.s.len;
+        const bool good = in && page >= 0 && page < p.num_pages;
+        const int64_t slot = good ? (int64_t)page * p.kv_sp + (int64_t)(t - page_of(p, t) * p.page_size) * p.kv_st + head : 0;
+        const bool fresh = knew != nullptr && in && t >= first_new;
+        const int64_t src = fresh ? (int64_t)(ld.s.q0 + t - first_new) * p.new_st + (int64_t)ld.g * p.new_sh : slot;
+        const int kind = fresh ? 2 : (good ? 1 : 0);
+        if (in && !good) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+        __syncwarp();
+        const bool any_new = __any_sync(0xffffffffu, fresh);
 #pragma unroll 1
         for (int i = 0; i < 16 / RPI; ++i) {
-          const int r = i * RPI + lane / CH;
+          const int r = i * RPI + rl;
           const int64_t so = __shfl_sync(0xffffffffu, src, r);
-          const int64_t to = __shfl_sync(0xffffffffu, slot, r);
-          const bool st = __shfl_sync(0xffffffffu, (int)(fresh && good), r) != 0;
-          if (st) {
-            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.k) + to + c * 8) =
-                __ldg(reinterpret_cast<const uint4*>(knew + so + c * 8));
-            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.v) + to + c * 8) =
-                __ldg(reinterpret_cast<const uint4*>(vnew + so + c * 8));
+          const int sk = __shfl_sync(0xffffffffu, kind, r);
+          const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
+          cp_async16(at, (sk == 2 ? knew : kb) + so + c * 8, sk != 0);
+          cp_async16(at + 16 * D * 2, (sk == 2 ? vnew : vb) + so + c * 8, sk != 0);
+          if (any_new) {  // store the new rows into their slots
+            const int64_t to = __shfl_sync(0xffffffffu, slot, r);
+            if (__shfl_sync(0xffffffffu, (int)(fresh && good), r)) {
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.k) + to + c * 8) =
+                  __ldg(reinterpret_cast<const uint4*>(knew + so + c * 8));
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.v) + to + c * 8) =
+                  __ldg(reinterpret_cast<const uint4*>(vnew + so + c * 8));
+            }
           }
         }
       }
@@ -231,6 +245,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   // ---- compute
   const int gid = lane >> 2, tq = lane & 3;
   const float sc = p.scale_log2;
+  // places of the fragments' rows in a stage (its K, then its V): chunk x of the row is reached by
+  // XOR with x << 4
+  const uint32_t k_at = ((lane & 7) + ((lane >> 4) << 3)) * (D * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+  const uint32_t v_at = 16 * D * 2 + (lane & 15) * (D * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
   uint32_t qf[MT][KS][4];
   float o[MT][NT][4];
   float m_run[MT][2], l_run[MT][2];
@@ -268,7 +286,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
     issue(stage == 0 ? 2 : stage - 1);  // two units ahead
     cp_async_wait<2>();
     __syncwarp();
-    const uint32_t ks_u32 = ring_u32 + stage * STAGE, vs_u32 = ks_u32 + 16 * D * 2;
+    const uint32_t ks_u32 = ring_u32 + stage * STAGE;
     const int key0 = (cw.s.lo & ~15) + cw.u * kMmaUnit + warp * 16;
 
     float s[MT][2][4];
@@ -279,11 +297,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
     {
-      const int r = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t b0, b1, b2, b3;
-        ldmatrix_x4(ks_u32 + r * (D * 2) + (((ks * 2 + hc) ^ (r & 7)) << 4), b0, b1, b2, b3);
+        ldmatrix_x4((ks_u32 + k_at) ^ (ks << 5), b0, b1, b2, b3);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           mma_bf16_16816(s[mt][0], qf[mt][ks], b0, b1);
@@ -301,22 +318,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
       float mx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int pos = first_new + (mt * 16 + gid + h * 8) / p.G;
+        if (edge) {
+          const int pos = first_new + (mt * 16 + gid + h * 8) / p.G;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[mt][nt][h * 2 + e] * sc;
-            if (edge) {
+            for (int e = 0; e < 2; ++e) {
               const int t = key0 + nt * 8 + tq * 2 + e;
               const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
-              x = vis ? x : neg_inf();
+              if (!vis) s[mt][nt][h * 2 + e] = neg_inf();
             }
-            s[mt][nt][h * 2 + e] = x;
-          }
+        }
         mx[h] = fmaxf(fmaxf(s[mt][0][h * 2], s[mt][0][h * 2 + 1]), fmaxf(s[mt][1][h * 2], s[mt][1][h * 2 + 1]));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        if (mx[h] != neg_inf()) mx[h] *= sc;  // scaled log2 units (sc > 0)
       }
       if (__any_sync(0xffffffffu, mx[0] > m_run[mt][0] || mx[1] > m_run[mt][1])) {
         float a[2];
@@ -337,21 +353,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float ref = m_run[mt][h] == neg_inf() ? 0.f : m_run[mt][h];
+        const float nref = m_run[mt][h] == neg_inf() ? 0.f : -m_run[mt][h];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          const float p0 = ex2_approx(s[mt][nt][h * 2] - ref), p1 = ex2_approx(s[mt][nt][h * 2 + 1] - ref);
+          const float p0 = ex2_approx(fmaf(s[mt][nt][h * 2], sc, nref));
+          const float p1 = ex2_approx(fmaf(s[mt][nt][h * 2 + 1], sc, nref));
           l_run[mt][h] += p0 + p1;
           pf[mt][nt * 2 + h] = pack_bf16(p0, p1);
         }
       }
     }
     {
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hc = lane >> 4;
 #pragma unroll
       for (int nn = 0; nn < NT / 2; ++nn) {
         uint32_t b0, b1, b2, b3;
-        ldmatrix_x4_trans(vs_u32 + r * (D * 2) + (((nn * 2 + hc) ^ (r & 7)) << 4), b0, b1, b2, b3);
+        ldmatrix_x4_trans((ks_u32 + v_at) ^ (nn << 5), b0, b1, b2, b3);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           mma_bf16_16816(o[mt][nn * 2], pf[mt], b0, b1);

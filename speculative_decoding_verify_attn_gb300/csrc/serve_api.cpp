@@ -168,6 +168,9 @@ int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
   ServeAttnParams p = base_params(s, a->scale);
   p.paged = 1;
   p.page_size = a->page_size; p.num_pages = a->num_pages; p.table_cols = a->table_cols;
+  p.page_shift = -1;
+  for (int i = 0; i <= 16; ++i)
+    if (a->page_size == 1 << i) p.page_shift = i;
   p.table = a->page_table; p.table_stride = a->table_stride;
   p.q_start = a->q_start; p.kv_len = a->kv_len;
   p.q = a->q; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;

@@ -43,18 +43,25 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ int page_of(const ServeAttnParams& p, int t) {
+  return p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+}
 // Element offset of token t's row of kv head g, or -1 for a page id out of range.
 __device__ __forceinline__ int64_t key_offset(const ServeAttnParams& p, const SeqInfo& s, int b, int g, int t) {
   if (!p.paged) return (int64_t)(s.q0 + t) * p.kv_st + (int64_t)g * p.kv_sh;
-  const int page = __ldg(p.table + (int64_t)b * p.table_stride + t / p.page_size);
+  const int col = page_of(p, t);
+  const int page = __ldg(p.table + (int64_t)b * p.table_stride + col);
   if (page < 0 || page >= p.num_pages) return -1;
-  return (int64_t)page * p.kv_sp + (int64_t)(t % p.page_size) * p.kv_st + (int64_t)g * p.kv_sh;
+  return (int64_t)page * p.kv_sp + (int64_t)(t - col * p.page_size) * p.kv_st + (int64_t)g * p.kv_sh;
 }
 
 // Element offset of chunk row r (token r / G of the chunk, head r % G of kv head g's group).

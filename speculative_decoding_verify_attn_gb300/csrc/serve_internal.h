@@ -41,6 +41,7 @@ struct ChunkPlan {
 struct ServeAttnParams {
   int B, Hq, Hkv, G, D, T, max_q, window;
   int paged, page_size, num_pages, table_cols;
+  int page_shift;         // log2(page_size), or -1
   const int32_t* table;
   int64_t table_stride;
   const int32_t* q_start;

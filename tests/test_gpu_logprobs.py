@@ -212,3 +212,24 @@ def test_a_serving_round(sv):
     assert float((lp.double() - got)[emitted].abs().max()) < 1e-5
     assert bool((ids.view(B, n)[out >= 0] == out[out >= 0]).all())  # greedy tokens are the top alternatives
     assert float((top[:, 0].double() - want.max(-1).values).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masks_of_the_lowest_value(sv, dtype):
+    """Ids masked by the type's lowest finite value take no part; a row of nothing else is uniform."""
+    torch = torch_mod()
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    low = torch.finfo(t).min
+    V = 9001
+    x = (torch.randn(3, V, generator=torch.Generator().manual_seed(1)) * 3).to(t)
+    x[:2, 100:] = low
+    x[1, :100] = low
+    ref = x.clone()
+    ref[0, 100:] = -float("inf")
+    tok = torch.tensor([5, 6, 7], dtype=torch.int32, device="cuda")
+    got, want = run(sv, x.cuda(), tok, 32), run(sv, ref.cuda(), tok, 32)
+    for a, b in zip(got[:4], want[:4]):
+        assert bool((a[0] == b[0]).all()) and bool((a[2] == b[2]).all())
+    # log V by a fp32 sum of V ones and logf: half an ulp of log V, twice
+    assert abs(float(got[0][1]) + np.log(V)) < 2e-6 and abs(float(got[1][1]) - np.log(V)) < 2e-6
+    assert got[2][1].tolist() == list(range(32))
