@@ -5,7 +5,7 @@
 // into units of 128 keys, laid end to end over all (sequence, kv head) segments; CTA c takes units
 // [c * per, (c + 1) * per), so ragged lengths balance.  A warp owns 16 keys of every unit and runs
 // its own pipeline: a private 3-stage ring filled by its own cp.async (16-byte chunks at
-// XOR-swizzled places, zeros for slots outside [lo, len)), mma.sync m16n8k16 for Q K^T and P V, and
+// XOR-swizzled places, zeros for slots outside [lo, len)), mma.sync m16n8k16 for K Q^T and V^T P^T, and
 // its own running (m, l, O), so no barrier of any kind stands between a warp and its data; the page
 // ids of a unit are looked up one unit ahead.  About 128 KB per SM stay in flight.  The eight warps'
 // states are joined through shared memory when a segment's part ends.  A part that is the whole
@@ -29,10 +29,11 @@ namespace specv {
 constexpr int kMmaWarps = 8;
 constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaStages = 3;
-constexpr int kMmaCmbStride = 40;  // floats per row of the 32-column join buffer (conflict-free)
+constexpr int kMmaCmbStride = 68;  // floats per row of the 64-column join buffer (conflict-free)
+constexpr float kMmaRescaleLog2 = 8.0f;
 
 __host__ __device__ constexpr int mma_stage_bytes(int D) { return 16 * D * 2 * 2; }  // a warp's K and V
-constexpr int kMmaCmbBytes = kMmaWarps * 16 * kMmaCmbStride * 4;
+constexpr int kMmaCmbBytes = kMmaWarps * 8 * kMmaCmbStride * 4;
 __host__ __device__ constexpr size_t mma_smem_bytes(int D) {
   return (size_t)kMmaWarps * kMmaStages * mma_stage_bytes(D) + kMmaCmbBytes;
 }
@@ -78,11 +79,10 @@ struct MmaWalk {
   }
 };
 
-template <int D, int MT>
+template <int D, int NR>
 __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constant__ ServeAttnParams p) {
   pdl_launch_dependents();
-  constexpr int KS = D / 16;        // k steps of Q K^T
-  constexpr int NT = D / 8;         // n tiles of P V
+  constexpr int KS = D / 16;        // k steps of K Q^T, m tiles of V^T P^T
   constexpr int CH = D / 8;         // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows one cp.async instruction of the warp covers
   constexpr int STAGE = mma_stage_bytes(D);
@@ -247,11 +247,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   const float sc = p.scale_log2;
   // places of the fragments' rows in a stage (its K, then its V): chunk x of the row is reached by
   // XOR with x << 4
-  const uint32_t k_at = ((lane & 7) + ((lane >> 4) << 3)) * (D * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-  const uint32_t v_at = 16 * D * 2 + (lane & 15) * (D * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
-  uint32_t qf[MT][KS][4];
-  float o[MT][NT][4];
-  float m_run[MT][2], l_run[MT][2];
+  const uint32_t k_at = (lane & 15) * (D * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+  const uint32_t v_at = 16 * D * 2 + ((lane & 7) + ((lane >> 4) << 3)) * (D * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+  uint32_t qf[NR][KS][2];
+  float o[NR][KS][4];  // columns d = ks * 16 + gid (+ 8) of rows nr * 8 + 2 tq (+ 1)
+  float m_run[NR][2], l_run[NR][2];
   int stage = 0;
   bool fresh_part = true;
   bool starts_at_begin = true;  // the current part starts where the CTA's range starts
@@ -262,25 +262,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
       fresh_part = false;
       part_u0 = cw.u;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = nr * 8 + gid;
+        const bool real = r < rows;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                                (real ? q_offset(p, cw.s, cw.g, r) : 0));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + gid + h * 8;
-          const bool real = r < rows;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                                  (real ? q_offset(p, cw.s, cw.g, r) : 0));
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[nr][ks][0] = real ? __ldg(src + ks * 8 + tq) : 0u;
+          qf[nr][ks][1] = real ? __ldg(src + ks * 8 + 4 + tq) : 0u;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qf[mt][ks][h] = real ? __ldg(src + ks * 8 + tq) : 0u;
-            qf[mt][ks][2 + h] = real ? __ldg(src + ks * 8 + 4 + tq) : 0u;
-          }
-          m_run[mt][h] = neg_inf();
-          l_run[mt][h] = 0.f;
+          for (int e = 0; e < 4; ++e) o[nr][ks][e] = 0.f;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          m_run[nr][h] = neg_inf();
+          l_run[nr][h] = 0.f;
+        }
       }
     }
     issue(stage == 0 ? 2 : stage - 1);  // two units ahead
@@ -289,91 +287,89 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
     const uint32_t ks_u32 = ring_u32 + stage * STAGE;
     const int key0 = (cw.s.lo & ~15) + cw.u * kMmaUnit + warp * 16;
 
-    float s[MT][2][4];
+    // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
+    // few query rows are padded to 8 instead of 16
+    float s[NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int e = 0; e < 4; ++e) s[nr][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-    {
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t a[4];
+      ldmatrix_x4((ks_u32 + k_at) ^ (ks << 5), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t b0, b1, b2, b3;
-        ldmatrix_x4((ks_u32 + k_at) ^ (ks << 5), b0, b1, b2, b3);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816(s[mt][0], qf[mt][ks], b0, b1);
-          mma_bf16_16816(s[mt][1], qf[mt][ks], b2, b3);
-        }
-      }
+      for (int nr = 0; nr < NR; ++nr) mma_bf16_16816(s[nr], a, qf[nr][ks][0], qf[nr][ks][1]);
     }
     // keys some row must not see: past the first new token, below the last row's window, or slots
     // outside [lo, len)
     const int first_new = cw.s.len - cw.s.n;
-    const bool edge = key0 + 16 > first_new || key0 < cw.s.lo || (p.window > 0 && key0 < cw.s.len - p.window);
-    uint32_t pf[MT][4];
+    if (key0 + 16 > first_new || key0 < cw.s.lo || (p.window > 0 && key0 < cw.s.len - p.window)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float mx[2];
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int pos = first_new + (nr * 8 + tq * 2 + (e & 1)) / p.G;
+          const int t = key0 + gid + (e & 2) * 4;
+          const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
+          if (!vis) s[nr][e] = neg_inf();
+        }
+    }
+    // the reference maximum moves only when a score exceeds it by more than 2^8 (P stays below 2^8,
+    // and the final division removes the reference), so most units need no exchange between lanes
+    bool over = false;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (edge) {
-          const int pos = first_new + (mt * 16 + gid + h * 8) / p.G;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = key0 + nt * 8 + tq * 2 + e;
-              const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
-              if (!vis) s[mt][nt][h * 2 + e] = neg_inf();
-            }
-        }
-        mx[h] = fmaxf(fmaxf(s[mt][0][h * 2], s[mt][0][h * 2 + 1]), fmaxf(s[mt][1][h * 2], s[mt][1][h * 2 + 1]));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        if (mx[h] != neg_inf()) mx[h] *= sc;  // scaled log2 units (sc > 0)
+        const float x = fmaxf(s[nr][h], s[nr][2 + h]);
+        over |= x != neg_inf() && x * sc > m_run[nr][h] + kMmaRescaleLog2;
       }
-      if (__any_sync(0xffffffffu, mx[0] > m_run[mt][0] || mx[1] > m_run[mt][1])) {
-        float a[2];
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float f[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(m_run[mt][h], mx[h]);
-          a[h] = m_run[mt][h] == neg_inf() ? 0.f : ex2_approx(m_run[mt][h] - mn);
-          m_run[mt][h] = mn;
-          l_run[mt][h] *= a[h];
+          float x = fmaxf(s[nr][h], s[nr][2 + h]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = x == neg_inf() ? m_run[nr][h] : fmaxf(m_run[nr][h], x * sc);
+          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - mn);
+          m_run[nr][h] = mn;
+          l_run[nr][h] *= f[h];
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[mt][nt][0] *= a[0];
-          o[mt][nt][1] *= a[0];
-          o[mt][nt][2] *= a[1];
-          o[mt][nt][3] *= a[1];
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float nref = m_run[mt][h] == neg_inf() ? 0.f : -m_run[mt][h];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const float p0 = ex2_approx(fmaf(s[mt][nt][h * 2], sc, nref));
-          const float p1 = ex2_approx(fmaf(s[mt][nt][h * 2 + 1], sc, nref));
-          l_run[mt][h] += p0 + p1;
-          pf[mt][nt * 2 + h] = pack_bf16(p0, p1);
+        for (int ks = 0; ks < KS; ++ks) {
+          o[nr][ks][0] *= f[0];
+          o[nr][ks][1] *= f[1];
+          o[nr][ks][2] *= f[0];
+          o[nr][ks][3] *= f[1];
         }
       }
     }
-    {
+    uint32_t pf[NR][2];  // P^T as the B operand: 16 keys x 8 rows
 #pragma unroll
-      for (int nn = 0; nn < NT / 2; ++nn) {
-        uint32_t b0, b1, b2, b3;
-        ldmatrix_x4_trans((ks_u32 + v_at) ^ (nn << 5), b0, b1, b2, b3);
+    for (int nr = 0; nr < NR; ++nr) {
+      float e[4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816(o[mt][nn * 2], pf[mt], b0, b1);
-          mma_bf16_16816(o[mt][nn * 2 + 1], pf[mt], b2, b3);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float m = m_run[nr][i & 1];
+        e[i] = ex2_approx(fmaf(s[nr][i], sc, m == neg_inf() ? 0.f : -m));
       }
+      l_run[nr][0] += e[0] + e[2];
+      l_run[nr][1] += e[1] + e[3];
+      pf[nr][0] = movmatrix_trans(pack_bf16(e[0], e[1]));
+      pf[nr][1] = movmatrix_trans(pack_bf16(e[2], e[3]));
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t a[4];
+      ldmatrix_x4_trans((ks_u32 + v_at) ^ (ks << 5), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) mma_bf16_16816(o[nr][ks], a, pf[nr][0], pf[nr][1]);
     }
     __syncwarp();  // every lane has read the stage before it is refilled
     stage = stage == kMmaStages - 1 ? 0 : stage + 1;
@@ -385,30 +381,31 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
       const int64_t rec = 2 * (int64_t)cta + (starts_at_begin ? 0 : 1);
       starts_at_begin = false;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float l = l_run[mt][h];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (tq == 0) s_ml[warp][mt * 16 + gid + h * 8] = make_float2(m_run[mt][h], l);
+          float l = l_run[nr][h];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (gid == 0) s_ml[warp][nr * 8 + tq * 2 + h] = make_float2(m_run[nr][h], l);
         }
       __syncthreads();
-#pragma unroll 1
-      for (int mt = 0; mt < MT; ++mt) {
-        if (mt * 16 >= rows) break;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        if (nr * 8 >= rows) break;
         float f[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + gid + h * 8;
+          const int r = nr * 8 + tq * 2 + h;
           float M = neg_inf();
 #pragma unroll
           for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
-          const float own = s_ml[warp][r].x;
-          f[h] = own == neg_inf() ? 0.f : ex2_approx(own - M);
+          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - M);
         }
-        const int row = tid >> 4, col = (tid & 15) * 2;  // 16 rows x 32 columns by 256 threads
-        const int r = mt * 16 + row;
+        // the warps' columns of 8 rows x 64 columns through shared memory; then a warp per row adds
+        // them up, two columns per lane
+        const int r = nr * 8 + warp, col = lane * 2;
         float M = neg_inf(), L = 0.f;
 #pragma unroll
         for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
@@ -418,27 +415,29 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
           L += v.x == neg_inf() ? 0.f : ex2_approx(v.x - M) * v.y;
         }
         const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-        if (!whole && r < rows && (tid & 15) == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M, L);
+        if (!whole && r < rows && lane == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M, L);
 #pragma unroll
-        for (int c4 = 0; c4 < D / 32; ++c4) {
+        for (int c4 = 0; c4 < D / 64; ++c4) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            float* dst = cmb + (warp * 16 + gid) * kMmaCmbStride + x * 8 + tq * 2;
-            const float* v = MT == 1 ? o[0][c4 * 4 + x] : (mt == 0 ? o[0][c4 * 4 + x] : o[MT - 1][c4 * 4 + x]);
-            *reinterpret_cast<float2*>(dst) = make_float2(v[0] * f[0], v[1] * f[0]);
-            *reinterpret_cast<float2*>(dst + 8 * kMmaCmbStride) = make_float2(v[2] * f[1], v[3] * f[1]);
+            float* dst = cmb + (warp * 8 + tq * 2) * kMmaCmbStride + x * 16 + gid;
+            const float* v = o[nr][c4 * 4 + x];
+            dst[0] = v[0] * f[0];
+            dst[kMmaCmbStride] = v[1] * f[1];
+            dst[8] = v[2] * f[0];
+            dst[kMmaCmbStride + 8] = v[3] * f[1];
           }
           __syncthreads();
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < kMmaWarps; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(cmb + (w * 16 + row) * kMmaCmbStride + col);
+            const float2 v = *reinterpret_cast<const float2*>(cmb + (w * 8 + warp) * kMmaCmbStride + col);
             sum.x += v.x;
             sum.y += v.y;
           }
           if (r < rows) {
             if (whole) {
-              const int64_t off = o_offset(p, cw.s, cw.g, r) + c4 * 32 + col;
+              const int64_t off = o_offset(p, cw.s, cw.g, r) + c4 * 64 + col;
               if (p.o_bf16) {
                 __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off;
                 const uint32_t v = pack_bf16(sum.x * inv, sum.y * inv);
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
                 dst[1] = sum.y * inv;
               }
             } else {
-              *reinterpret_cast<float2*>(p.part_o + (rec * kMmaMaxRows + r) * D + c4 * 32 + col) = sum;
+              *reinterpret_cast<float2*>(p.part_o + (rec * kMmaMaxRows + r) * D + c4 * 64 + col) = sum;
             }
           }
           __syncthreads();
@@ -539,10 +538,10 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p) {
   p->part_o = reinterpret_cast<float*>(b + 256 + 2 * (size_t)kServeMaxGrid * kMmaMaxRows * sizeof(float2));
 }
 
-template <int D, int MT>
+template <int D, int NR>
 static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   const size_t smem = mma_smem_bytes(D);
-  auto kern = paged_mma<D, MT>;
+  auto kern = paged_mma<D, NR>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
@@ -551,10 +550,18 @@ static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   return launch_dependent(paged_mma_merge<D>, dim3(p.B * p.Hkv), dim3(kMmaThreads), 0, stream, 0u, p);
 }
 
+template <int D>
+static cudaError_t launch_mma_d(const ServeAttnParams& p, cudaStream_t stream) {
+  switch ((p.max_q * p.G + 7) / 8) {  // tiles of 8 query rows
+    case 1: return launch_mma<D, 1>(p, stream);
+    case 2: return launch_mma<D, 2>(p, stream);
+    case 3: return launch_mma<D, 3>(p, stream);
+    default: return launch_mma<D, 4>(p, stream);
+  }
+}
+
 cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream) {
-  const bool two = p.max_q * p.G > 16;
-  if (p.D == 128) return two ? launch_mma<128, 2>(p, stream) : launch_mma<128, 1>(p, stream);
-  return two ? launch_mma<64, 2>(p, stream) : launch_mma<64, 1>(p, stream);
+  return p.D == 128 ? launch_mma_d<128>(p, stream) : launch_mma_d<64>(p, stream);
 }
 
 }  // namespace specv
