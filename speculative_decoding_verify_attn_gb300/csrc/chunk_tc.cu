@@ -3,16 +3,21 @@
 //
 // One CTA per SM takes the pieces of the plan (chunk_plan.cu) in turn: 256 query rows (tokens x heads
 // of one kv head's group, two blocks of 128) against 128-key tiles.  Flash attention with the scores
-// of a tile in TMEM: S_w = Q_w K^T (M = N = 128, both operands in shared memory), then the row maximum,
+// of a tile in TMEM: S_w = Q_w K^T (M = N = 128, both operands in shared memory), then
 // P_w = 2^(s * scale - mu) rounded to bf16 over S_w's first 64 columns, then O_w += P_w V (P from TMEM,
-// V as an MN-major operand).  mu moves only when a tile's maximum exceeds it by more than 2^8 (O is
-// then rescaled in TMEM), which keeps every P below 2^8 and the result exact after normalisation.
+// V as an MN-major operand).  mu is the maximum of the piece's first tile; later tiles take no maximum
+// but look at their row sums, and only a sum above 2^20 moves mu (O is then rescaled in TMEM and the
+// tile done again).  Any mu gives the same normalised result as long as nothing overflows.
 //   warps 0, 1    loaders: K and V tiles into a ring of 32 KB stages (D = 128).  A tile that lies
 //                 wholly inside the sequence comes by TMA; edges (the sequence's end, tokens before the
 //                 window, bad page ids) and pages too small for TMA by cp.async with zeros in the gaps,
 //                 so nothing outside [lo, len) reaches the tensor core, NaN or not.
-//   warps 2, 3    MMA issuers, one per block; each walks the stages in order (K: Q K^T, V: P V), so
-//                 while one block's warps compute probabilities the other block's products run.
+//   warp 2        MMA issuer (one lane): P V of a tile and Q K^T of the next for block 0, then for block
+//                 1.  One issuer, because products of two issuers interleave in the tensor pipe: both
+//                 blocks' scores are then ready at the same time, and the blocks run in step instead
+//                 of one block's probabilities under the other's products.  The lane is chosen by
+//                 elect.sync: with lane == 0 the products of a tile took 3000 cycles to issue instead
+//                 of the 2050 they take to run (16K prompt: 1.85 ms against 1.34).
 //   warps 4-11    two warpgroups, a thread per query row.
 // Why 128-key tiles: an operand in shared memory is read anew by every instruction; per pair of blocks
 // and 128 keys that is 192 KB of reads with 128-key scores and 256 KB with 64-key ones, against 2048
@@ -33,7 +38,9 @@ namespace specv {
 constexpr int kCtThreads = 128 + 2 * 128;
 constexpr uint32_t kCtTmemCols = 512;
 constexpr int kCtHalf = 128 * 128;  // 128 rows of one 64-column half: 16 KB
-constexpr float kCtRescaleLog2 = 8.0f;
+// A row's sum over one tile up to which its reference stays (P is then below it, far inside bf16's and
+// fp32's range, and the final division removes the reference).
+constexpr float kCtMaxSum = 1048576.f;
 constexpr int kCtLag = 2;           // steps a loader's cp.async tiles may be in flight
 
 template <int D>
@@ -91,7 +98,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[NS], empty[NS];
-  __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain[2];
+  __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const uint32_t raw = smem_u32(smem_raw);
@@ -103,7 +110,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 2);   // one arrival per loader warp
-      mbar_init(&empty[i], 2);  // one per issuer
+      mbar_init(&empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sfull[w], 1);
@@ -111,8 +118,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_init(&pvdone[w], 1);
       mbar_init(&ofree[w], 4);
       mbar_init(&qfull[w], 4);
-      mbar_init(&drain[w], 1);
     }
+    mbar_init(&drain, 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll 1
         for (int x = 0; x < 2; ++x, ++step) {
           const int s = step % NS;
-          const bool got = mbar_wait_bounded(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
+          const bool got = mbar_wait_spin(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
           if (!__all_sync(0xffffffffu, got)) {
             fail();
             ok = false;
@@ -233,71 +240,76 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if ((by_copy >> (i - 1)) & 1u) hand_over(step - i);
     if (!ok || s_abort) {
       // copies still in flight into this CTA
-      for (int i = 1; i <= min(step, NS); ++i) mbar_wait_bounded(&full[(step - i) % NS], ((step - i) / NS) & 1, nullptr);
+      for (int i = 1; i <= min(step, NS); ++i) mbar_wait_spin(&full[(step - i) % NS], ((step - i) / NS) & 1, nullptr);
     }
   } else if (warp < 4) {
-    // ------------------------------------------------------------------ MMA issuer of block w
-    const int w = warp - 2;
-    if (lane == 0) {
-      const uint32_t qa = qs_u32 + w * C::kTile, sd = tmem + ct_col_s(w), od = tmem + ct_col_o(w);
-      int step = 0, t = 0, part = 0;  // t: tiles of this block so far, part: pieces it had tiles of
+    // ------------------------------------------------------------------ MMA issuer (warp 2, one lane)
+    if (warp == 2 && elect_one()) {
+      int step = 0, part[2] = {0, 0}, t[2] = {0, 0};  // pieces and tiles so far, by block
       bool ok = true;
+      // S_w = Q_w K^T (behind P_w V of the tile before, whose P it overwrites)
+      const uint32_t q_lo = tc::desc_lo(qs_u32, 16), k_lo = tc::desc_lo(stages_u32, 16);
+      const uint32_t v_lo = tc::desc_lo(stages_u32, kCtHalf);
+      auto issue_qk = [&](int w, int stage) {
+        const uint32_t qa = q_lo + w * (C::kTile >> 4), kb = k_lo + stage * (C::kTile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t koff = ((ks >> 2) * kCtHalf + (ks & 3) * 32) >> 4;
+          tc::mma_ss_lo(tmem + ct_col_s(w), qa + koff, kb + koff, C::kIdescQK, ks > 0 ? 1u : 0u);
+        }
+        tc::commit(&sfull[w]);
+      };
       for (int round = 0; ok && round < rounds; ++round) {
         CtItem it;
         if (!ct_item(p, n_items, round, it)) continue;
-        int b0, b1;
-        ct_block_units(p, it, w, b0, b1);
-        for (int u = it.u0; ok && u < it.u1; ++u) {
-          const bool in = u >= b0 && u < b1;
-          // K: S = Q K^T (behind P V of the tile before, whose P it overwrites)
-          {
-            const int s = step % NS;
-            if (in && u == b0 && !mbar_wait_bounded(&qfull[w], part & 1, &s_abort)) { ok = false; break; }
-            if (!mbar_wait_bounded(&full[s], (step / NS) & 1, &s_abort)) { ok = false; break; }
-            if (in) {
-              tc::fence_after();
-              const uint32_t kb = stages_u32 + s * C::kTile;
+        int b0[2], b1[2];
+        ct_block_units(p, it, 0, b0[0], b1[0]);
+        ct_block_units(p, it, 1, b0[1], b1[1]);
+        for (int u = it.u0 - 1; u < it.u1; ++u) {  // V of unit u (none before the first), K of u + 1
+          const int sv = step % NS, sk = (step + (u >= it.u0 ? 1 : 0)) % NS;
+          if (u >= it.u0 && !mbar_wait_spin(&full[sv], (step / NS) & 1, &s_abort)) { ok = false; break; }
+          if (u >= it.u0) ++step;
+          const bool more = u + 1 < it.u1;
+          if (more && !mbar_wait_spin(&full[sk], (step / NS) & 1, &s_abort)) { ok = false; break; }
+          if (more) ++step;
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t koff = (ks >> 2) * kCtHalf + (ks & 3) * 32;
-                tc::mma_ss(sd, tc::smem_desc(qa + koff, 16, 1024), tc::smem_desc(kb + koff, 16, 1024), C::kIdescQK,
-                           ks > 0 ? 1u : 0u);
+          for (int w = 0; w < 2; ++w) {
+            if (!ok) break;
+            if (u >= b0[w] && u < b1[w]) {  // O_w += P_w V
+              if ((u == b0[w] && part[w] >= 1 && !mbar_wait_spin(&ofree[w], (part[w] - 1) & 1, &s_abort)) ||
+                  !mbar_wait_spin(&pfull[w], t[w] & 1, &s_abort)) {
+                ok = false;
+                break;
               }
-              tc::commit(&sfull[w]);
-              tc::commit(&empty[s]);
-            } else {
-              mbar_arrive(&empty[s]);
-            }
-            ++step;
-          }
-          // V: O += P V
-          {
-            const int s = step % NS;
-            if (!mbar_wait_bounded(&full[s], (step / NS) & 1, &s_abort)) { ok = false; break; }
-            if (in) {
-              if (u == b0 && part >= 1 && !mbar_wait_bounded(&ofree[w], (part - 1) & 1, &s_abort)) { ok = false; break; }
-              if (!mbar_wait_bounded(&pfull[w], t & 1, &s_abort)) { ok = false; break; }
               tc::fence_after();
-              const uint32_t vb = stages_u32 + s * C::kTile;
+              const uint32_t vb = v_lo + sv * (C::kTile >> 4);
 #pragma unroll
               for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                tc::mma_ts(od, sd + ks * 8, tc::smem_desc(vb + ks * 2048, kCtHalf, 1024), C::kIdescPV,
-                           (ks > 0 || u > b0) ? 1u : 0u);
-              tc::commit(&pvdone[w]);
-              tc::commit(&empty[s]);
-              ++t;
-            } else {
-              mbar_arrive(&empty[s]);
+                tc::mma_ts_lo(tmem + ct_col_o(w), tmem + ct_col_s(w) + ks * 8, vb + ks * (2048 >> 4), C::kIdescPV,
+                              (ks > 0 || u > b0[w]) ? 1u : 0u);
+              if (u == b1[w] - 1) tc::commit(&pvdone[w]);
+              ++t[w];
             }
-            ++step;
+            if (more && u + 1 >= b0[w] && u + 1 < b1[w]) {
+              if (u + 1 == b0[w] && !mbar_wait_spin(&qfull[w], part[w] & 1, &s_abort)) {
+                ok = false;
+                break;
+              }
+              tc::fence_after();
+              issue_qk(w, sk);
+            }
           }
+          if (!ok) break;
+          if (u >= it.u0) tc::commit(&empty[sv]);
+          if (more) tc::commit(&empty[sk]);
         }
-        if (b1 > b0) ++part;
+        if (b1[0] > b0[0]) ++part[0];
+        if (b1[1] > b0[1]) ++part[1];
       }
       if (!ok) {
         fail();
-        tc::commit(&drain[w]);  // every MMA issued so far has finished before TMEM is released
-        mbar_wait_bounded(&drain[w], 0, nullptr);
+        tc::commit(&drain);  // every MMA issued so far has finished before TMEM is released
+        mbar_wait_spin(&drain, 0, nullptr);
       }
     }
   } else {
@@ -311,7 +323,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const float sc = p.scale_log2;
 
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool got = mbar_wait_bounded(bar, parity, &s_abort);
+      const bool got = mbar_wait_spin(bar, parity, &s_abort);
       return __all_sync(0xffffffffu, got);
     };
     // the next piece in which this block has tiles, its rows into shared memory (K-major, 128-byte
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
     bool have = next_piece(it, b0, b1), ok = true;
     if (have) load_q(it);
-    int t = 0;
+    int t = 0, part = 0;
     while (have && ok) {
       CtItem nx;
       int nb0 = 0, nb1 = 0;
@@ -366,87 +378,89 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       for (int u = b0; u < b1; ++u, ++t) {
         if (!warp_wait(&sfull[w], t & 1)) { ok = false; break; }
         tc::fence_after();
-        uint32_t s0[32], s1[32], s2[32], s3[32];
-        tc::ld32(sbuf, s0);
-        tc::ld32(sbuf + 32, s1);
-        tc::ld32(sbuf + 64, s2);
-        tc::ld32(sbuf + 96, s3);
         const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
-        tc::ld_wait(s0);
-        tc::ld_wait(s1);
-        tc::ld_wait(s2);
-        tc::ld_wait(s3);
-        if (edge) {
-          auto hide = [&](uint32_t(&v)[32], int c0) {
+        // P = 2^(s * scale - mu) against the present reference, as bf16 pairs; only where a row's sum
+        // says that a score lies far above it (or nothing has been seen yet) is the tile's maximum
+        // taken, O rescaled and the tile done again
+        uint32_t pk[64];
+        float sum;
+        bool exact = u == b0;
+        for (;;) {
+          uint32_t s0[32], s1[32], s2[32], s3[32];
+          tc::ld32(sbuf, s0);
+          tc::ld32(sbuf + 32, s1);
+          tc::ld32(sbuf + 64, s2);
+          tc::ld32(sbuf + 96, s3);
+          tc::ld_wait(s0);
+          tc::ld_wait(s1);
+          tc::ld_wait(s2);
+          tc::ld_wait(s3);
+          if (edge) {
+            auto hide = [&](uint32_t(&v)[32], int c0) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e > hi || c0 + e < lo) v[e] = 0xff800000u;
-          };
-          hide(s0, 0);
-          hide(s1, 32);
-          hide(s2, 64);
-          hide(s3, 96);
-        }
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+              for (int e = 0; e < 32; ++e)
+                if (c0 + e > hi || c0 + e < lo) v[e] = 0xff800000u;
+            };
+            hide(s0, 0);
+            hide(s1, 32);
+            hide(s2, 64);
+            hide(s3, 96);
+          }
+          if (exact) {
+            float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          mx[0] = fmax3(mx[0], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-          mx[1] = fmax3(mx[1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
-          mx[2] = fmax3(mx[2], __uint_as_float(s2[e]), __uint_as_float(s2[e + 1]));
-          mx[3] = fmax3(mx[3], __uint_as_float(s3[e]), __uint_as_float(s3[e + 1]));
-        }
-        const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float tmax = raw_max == neg_inf() ? raw_max : raw_max * sc;
-        // ---- reference maximum: the first tile's, moved when a tile exceeds it by more than 2^8
-        if (u == b0) {
-          m_run = tmax;
-        } else {
-          const bool need = tmax > m_run + kCtRescaleLog2 || (m_run == neg_inf() && tmax > neg_inf());
-          if (__any_sync(0xffffffffu, need)) {
-            // O may be touched once the P V before has completed
-            if (!warp_wait(&pvdone[w], (t - 1) & 1)) { ok = false; break; }
-            tc::fence_after();
-            float alpha = 1.f;
-            if (need) {
-              alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - tmax);
-              l *= alpha;
-              m_run = tmax;
+            for (int e = 0; e < 32; e += 2) {
+              mx[0] = fmax3(mx[0], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+              mx[2] = fmax3(mx[2], __uint_as_float(s2[e]), __uint_as_float(s2[e + 1]));
+              mx[3] = fmax3(mx[3], __uint_as_float(s3[e]), __uint_as_float(s3[e + 1]));
             }
-            uint32_t v[32];
+            const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float m_new = raw_max == neg_inf() ? m_run : fmaxf(m_run, raw_max * sc);
+            const float alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - m_new);
+            l *= alpha;
+            m_run = m_new;
+            if (u > b0) {
+              // the P V before has completed: this tile's Q K^T, issued after it, has
+              uint32_t v[32];
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tc::ld32(obuf + c * 32, v);
-              tc::ld_wait(v);
+              for (int c = 0; c < D / 32; ++c) {
+                tc::ld32(obuf + c * 32, v);
+                tc::ld_wait(v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tc::st32(obuf + c * 32, v);
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                tc::st32(obuf + c * 32, v);
+              }
+              tc::st_wait();
             }
-            tc::st_wait();
           }
-        }
-        // ---- P = 2^(s * scale - mu) as bf16 pairs over S's first 64 columns
-        const float mu = m_run == neg_inf() ? 0.f : m_run;
-        float sums[4] = {0.f, 0.f, 0.f, 0.f};
-        auto chunk = [&](const uint32_t(&v)[32], int c) {
-          uint32_t pk[16];
+          const float nmu = m_run == neg_inf() ? 0.f : -m_run;
+          float sums[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          auto chunk = [&](const uint32_t(&v)[32], int c) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0, x1;
-            fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), sc, -mu, x0, x1);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            add2(sums[(e >> 1) & 1], sums[2 + ((e >> 1) & 1)], p0, p1);
-            pk[e / 2] = pack_bf16(p0, p1);
-          }
-          __syncwarp();
-          tc::st16(sbuf + c * 16, pk);
-        };
-        chunk(s0, 0);
-        chunk(s1, 1);
-        chunk(s2, 2);
-        chunk(s3, 3);
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), sc, nmu, x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              add2(sums[e & 6], sums[(e & 6) + 1], p0, p1);
+              pk[c * 16 + e / 2] = pack_bf16(p0, p1);
+            }
+          };
+          chunk(s0, 0);
+          chunk(s1, 1);
+          chunk(s2, 2);
+          chunk(s3, 3);
+          sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
+          if (exact || !__any_sync(0xffffffffu, !(sum <= kCtMaxSum) || m_run == neg_inf())) break;
+          exact = true;
+        }
+        if (!ok) break;
+        l += sum;
+        __syncwarp();
+        tc::st32(sbuf, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
+        tc::st32(sbuf + 32, reinterpret_cast<uint32_t(&)[32]>(pk[32]));
         tc::st_wait();
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[w]);
@@ -454,7 +468,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (!ok) break;
       if (have_next) load_q(nx);  // the piece's last Q K^T has read its rows
       // ---- epilogue, once the piece's last P V is done
-      if (!warp_wait(&pvdone[w], (t - 1) & 1)) { ok = false; break; }
+      if (!warp_wait(&pvdone[w], part & 1)) { ok = false; break; }
+      ++part;
       tc::fence_after();
       if (it.slot >= 0) {
         const int64_t rec = (int64_t)it.slot * p.Hkv + it.g;

@@ -421,6 +421,28 @@ def test_large_scores_and_scale(sv):
     check(o[:r], ref[:r], A[:r], S, 64, 300, "bf16", "f32")
 
 
+@pytest.mark.parametrize("q_len", [[2], [60]])
+@pytest.mark.parametrize("growth", [0.02, 0.2, -0.2])
+def test_rising_scores(sv, q_len, growth):
+    """Scores that rise (or fall) along the keys, so that the running reference lags behind the maximum
+    by a few powers of two, or has to move in every tile."""
+    torch = torch_mod()
+    p = Paged(q_len, [1500], 4, 2, 64, 64, seed=140)
+    k = p.k.float().cpu()
+    u = torch.randn(64, generator=torch.Generator().manual_seed(1))
+    u /= u.norm()
+    for t in range(1500):
+        k[p.table[0, t // 64], :, t % 64] = 0.2 * k[p.table[0, t // 64], :, t % 64] + growth * t * u
+    p.k = k.to(torch.bfloat16).cuda()
+    p.q = (p.q.float() * 0.1 + 4 * u).to(torch.bfloat16)
+    p.d_q = p.q.cuda()
+    (ref, A, S), _, _ = p.oracle()
+    o, st = p.run(sv)
+    assert st == 0
+    r = p.start[-1]
+    check(o[:r], ref[:r], A[:r], S, 64, 1500, "bf16", "f32")
+
+
 def test_mixed_lists_agree_with_verify_attn(sv):
     """The paged call on pages that tile a dense cache gives spec_verify_attn's answer."""
     torch = torch_mod()
