@@ -43,10 +43,10 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
     if (round * (int)gridDim.x >= n_items) break;
     if (idx >= n_items) continue;
     const int g = idx % p.Hkv;
-    const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p.items + idx / p.Hkv));
-    const int slot = __ldcg(&p.items[idx / p.Hkv].slot);
-    const int b = w0.x, row0 = w0.y, u0 = w0.z, u1 = w0.w;
-    const SeqInfo s = seq_info(p, b);
+    const int4* src = reinterpret_cast<const int4*>(p.items + idx / p.Hkv);
+    const int4 w0 = __ldcg(src), w1 = __ldcg(src + 1), w2 = __ldcg(src + 2);
+    const int b = w0.x, row0 = w0.y, u0 = w0.z, u1 = w0.w, slot = w1.x;
+    const SeqInfo s{w1.y, w1.z, w1.w, w2.x, 0u};
     const int rows = min(kF32Rows, s.n * p.G - row0);
     __syncthreads();
     for (int i = tid; i < kF32Rows * C4; i += kF32Threads) {

@@ -4,7 +4,7 @@
 // A row tile (row_tile consecutive rows of one sequence's chunk, for one kv head) needs the key units
 // its rows see; under the causal mask these differ from tile to tile, and lengths are known on the
 // device only.  One CTA therefore plans each call: with U units in all, a tile of more than
-// per = ceil(U / grid) units is cut into equal pieces of at most `per`, and the pieces are sorted by
+// per = ceil(U / grid) units (min_units at least) is cut into equal pieces of at most `per`, and the pieces are sorted by
 // size in descending order (a counting sort over 256 sizes), so that CTA c taking pieces c,
 // 2 grid - 1 - c, 2 grid + c, ... gets nearly equal work.  The order among equal sizes varies from
 // run to run; it decides only who computes a piece, and pieces are merged in key order.
@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "launch_cache.h"
 #include "serve_common.cuh"
 #include "serve_internal.h"
 
@@ -19,16 +20,17 @@ namespace specv {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 256;
-constexpr int kPlanMaxB = 4096;
 
 __device__ __forceinline__ int chunk_tiles(const ServeAttnParams& p, const SeqInfo& s) {
   return s.len > 0 ? (int)(((int64_t)s.n * p.G + p.row_tile - 1) / p.row_tile) : 0;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant__ ServeAttnParams p) {
-  pdl_launch_dependents();
-  __shared__ int s_pre[kPlanMaxB + 1];  // tiles of the sequences before b
-  __shared__ int64_t s_warp[32];
+struct PlanTile {
+  int b, row0, u0, u1;
+};
+
+__device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, int* s_n, int* s_len) {
+  __shared__ uint32_t s_warp[32];
   __shared__ int64_t s_sum[32];
   __shared__ int s_bin[kPlanBins];
   __shared__ int s_slots, s_splits;
@@ -39,46 +41,42 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
     s_splits = 0;
   }
   if (tid < kPlanBins) s_bin[tid] = 0;
-  __syncthreads();
 
-  // ---- tiles per sequence, and their prefix
-  int64_t run = 0;
-  for (int b0 = 0; b0 < p.B && run <= p.max_tiles; b0 += kPlanThreads) {
+  // ---- tiles per sequence, and their prefix s_pre.  Overlapping ranges can add up to more rows than
+  // there are; sums are capped where the plan has no room for them anyway.
+  constexpr uint32_t kCap = 1u << 25;  // above any max_tiles
+  uint32_t run = 0;
+  for (int b0 = 0; b0 < p.B && run <= (uint32_t)p.max_tiles; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int n = 0;
+    uint32_t n = 0;
     if (b < p.B) {
       const SeqInfo s = seq_info(p, b);
-      n = chunk_tiles(p, s);
+      n = (uint32_t)chunk_tiles(p, s);
+      s_n[b] = s.n;
+      s_len[b] = s.len;
       if (s.bad) status_report(p.status, s.bad);
     }
-    int64_t x = n;
+    uint32_t x = n;  // at most 2^22 each
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) s_warp[warp] = min(x, kCap);
     __syncthreads();
-    int64_t pre = run, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < warp) pre += s_warp[w];
-      all += s_warp[w];
-    }
-    if (b < p.B) s_pre[b] = (int)min(pre + x - n, (int64_t)p.max_tiles);
-    run += all;
+    const uint32_t sums = s_warp[lane];
+    const uint32_t pre = run + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
+    run = min(run + __reduce_add_sync(0xffffffffu, sums), kCap);
+    if (b < p.B) s_pre[b] = (int)min(pre + x - n, kCap);
     __syncthreads();
   }
-  // ranges that overlap can add up to more rows than there are: the plan then has no room for them
-  const int tiles = run <= p.max_tiles ? (int)run : 0;
+  const int tiles = run <= (uint32_t)p.max_tiles ? (int)run : 0;
   if (tid == 0) {
     s_pre[p.B] = tiles;
-    if (tiles != run) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_RANGE);
+    if (tiles == 0 && run > 0) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_RANGE);
   }
   __syncthreads();
 
-  struct Tile {
-    int b, row0, u0, u1;
-  };
   auto tile_of = [&](int t) {
     int lo = 0, hi = p.B;  // the last b with s_pre[b] <= t
     while (hi - lo > 1) {
@@ -86,65 +84,73 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
       if (s_pre[mid] <= t) lo = mid;
       else hi = mid;
     }
-    Tile r;
+    PlanTile r;
     r.b = lo;
-    const SeqInfo s = seq_info(p, lo);
+    const int n = s_n[lo], len = s_len[lo], base = len - n;
     r.row0 = (t - s_pre[lo]) * p.row_tile;
-    const int last = min(s.n * p.G, r.row0 + p.row_tile) - 1;
-    const int base = s.len - s.n;
-    const int first_key = p.window > 0 ? max(0, base + r.row0 / p.G + 1 - min(p.window, s.len)) : 0;
+    const int last = min(n * p.G, r.row0 + p.row_tile) - 1;
+    const int first_key = p.window > 0 ? max(0, base + r.row0 / p.G + 1 - min(p.window, len)) : 0;
     r.u0 = first_key / p.unit_keys;
     r.u1 = (base + last / p.G) / p.unit_keys + 1;
     return r;
   };
+  // the usual plan has a tile per thread at most
+  PlanTile own{0, 0, 0, 0};
+  if (tid < tiles) own = tile_of(tid);
+  auto tile = [&](int t) { return t == tid ? own : tile_of(t); };
 
   // ---- total units
   int64_t mine = 0;
   for (int t = tid; t < tiles; t += kPlanThreads) {
-    const Tile r = tile_of(t);
+    const PlanTile r = tile(t);
     mine += r.u1 - r.u0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_sum[warp] = mine;
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) total += s_sum[w];
-  const int per = (int)max((int64_t)1, (total * p.Hkv + p.grid - 1) / p.grid);
+  int64_t total = s_sum[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int per = (int)max((int64_t)p.min_units, (total * p.Hkv + p.grid - 1) / p.grid);
 
-  // pieces of a tile and the bin of their size; a tile is left whole where the records would not
-  // hold its pieces (sum of ceil(n / per) over tiles of n > per units is below 2 grid / Hkv)
+  // the sum of ceil(n / per) over tiles of n > per units is below 2 grid / Hkv, what the records hold
   auto pieces_of = [&](int n) { return n > per ? (n + per - 1) / per : 1; };
+  const float bin_scale = (float)(kPlanBins - 1) / (float)per;
   auto bin_of = [&](int n, int k) {
-    const int size = (n + k - 1) / k;
-    return kPlanBins - 1 - (int)((int64_t)size * (kPlanBins - 1) / per);
+    const int size = k == 1 ? n : (n + k - 1) / k;
+    return kPlanBins - 1 - min(kPlanBins - 1, (int)((float)size * bin_scale));
   };
   for (int t = tid; t < tiles; t += kPlanThreads) {
-    const Tile r = tile_of(t);
+    const PlanTile r = tile(t);
     const int n = r.u1 - r.u0, k = pieces_of(n);
     atomicAdd(&s_bin[bin_of(n, k)], k);
   }
   __syncthreads();
-  if (warp == 0) {  // exclusive prefix of the bins
-    int carry = 0;
-    for (int i0 = 0; i0 < kPlanBins; i0 += 32) {
-      const int n = s_bin[i0 + lane];
-      int x = n;
+  if (warp == 0) {  // exclusive prefix of the bins, 8 per lane
+    int v[kPlanBins / 32], sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      s_bin[i0 + lane] = carry + x - n;
-      carry += __shfl_sync(0xffffffffu, x, 31);
+    for (int i = 0; i < kPlanBins / 32; ++i) {
+      v[i] = s_bin[lane * (kPlanBins / 32) + i];
+      sum += v[i];
     }
-    if (lane == 0) {
-      p.plan->n_items = carry;
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    int at = x - sum;
+#pragma unroll
+    for (int i = 0; i < kPlanBins / 32; ++i) {
+      s_bin[lane * (kPlanBins / 32) + i] = at;
+      at += v[i];
+    }
+    if (lane == 31) p.plan->n_items = x;
   }
   __syncthreads();
   for (int t = tid; t < tiles; t += kPlanThreads) {
-    const Tile r = tile_of(t);
+    const PlanTile r = tile(t);
     const int n = r.u1 - r.u0, k = pieces_of(n);
     const int at = atomicAdd(&s_bin[bin_of(n, k)], k);
     int slot = -1;
@@ -152,35 +158,40 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
       slot = atomicAdd(&s_slots, k);
       p.splits[atomicAdd(&s_splits, 1)] = ChunkSplit{r.b, r.row0, slot, k};
     }
+    const SeqInfo s = seq_info(p, r.b);
     for (int i = 0; i < k; ++i) {
-      ChunkItem it;
-      it.b = r.b;
-      it.row0 = r.row0;
-      it.u0 = r.u0 + (int)((int64_t)n * i / k);
-      it.u1 = r.u0 + (int)((int64_t)n * (i + 1) / k);
-      it.slot = k > 1 ? slot + i : -1;
-      it.pad0 = it.pad1 = it.pad2 = 0;
-      p.items[at + i] = it;
+      int4* dst = reinterpret_cast<int4*>(p.items + at + i);
+      const int u0 = r.u0 + (k == 1 ? 0 : (int)((int64_t)n * i / k));
+      const int u1 = r.u0 + (k == 1 ? n : (int)((int64_t)n * (i + 1) / k));
+      dst[0] = make_int4(r.b, r.row0, u0, u1);
+      dst[1] = make_int4(k > 1 ? slot + i : -1, s.q0, s.n, s.len);
+      dst[2] = make_int4(s.lo, 0, 0, 0);
     }
   }
   __syncthreads();
   if (tid == 0) p.plan->n_splits = s_splits;
 }
 
-// Sequence blockIdx.x's new K and V rows, a thread per 16-byte chunk.
-__global__ void __launch_bounds__(256) chunk_append(const __grid_constant__ ServeAttnParams p, int elem) {
+// CTA 0 makes the plan; the others (if there are new rows) append: CTA 1 + b + B y takes sequence b, a
+// thread per 16-byte chunk of a row.
+__global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_constant__ ServeAttnParams p, int elem) {
   pdl_launch_dependents();
-  const int b = blockIdx.x, per_row = p.D * elem / 16;
+  extern __shared__ int s_seq[];  // [B + 1], [B], [B]
+  if (blockIdx.x == 0) {
+    plan_body(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1);
+    return;
+  }
+  const int b = (blockIdx.x - 1) % p.B, y = (blockIdx.x - 1) / p.B, ny = (gridDim.x - 1) / p.B;
+  const int per_row = p.D * elem / 16;
   const SeqInfo s = seq_info(p, b);
   const int64_t total = s.len > 0 ? (int64_t)s.n * p.Hkv * per_row : 0;
-  pdl_wait();  // the plan clears the status word first
-  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.y * blockDim.x) {
+  for (int64_t i = (int64_t)y * blockDim.x + threadIdx.x; i < total; i += (int64_t)ny * blockDim.x) {
     const int c = (int)(i % per_row);
-    const int g = (int)(i / per_row % p.Hkv);
-    const int j = (int)(i / per_row / p.Hkv);
+    const int64_t rest = i / per_row;
+    const int g = (int)(rest % p.Hkv), j = (int)(rest / p.Hkv);
     const int64_t to = key_offset(p, s, b, g, s.len - s.n + j);
     if (to < 0) {
-      atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+      status_report(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
       continue;
     }
     const int64_t from = (int64_t)(s.q0 + j) * p.new_st + (int64_t)g * p.new_sh;
@@ -191,13 +202,19 @@ __global__ void __launch_bounds__(256) chunk_append(const __grid_constant__ Serv
   }
 }
 
-// Merge of split tiles, thread m a row, 8 columns per CTA; records are column-major, so a warp's
-// loads of one column are one line.  Also zeros the rows of sequences with a bad kv_len.
+// Merge of split tiles: a unit of work is (split tile, kv head, block of kMergeRows rows, 8 columns),
+// thread m a row; records are column-major, so a warp's loads of one column are one line.  The pieces'
+// weights 2^(m_i - M) are worked out once per row and unit; loads go out several pieces at a time.
+// Also zeros the rows of sequences with a bad kv_len.
 constexpr int kChunkMergeCols = 8;
-__global__ void __launch_bounds__(128) chunk_merge(const __grid_constant__ ServeAttnParams p) {
+constexpr int kMergeThreads = 128;
+constexpr int kMergeBatch = 4;
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_constant__ ServeAttnParams p) {
+  const int rows_per = min(kMergeThreads, p.row_tile), groups = kMergeThreads / rows_per;
+  const int m_in = threadIdx.x % rows_per, sub = threadIdx.x / rows_per;
+  const int blocks = p.row_tile / rows_per, chunks = p.D / kChunkMergeCols;
   pdl_wait();
-  const int flat = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-  for (int b = flat; b < p.B; b += gridDim.x * gridDim.y * gridDim.z) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const SeqInfo s = seq_info(p, b);
     if (s.len > 0 || s.n == 0) continue;
     for (int64_t i = threadIdx.x; i < (int64_t)s.n * p.Hq * p.D; i += blockDim.x) {
@@ -207,35 +224,41 @@ __global__ void __launch_bounds__(128) chunk_merge(const __grid_constant__ Serve
       else reinterpret_cast<float*>(p.o)[off] = 0.f;
     }
   }
-  const int n_splits = __ldcg(&p.plan->n_splits);
-  const int d0 = blockIdx.z * kChunkMergeCols;
-  for (int x = blockIdx.x; x < n_splits * p.Hkv; x += gridDim.x) {
-    const int g = x % p.Hkv;
-    const int4 sp = __ldcg(reinterpret_cast<const int4*>(p.splits + x / p.Hkv));
+  const int total = __ldcg(&p.plan->n_splits) * p.Hkv * blocks * chunks;  // below 2^20
+  for (int x = blockIdx.x * groups + sub; x < total; x += gridDim.x * groups) {
+    const int d0 = x % chunks * kChunkMergeCols;
+    const int m = x / chunks % blocks * rows_per + m_in;
+    const int g = x / chunks / blocks % p.Hkv;
+    const int4 sp = __ldcg(reinterpret_cast<const int4*>(p.splits + x / chunks / blocks / p.Hkv));
     const ChunkSplit split{sp.x, sp.y, sp.z, sp.w};
     const SeqInfo s = seq_info(p, split.b);
-    const int m = blockIdx.y * blockDim.x + threadIdx.x;
-    if (m >= p.row_tile || split.row0 + m >= s.n * p.G) continue;
+    if (split.row0 + m >= s.n * p.G) continue;
+    const float2* ml = p.part_ml + ((int64_t)split.slot * p.Hkv + g) * p.row_tile + m;
+    const int64_t ml_step = (int64_t)p.Hkv * p.row_tile, o_step = ml_step * p.D;
+    const float* src = p.part_o + (((int64_t)split.slot * p.Hkv + g) * p.D + d0) * p.row_tile + m;
     float M = neg_inf();
-    for (int i = 0; i < split.pieces; ++i)
-      M = fmaxf(M, __ldcg(&p.part_ml[((int64_t)(split.slot + i) * p.Hkv + g) * p.row_tile + m]).x);
+#pragma unroll 8
+    for (int i = 0; i < split.pieces; ++i) M = fmaxf(M, __ldcg(ml + i * ml_step).x);
     float L = 0.f, acc[kChunkMergeCols];
 #pragma unroll
     for (int e = 0; e < kChunkMergeCols; ++e) acc[e] = 0.f;
-    if (M != neg_inf()) {
-#pragma unroll 2
-      for (int i = 0; i < split.pieces; ++i) {
-        const int64_t rec = (int64_t)(split.slot + i) * p.Hkv + g;
-        const float2 ml = __ldcg(&p.part_ml[rec * p.row_tile + m]);
-        const float w = ml.x == neg_inf() ? 0.f : exp2f(ml.x - M);
-        const float* src = p.part_o + (rec * p.D + d0) * p.row_tile + m;
-        L += w * ml.y;
+    for (int i0 = 0; i0 < split.pieces; i0 += kMergeBatch) {
+      float2 a[kMergeBatch];
+      float v[kMergeBatch][kChunkMergeCols];
 #pragma unroll
-        for (int e = 0; e < kChunkMergeCols; ++e) {
-          // a piece in which the row saw nothing holds no value
-          const float v = __ldcg(src + e * p.row_tile);
-          acc[e] = fmaf(w, ml.x == neg_inf() ? 0.f : v, acc[e]);
-        }
+      for (int u = 0; u < kMergeBatch; ++u) {
+        const bool in = i0 + u < split.pieces;
+        a[u] = in ? __ldcg(ml + (i0 + u) * ml_step) : make_float2(neg_inf(), 0.f);
+#pragma unroll
+        for (int e = 0; e < kChunkMergeCols; ++e) v[u][e] = in ? __ldcg(src + (i0 + u) * o_step + e * p.row_tile) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kMergeBatch; ++u) {
+        if (a[u].x == neg_inf()) continue;  // the row saw nothing there: no value was written
+        const float w = exp2f(a[u].x - M);
+        L += w * a[u].y;
+#pragma unroll
+        for (int e = 0; e < kChunkMergeCols; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -243,12 +266,12 @@ __global__ void __launch_bounds__(128) chunk_merge(const __grid_constant__ Serve
     if (p.o_bf16) {
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off;
       if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-        uint4 v;
-        v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-        v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-        v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
-        v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
-        *reinterpret_cast<uint4*>(dst) = v;
+        uint4 q;
+        q.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+        q.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+        q.z = pack_bf16(acc[4] * inv, acc[5] * inv);
+        q.w = pack_bf16(acc[6] * inv, acc[7] * inv);
+        *reinterpret_cast<uint4*>(dst) = q;
       } else {
 #pragma unroll
         for (int e = 0; e < kChunkMergeCols; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
@@ -294,20 +317,21 @@ void chunk_workspace_carve(void* ws, ServeAttnParams* p) {
   p->max_tiles = (int)chunk_max_tiles(p->T, p->G, p->B, p->row_tile);
 }
 
-cudaError_t launch_chunk_plan(const ServeAttnParams& p, cudaStream_t stream) {
-  chunk_plan<<<1, kPlanThreads, 0, stream>>>(p);
+cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
+  const int smem = (3 * p.B + 1) * (int)sizeof(int);
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(chunk_prepare), smem);
+  if (e != cudaSuccess) return e;
+  unsigned grid = 1;
+  if (p.k_new) {  // about 600 CTAs at most, one per sequence at least
+    const int64_t want = ((int64_t)p.max_q * p.Hkv * (p.D * elem_bytes / 16) + kPlanThreads - 1) / kPlanThreads;
+    const int64_t most = (600 + p.B - 1) / p.B;
+    grid += (unsigned)p.B * (unsigned)(want < most ? want : most);
+  }
+  chunk_prepare<<<grid, kPlanThreads, smem, stream>>>(p, elem_bytes);
   return cudaGetLastError();
 }
-cudaError_t launch_chunk_append(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
-  const int64_t want = ((int64_t)p.max_q * p.Hkv * (p.D * elem_bytes / 16) + 255) / 256;
-  const int64_t most = p.B < 4096 ? 4096 / p.B : 1;  // about 4096 CTAs of 256 threads at most
-  return launch_dependent(chunk_append, dim3(p.B, (unsigned)(want < most ? want : most)), dim3(256), 0, stream, 0u, p,
-                          elem_bytes);
-}
 cudaError_t launch_chunk_merge(const ServeAttnParams& p, cudaStream_t stream) {
-  const unsigned threads = p.row_tile < 128 ? p.row_tile : 128;
-  const dim3 grid(p.grid, p.row_tile / threads, p.D / kChunkMergeCols);
-  return launch_dependent(chunk_merge, grid, dim3(threads), 0, stream, 0u, p);
+  return launch_dependent(chunk_merge, dim3(4 * p.grid), dim3(kMergeThreads), 0, stream, 0u, p);
 }
 
 }  // namespace specv

@@ -60,21 +60,29 @@ struct CtItem {
   int b, g, row0, u0, u1, slot;
   SeqInfo s;
 };
-// The round's piece of this CTA (pieces sorted by size: forth and back over the CTAs).
-__device__ __forceinline__ bool ct_item(const ServeAttnParams& p, int n_items, int round, CtItem& it) {
+// The round's piece of this CTA (pieces sorted by size: forth and back over the CTAs), as it lies in
+// memory (u0 == u1: none).  Readers fetch a round ahead.
+struct CtRaw {
+  int4 a, b;
+  int lo, g;
+};
+__device__ __forceinline__ CtRaw ct_fetch(const ServeAttnParams& p, int n_items, int round) {
   const int grid = gridDim.x, cta = blockIdx.x;
   const int64_t idx = (int64_t)round * grid + ((round & 1) ? grid - 1 - cta : cta);
-  if (idx >= n_items) return false;
-  const ChunkItem* src = p.items + idx / p.Hkv;
-  const int4 a = __ldcg(reinterpret_cast<const int4*>(src));
-  it.b = a.x;
-  it.row0 = a.y;
-  it.u0 = a.z;
-  it.u1 = a.w;
-  it.slot = __ldcg(&src->slot);
-  it.g = (int)(idx % p.Hkv);
-  it.s = seq_info(p, it.b);
-  return true;
+  CtRaw r;
+  r.a = r.b = make_int4(0, 0, 0, 0);
+  r.lo = r.g = 0;
+  if (idx < n_items) {
+    const int4* src = reinterpret_cast<const int4*>(p.items + idx / p.Hkv);
+    r.a = __ldcg(src);
+    r.b = __ldcg(src + 1);
+    r.lo = __ldcg(reinterpret_cast<const int*>(src + 2));
+    r.g = (int)(idx % p.Hkv);
+  }
+  return r;
+}
+__device__ __forceinline__ CtItem ct_item(const CtRaw& r) {
+  return CtItem{r.a.x, r.g, r.a.y, r.a.z, r.a.w, r.b.x, SeqInfo{r.b.y, r.b.z, r.b.w, r.lo, 0u}};
 }
 __device__ __forceinline__ int ct_rounds(int n_items) { return (n_items + (int)gridDim.x - 1) / (int)gridDim.x; }
 
@@ -155,9 +163,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[done % NS]);
     };
+    CtRaw ahead = ct_fetch(p, n_items, 0);
     for (int round = 0; ok && round < rounds; ++round) {
-      CtItem it;
-      if (!ct_item(p, n_items, round, it)) continue;
+      const CtItem it = ct_item(ahead);
+      ahead = ct_fetch(p, n_items, round + 1);
       for (int u = it.u0; ok && u < it.u1; ++u) {
         const int key0 = u * kTcKeys;
         // rows of the tile: offsets of this lane's two of the warp's 64 keys, -1 where zeros go
@@ -184,6 +193,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
           }
         }
+        const bool groups = !tma && (!p.paged || (p.page_size & 15) == 0) &&
+                            __all_sync(0xffffffffu, off[0] >= 0 && off[1] >= 0);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x, ++step) {
           const int s = step % NS;
@@ -213,6 +224,21 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     "l"(reinterpret_cast<uint64_t>(x == 0 ? &tmK : &tmV)), "r"(0), "r"(ip), "r"(half), "r"(it.g),
                     "r"(pg), "r"(smem_u32(&full[s]))
                     : "memory");
+              }
+            }
+          } else if (groups) {
+            // 16 consecutive tokens of one page at a time; for rows i * RPI + lane / CH the lane's part
+            // of the place in the tile is constant, and i changes it by an offset and an XOR
+            const int c = lane % CH, rl = lane / CH;
+            const uint32_t at = dst + (c >> 3) * kCtHalf + (warp * 64 + rl) * 128 + (((c & 7) ^ rl) << 4);
+            const int64_t step_b = p.kv_st * RPI;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __nv_bfloat16* src = kv[x] + __shfl_sync(0xffffffffu, off[q >> 1], (q & 1) * 16) + rl * p.kv_st + c * 8;
+#pragma unroll
+              for (int i = 0; i < 16 / RPI; ++i) {
+                cp_async16((at + (q * 16 + i * RPI) * 128) ^ (((i * RPI) & 7) << 4), src);
+                src += step_b;
               }
             }
           } else {
@@ -259,9 +285,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tc::commit(&sfull[w]);
       };
+      CtRaw ahead = ct_fetch(p, n_items, 0);
       for (int round = 0; ok && round < rounds; ++round) {
-        CtItem it;
-        if (!ct_item(p, n_items, round, it)) continue;
+        const CtItem it = ct_item(ahead);
+        ahead = ct_fetch(p, n_items, round + 1);
+        if (it.u0 >= it.u1) continue;
         int b0[2], b1[2];
         ct_block_units(p, it, 0, b0[0], b1[0]);
         ct_block_units(p, it, 1, b0[1], b1[1]);
@@ -319,56 +347,62 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const int m = sub * 32 + lane;   // TMEM lane = row of the block
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
     const uint32_t sbuf = tl + ct_col_s(w), obuf = tl + ct_col_o(w);
-    uint8_t* qblock = qs + w * C::kTile;
+    const uint32_t qblock_u32 = qs_u32 + w * C::kTile;
     const float sc = p.scale_log2;
 
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       const bool got = mbar_wait_spin(bar, parity, &s_abort);
       return __all_sync(0xffffffffu, got);
     };
-    // the next piece in which this block has tiles, its rows into shared memory (K-major, 128-byte
-    // swizzle; zeros for padding rows); pieces without tiles leave an empty record
-    CtItem it;
-    int b0 = 0, b1 = 0, round = 0;
+    // the next piece in which this block has tiles; pieces without leave an empty record
+    int round = 0;
+    CtRaw ahead = ct_fetch(p, n_items, 0);
     auto next_piece = [&](CtItem& n, int& nb0, int& nb1) -> bool {
-      for (; round < rounds; ++round) {
-        if (!ct_item(p, n_items, round, n)) continue;
+      while (round < rounds) {
+        n = ct_item(ahead);
+        ahead = ct_fetch(p, n_items, ++round);
         ct_block_units(p, n, w, nb0, nb1);
-        if (nb1 > nb0) {
-          ++round;
-          return true;
-        }
+        if (nb1 > nb0) return true;
         if (n.slot >= 0)
           p.part_ml[((int64_t)n.slot * p.Hkv + n.g) * kTcRows + w * 128 + m] = make_float2(neg_inf(), 0.f);
       }
       return false;
     };
-    auto load_q = [&](const CtItem& n) {
+    // the warp's 32 rows of a piece into shared memory (K-major, 128-byte swizzle; zeros for padding
+    // rows), asynchronously
+    auto start_q = [&](const CtItem& n) {
+      constexpr int CH = D / 8, RPI = 32 / CH;
       const int r = n.row0 + w * 128 + m;
-      const bool real = r < n.s.n * p.G;
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                        (real ? q_offset(p, n.s, n.g, r) : 0));
+      const int64_t mine = r < n.s.n * p.G ? q_offset(p, n.s, n.g, r) : -1;
+      const int c = lane % CH;
 #pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) {
-        uint4 v[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = real ? __ldg(src + h * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(qblock + h * kCtHalf + m * 128 + ((c ^ (m & 7)) << 4)) = v[c];
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int row = i * RPI + lane / CH;
+        const int64_t off = __shfl_sync(0xffffffffu, mine, row);
+        cp_async16(qblock_u32 + (c >> 3) * kCtHalf + (sub * 32 + row) * 128 + (((c & 7) ^ (row & 7)) << 4),
+                   reinterpret_cast<const __nv_bfloat16*>(p.q) + (off < 0 ? 0 : off) + c * 8, off >= 0);
       }
+      cp_async_commit();
+    };
+    auto finish_q = [&]() {
+      cp_async_wait<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull[w]);
     };
 
+    CtItem it;
+    int b0 = 0, b1 = 0;
     bool have = next_piece(it, b0, b1), ok = true;
-    if (have) load_q(it);
+    if (have) {
+      start_q(it);
+      finish_q();
+    }
     int t = 0, part = 0;
     while (have && ok) {
       CtItem nx;
       int nb0 = 0, nb1 = 0;
-      const bool have_next = next_piece(nx, nb0, nb1);
+      bool have_next = false;
       const int r = it.row0 + w * 128 + m;
       const bool real = r < it.s.n * p.G;
       // position of the row's token; padding rows see what the last row sees
@@ -376,8 +410,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float m_run = neg_inf(), l = 0.f;
       for (int u = b0; u < b1; ++u, ++t) {
+        if (u == b1 - 1) have_next = next_piece(nx, nb0, nb1);
         if (!warp_wait(&sfull[w], t & 1)) { ok = false; break; }
         tc::fence_after();
+        if (u == b1 - 1 && have_next) start_q(nx);  // the piece's last Q K^T has read its rows
         const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
         // P = 2^(s * scale - mu) against the present reference, as bf16 pairs; only where a row's sum
@@ -466,7 +502,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[w]);
       }
       if (!ok) break;
-      if (have_next) load_q(nx);  // the piece's last Q K^T has read its rows
+      if (have_next) finish_q();
       // ---- epilogue, once the piece's last P V is done
       if (!warp_wait(&pvdone[w], part & 1)) { ok = false; break; }
       ++part;
@@ -486,30 +522,52 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         p.part_ml[rec * kTcRows + w * 128 + m] = make_float2(m_run, l);
       } else {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t off = real ? o_offset(p, it.s, it.g, r) : 0;
+        const int64_t off = real ? o_offset(p, it.s, it.g, r) : -1;
+        // bf16 rows on 16-byte boundaries: four lanes turn their four rows' 64 bytes around, so that a
+        // store covers 64 bytes of a row instead of 16
+        const bool quads = p.o_bf16 && __all_sync(0xffffffffu, !real || ((reinterpret_cast<uintptr_t>(p.o) + off * 2) & 15u) == 0);
+        int64_t quad_off[4];
+        if (quads) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) quad_off[i] = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
+        }
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           __syncwarp();
           tc::ld32(obuf + c * 32, v);
           tc::ld_wait(v);
-          if (real) {
+          if (quads) {
+            uint32_t x[4][4];  // [8 columns][pair]
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              x[e >> 3][(e >> 1) & 3] = pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+            // 4 x 4 transposition of 16-byte blocks over the quad: exchange with lanes ^ 1, then ^ 2
+#pragma unroll
+            for (int s = 1; s <= 2; s <<= 1) {
+              const bool up = (lane & s) != 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i & s) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t give = up ? x[i][e] : x[i | s][e];
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
+                  if (up) x[i][e] = got;
+                  else x[i | s][e] = got;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (quad_off[i] >= 0)
+                *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + quad_off[i] + c * 32 + (lane & 3) * 8) =
+                    make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          } else if (real) {
             if (p.o_bf16) {
               __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off + c * 32;
-              if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 x;
-                  x.x = pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-                  x.y = pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-                  x.z = pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-                  x.w = pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-                  *reinterpret_cast<uint4*>(dst + e) = x;
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) dst[e] = __float2bfloat16_rn(__uint_as_float(v[e]) * inv);
-              }
+              for (int e = 0; e < 32; ++e) dst[e] = __float2bfloat16_rn(__uint_as_float(v[e]) * inv);
             } else {
               float* dst = reinterpret_cast<float*>(p.o) + off + c * 32;
               if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {

@@ -313,9 +313,12 @@ __global__ void __launch_bounds__(32) logprob_join(const __grid_constant__ Logpr
   st = warp_stat(st);
   TopList top;
   const int nk = p.slices * p.K;
+  // the slices' best keys first, then their second best, ...: the K-th value is high early on, and
+  // most of the rest is turned away by one vote
+  const Key* keys = p.part_keys + (int64_t)row * nk;
   for (int i0 = 0; i0 < nk; i0 += 32) {
     const int i = i0 + lane;
-    top.offer(i < nk ? __ldcg(p.part_keys + (int64_t)row * nk + i) : 0, p.K);
+    top.offer(i < nk ? __ldcg(keys + (i % p.slices) * p.K + i / p.slices) : 0, p.K);
   }
   if (state < 0 && lane == 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_TOKEN);
   write_row(p, row, st, top.mine, given, state);

@@ -99,6 +99,7 @@ int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream
   const bool bf16 = kv_dtype == SPEC_BF16;
   p.row_tile = chunk_row_tile(kv_dtype);
   p.unit_keys = bf16 ? specv::kTcKeys : specv::kF32Keys;
+  p.min_units = 2;
   specv::chunk_workspace_carve(ws, &p);
   CUtensorMap tm[2];
   if (bf16) {
@@ -109,8 +110,7 @@ int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream
     // a copy of a packed tile is never issued where T < kTcKeys
     p.use_tma = p.tma_page_keys > 0 && encode_kv(&tm[0], p.k, p) && encode_kv(&tm[1], p.v, p);
   }
-  if (specv::launch_chunk_plan(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (p.k_new && specv::launch_chunk_append(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (specv::launch_chunk_prepare(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
   const cudaError_t e = bf16 ? specv::launch_chunk_tc(p, &tm[0], &tm[1], stream) : specv::launch_chunk_f32(p, stream);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
   return specv::launch_chunk_merge(p, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

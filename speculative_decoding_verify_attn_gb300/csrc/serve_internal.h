@@ -19,15 +19,17 @@ constexpr int kMmaUnit = 128;   // keys per unit of work of the mma.sync kernel 
 constexpr int kMmaDirectKeys = 4 * kMmaUnit;
 constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
 constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
-constexpr int kTmaMinPage = 64; // tokens per page from which the tcgen05 kernel copies pages by TMA
+constexpr int kTmaMinPage = 32; // tokens per page from which the tcgen05 kernel copies pages by TMA
 constexpr int kF32Rows = 32;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 
 // One piece of work of a chunk kernel, for every kv head: the row tile starting at row `row0` of
 // sequence b (row r: token r / G of the chunk, head r % G of the group), key units [u0, u1).
 // slot < 0: the piece is the whole tile and writes o; else its record is slot * Hkv + g.
-struct ChunkItem {
-  int32_t b, row0, u0, u1, slot, pad0, pad1, pad2;
+// The sequence's own numbers (serve_common.cuh) come along, so that a piece costs its reader one trip
+// to memory.
+struct alignas(16) ChunkItem {
+  int32_t b, row0, u0, u1, slot, q0, n, len, lo, pad0, pad1, pad2;
 };
 // A tile whose pieces were split: records slot .. slot + pieces - 1.
 struct ChunkSplit {
@@ -61,6 +63,7 @@ struct ServeAttnParams {
   int grid;               // CTAs of the attention kernel
   int direct;             // mma.sync kernel: a CTA per segment, no records
   int row_tile, unit_keys;  // chunk kernels: rows per tile, keys per unit
+  int min_units;          // chunk kernels: units a piece of a split tile has at least
   int use_tma;            // tcgen05 kernel: the tensor maps are valid
   int tma_page_keys;      // keys one copy brings (min(page_size, kTcKeys); packed: kTcKeys)
   int max_tiles;          // chunk kernels: tiles (per kv head) the plan has room for
@@ -81,9 +84,8 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p);
 void chunk_workspace_carve(void* ws, ServeAttnParams* p);
 
 cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream);
-// plan, [append], attention, merge
-cudaError_t launch_chunk_plan(const ServeAttnParams& p, cudaStream_t stream);
-cudaError_t launch_chunk_append(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
+// plan and append, attention, merge
+cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             cudaStream_t stream);
 cudaError_t launch_chunk_f32(const ServeAttnParams& p, cudaStream_t stream);

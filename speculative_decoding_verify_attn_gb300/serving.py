@@ -77,63 +77,90 @@ def _serve_lib():
 
 
 # ---------------------------------------------------------------------------- helpers
+_torch = None
+
+
+def _t():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    torch = _t()
+    if t.dtype is torch.bfloat16:
         return SPEC_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return SPEC_F32
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def _check(device, **tensors):
-    """All on one CUDA device, with a contiguous innermost dimension."""
-    if device.type != "cuda":
-        raise ValueError("all tensors must be CUDA tensors (host buffers: copy them to the device first)")
+def _check(**tensors) -> int:
+    """All on one CUDA device, with a contiguous innermost dimension; returns the device's index."""
+    index = None
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        at = t.get_device()
+        if at < 0 or not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors (host buffers: copy them to the device first)")
+        if index is None:
+            index = at
+        elif at != index:
+            raise ValueError(f"{name} is on cuda:{at}, not on cuda:{index}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
             raise ValueError(f"{name}: innermost dimension must be contiguous")
+    return index
 
 
-def _int32(shapes, **tensors):
-    import torch
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shapes[name]):
-            raise ValueError(f"{name} must be int32 of shape {shapes[name]}, got {t.dtype} {tuple(t.shape)}")
+def _int32(name, t, *shape):
+    if t is not None and (t.dtype is not _t().int32 or t.shape != shape):
+        raise ValueError(f"{name} must be int32 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _call(name, args, device, workspace, stream):
-    """Sizes the workspace, fills it in and makes the call on the tensors' device."""
-    import torch
-    L = _serve_lib()
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(name, args, device, workspace, stream)
-    need = getattr(L, name + "_workspace")(byref(args))
-    if need == 0:
-        # the call itself says why the sizes are refused
-        raise SpecError(getattr(L, name)(byref(args), None) or SPEC_ERR_INVALID_ARG, name)
-    current = torch.cuda.current_stream(device)
-    if stream is None:
-        stream = current
-    elif not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+_sizes = {}
+
+
+def _call(name, args, sizes, index, workspace, stream):
+    """Sizes the workspace, fills it in and makes the call on the tensors' device.  `sizes` is what the
+    workspace's size depends on: the library is asked once for each."""
+    torch = _t()
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(name, args, sizes, index, workspace, stream)
+    L = _lib or _serve_lib()
+    ref = byref(args)
+    need = _sizes.get((name, sizes))
+    if need is None:
+        need = getattr(L, name + "_workspace")(ref)
+        if need == 0:
+            # the call itself says why the sizes are refused
+            raise SpecError(getattr(L, name)(ref, None) or SPEC_ERR_INVALID_ARG, name)
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[(name, sizes)] = need
+    handle = torch.cuda.current_stream().cuda_stream
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream != current:
-            workspace.record_stream(stream)
+        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        given = need
     else:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {device}")
-        if workspace.numel() * workspace.element_size() < need:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+        given = workspace.numel() * workspace.element_size()
+        if given < need:
             raise ValueError(f"workspace too small: need {need} bytes")
+    if stream is not None:
+        own = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        if own.cuda_stream != handle:
+            # its memory is not handed out again before the other stream has passed this call
+            workspace.record_stream(own)
+        handle = own.cuda_stream
     args.workspace = workspace.data_ptr()
-    args.workspace_bytes = workspace.numel() * workspace.element_size()
-    st = getattr(L, name)(byref(args), stream.cuda_stream)
+    args.workspace_bytes = given
+    st = getattr(L, name)(ref, handle)
     if st != SPEC_OK:
         raise SpecError(st, name)
 
@@ -158,8 +185,9 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
         raise TypeError("k_pages and v_pages must share a dtype")
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
-    _int32({"page_table": (B, cols), "q_start": (B + 1,), "kv_len": (B,)}, page_table=page_table, q_start=q_start,
-           kv_len=kv_len)
+    _int32("page_table", page_table, B, cols)
+    _int32("q_start", q_start, B + 1)
+    _int32("kv_len", kv_len, B)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if k_new is not None:
@@ -194,11 +222,11 @@ def spec_paged_attn(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
     max_q: an upper bound on the chunk lengths.  With k_new, v_new [T, Hkv, D] the call also writes
     them into the new tokens' slots.  window > 0: rows see the last `window` tokens only.  Writes o
     and returns it."""
-    _check(q.device, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, q_start=q_start, kv_len=kv_len,
-           o=o, k_new=k_new, v_new=v_new)
+    index = _check(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, q_start=q_start, kv_len=kv_len,
+                   o=o, k_new=k_new, v_new=v_new)
     a = paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, max_q=max_q, k_new=k_new, v_new=v_new,
                         window=window, scale=scale)
-    _call("spec_paged_attn", a, q.device, workspace, stream)
+    _call("spec_paged_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.max_q, a.kv_dtype), index, workspace, stream)
     return o
 
 
@@ -213,7 +241,7 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
     B = seq_start.shape[0] - 1
-    _int32({"seq_start": (B + 1,)}, seq_start=seq_start)
+    _int32("seq_start", seq_start, B + 1)
     return SpecPrefillArgs(
         B, Hq, k.shape[1], D, T, int(window), _dtype_code(q), _dtype_code(k), _dtype_code(o), scale,
         q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
@@ -234,25 +262,26 @@ def spec_prefill_attn(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     q, o [T, Hq, D]; k, v [T, Hkv, D]; seq_start [B + 1] int32, sequence b being rows seq_start[b] ..
     seq_start[b + 1] - 1.  window > 0: rows see the last `window` tokens only.  Writes o and returns
     it."""
-    _check(q.device, q=q, k=k, v=v, seq_start=seq_start, o=o)
+    index = _check(q=q, k=k, v=v, seq_start=seq_start, o=o)
     a = prefill_attn_args(q, k, v, seq_start, o, window=window, scale=scale)
-    _call("spec_prefill_attn", a, q.device, workspace, stream)
+    _call("spec_prefill_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.kv_dtype), index, workspace, stream)
     return o
 
 
 # ---------------------------------------------------------------------------- log probabilities
 def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None) -> SpecLogprobArgs:
     """Fill SpecLogprobArgs from tensors (no workspace yet)."""
-    import torch
+    torch = _t()
     N, V = logits.shape
     if (tokens is None) != (logprobs is None):
         raise ValueError("tokens and logprobs go together")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
     K = 0 if top_ids is None else top_ids.shape[1]
-    _int32({"tokens": (N,), "top_ids": (N, K)}, tokens=tokens, top_ids=top_ids)
+    _int32("tokens", tokens, N)
+    _int32("top_ids", top_ids, N, K)
     for name, t, shape in (("logprobs", logprobs, (N,)), ("entropy", entropy, (N,)), ("top_logprobs", top_logprobs, (N, K))):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+        if t is not None and (t.dtype is not torch.float32 or t.shape != shape):
             raise ValueError(f"{name} must be float32 of shape {shape}")
     for t in (tokens, logprobs, entropy, top_ids, top_logprobs):
         if t is not None and not t.is_contiguous():
@@ -276,8 +305,8 @@ def spec_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None,
     logits [N, V] fp32 or bf16; tokens [N] int32 and logprobs [N] fp32 (both or neither); entropy [N]
     fp32; top_ids [N, K] int32 and top_logprobs [N, K] fp32 (K <= 32, descending, lower ids first
     among equals).  Outputs not wanted are None.  Writes them and returns logprobs."""
-    _check(logits.device, logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_ids=top_ids,
-           top_logprobs=top_logprobs)
+    index = _check(logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_ids=top_ids,
+                   top_logprobs=top_logprobs)
     a = token_logprobs_args(logits, tokens, logprobs, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs)
-    _call("spec_token_logprobs", a, logits.device, workspace, stream)
+    _call("spec_token_logprobs", a, (a.N, a.V, a.K), index, workspace, stream)
     return logprobs
