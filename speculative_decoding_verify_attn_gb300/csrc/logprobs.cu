@@ -10,9 +10,9 @@
 // Top alternatives: an id's key is (order of its logit, lower id first) as one 64-bit number; each
 // warp keeps its K best keys sorted over its lanes.  A batch of vectors is looked at one by one only
 // if its maximum, which the softmax needs anyway, reaches a floor that the CTA's warps share: the
-// least of the warps' ceil(K / 8)-th best values, at or above which K ids exist.  The first floor comes
+// least of the warps' ceil(K / 4)-th best values, at or above which K ids exist.  The first floor comes
 // from the lanes' maxima of the first batch, before anything is inserted, so a row of n ids costs
-// about K log(n / 8192) insertions in all.
+// about K log(n / 4096) insertions in all.
 //
 // Bound: HBM, one read of the logits.  A row is one CTA when there are enough rows to fill the GPU,
 // else kSliceTarget / N slices whose records a second kernel joins (launched as a programmatic
@@ -26,10 +26,10 @@
 
 namespace specv {
 
-constexpr int kLpWarps = 8;
+constexpr int kLpWarps = 4;
 constexpr int kLpThreads = kLpWarps * 32;
 constexpr int kLpVecs = 4;            // 16-byte vectors per lane and batch
-constexpr int kLpCtasPerSm = 3;
+constexpr int kLpCtasPerSm = 8;
 constexpr int kSliceTarget = 608;     // CTAs wanted (four per SM) before rows are no longer sliced
 constexpr int kMinSlice = 4096;       // elements of a slice at least (one fp32 batch of a CTA)
 
@@ -147,9 +147,9 @@ template <bool BF16, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_stats(const __grid_constant__ LogprobParams p) {
   pdl_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) status_clear_for_launch(p.status);
-  __shared__ Key s_keys[kLpWarps][32];
+  __shared__ Key s_keys[kLpWarps][32], s_top[32];
   __shared__ Stat s_stat[kLpWarps];
-  __shared__ uint32_t s_rank[kLpWarps];  // order of each warp's ceil(K / 8)-th best value (or below it)
+  __shared__ uint32_t s_rank[kLpWarps];  // order of each warp's ceil(K / 4)-th best value (or below it)
   __shared__ uint32_t s_floor;
   constexpr int VN = Vec<BF16>::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -238,24 +238,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_stats(const 
       const uint32_t lim = max(*reinterpret_cast<volatile uint32_t*>(&s_floor), top.thr ? (uint32_t)(top.thr >> 32) + 1u : 0u);
       const float lf = order_value(lim);
       if (__any_sync(0xffffffffu, bm >= lf)) {
-        uint32_t todo = 0;  // bit u * VN + e: element e of vector u of this lane
 #pragma unroll
-        for (int u = 0; u < kLpVecs; ++u)
+        for (int u = 0; u < kLpVecs; ++u) {
+          if (!__any_sync(0xffffffffu, cur[u].max() >= lf)) continue;
+          const int i = base + u * 32 + lane;
+          uint32_t todo = 0;  // this lane's elements that count
 #pragma unroll
-          for (int e = 0; e < VN; ++e) todo |= cur[u].get(e) >= lf ? 1u << (u * VN + e) : 0u;
-#pragma unroll
-        for (int u = 0; u < kLpVecs; ++u)
-          if (base + u * 32 + lane >= v1) todo &= ~(((1u << VN) - 1u) << (u * VN));
-        // few: read again rather than picked out of registers by a run-time index
-        while (__any_sync(0xffffffffu, todo != 0)) {
-          Key k = 0;
-          if (todo) {
-            const int j = __ffs(todo) - 1;
-            const int id = head + (base + j / VN * 32 + lane) * VN + j % VN;
-            k = make_key(load_elem<BF16>(row_ptr, id), (uint32_t)id);
-            todo &= todo - 1;
+          for (int e = 0; e < VN; ++e) todo |= cur[u].get(e) >= lf ? 1u << e : 0u;
+          if (i >= v1) todo = 0;
+          while (__any_sync(0xffffffffu, todo != 0)) {
+            Key k = 0;
+            if (todo) {
+              const int e = __ffs(todo) - 1, word = BF16 ? e >> 1 : e;
+              const uint32_t lo = (word & 1) ? cur[u].v.y : cur[u].v.x, hi = (word & 1) ? cur[u].v.w : cur[u].v.z;
+              const uint32_t w = (word & 2) ? hi : lo;
+              const float x = __uint_as_float(!BF16 ? w : (e & 1) ? (w & 0xffff0000u) : (w << 16));
+              k = make_key(x, (uint32_t)(head + i * VN + e));
+              todo &= todo - 1;
+            }
+            top.offer(k, p.K);
           }
-          top.offer(k, p.K);
         }
         // a better floor
         const uint32_t o = (uint32_t)(__shfl_sync(0xffffffffu, top.mine, rank - 1) >> 32);
@@ -277,51 +279,102 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_stats(const 
 
   st = warp_stat(st);
   if (lane == 0) s_stat[warp] = st;
-  if (TOP) s_keys[warp][lane] = top.mine;
+  if (TOP) {
+    // the warps' lists as one: a key's place is the number of greater keys; those below the floor
+    // have no place among the K best
+    s_keys[warp][lane] = lane < p.K && (uint32_t)(top.mine >> 32) >= *reinterpret_cast<volatile uint32_t*>(&s_floor) ? top.mine : 0;
+    if (warp == 0) s_top[lane] = 0;
+  }
   __syncthreads();
+  if (TOP) {
+    const Key mine = s_keys[warp][lane];
+    // a list is sorted, so its first zero ends it
+    int above = 0;
+    for (int w = 0; w < kLpWarps; ++w)
+      for (int i = 0; i < p.K; ++i) {
+        const Key k = s_keys[w][i];
+        if (k == 0) break;
+        above += k > mine;
+      }
+    if (mine != 0 && above < p.K) s_top[above] = mine;
+    __syncthreads();
+  }
   if (warp != 0) return;
   st = s_stat[0];
 #pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) {
-    st = stat_join(st, s_stat[w]);
-    if (TOP) top.offer(lane < p.K ? s_keys[w][lane] : 0, p.K);
-  }
+  for (int w = 1; w < kLpWarps; ++w) st = stat_join(st, s_stat[w]);
+  const Key best = TOP ? s_top[lane] : 0;
   if (p.slices == 1) {
     int state;
     const float given = given_logit<BF16>(p, row_ptr, row, state);
     if (state < 0 && lane == 0) status_report(p.status, (uint32_t)SPEC_STATUS_BAD_TOKEN);
-    write_row(p, row, st, top.mine, given, state);
+    write_row(p, row, st, best, given, state);
   } else {
     if (lane == 0) p.part_stat[blockIdx.x] = make_float4(st.m, st.s, st.w, 0.f);
-    if (TOP && lane < p.K) p.part_keys[(int64_t)blockIdx.x * p.K + lane] = top.mine;
+    if (TOP && lane < p.K) p.part_keys[(int64_t)blockIdx.x * p.K + lane] = best;
   }
 }
 
-// Joins the slices of a row (one warp per row).
+// Joins the slices of a row.  If there are more than K slices, the K-th of their best keys is a floor;
+// at most K slices reach it, so at most K * K keys remain, whose places are counted out.
+constexpr int kJoinThreads = 256;
 template <bool BF16>
-__global__ void __launch_bounds__(32) logprob_join(const __grid_constant__ LogprobParams p) {
-  const int row = blockIdx.x, lane = threadIdx.x;
+__global__ void __launch_bounds__(kJoinThreads) logprob_join(const __grid_constant__ LogprobParams p) {
+  __shared__ Key s_best[kSliceTarget];
+  __shared__ Key s_cand[32 * 32];
+  __shared__ Key s_top[32];
+  __shared__ Key s_floor;
+  __shared__ int s_n;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const char* row_ptr = reinterpret_cast<const char*>(p.logits) + (int64_t)row * p.stride * (BF16 ? 2 : 4);
-  int state;
-  const float given = given_logit<BF16>(p, row_ptr, row, state);
+  int state = 0;
+  float given = 0.f;
+  if (tid < 32) {
+    given = given_logit<BF16>(p, row_ptr, row, state);
+    s_top[lane] = 0;
+    if (tid == 0) {
+      s_floor = 1;
+      s_n = 0;
+    }
+  }
   pdl_wait();
   Stat st{neg_inf(), 0.f, 0.f};
-  for (int i = lane; i < p.slices; i += 32) {
-    const float4 v = __ldcg(p.part_stat + (int64_t)row * p.slices + i);
-    st = stat_join(st, Stat{v.x, v.y, v.z});
+  if (tid < 32) {
+    for (int i = lane; i < p.slices; i += 32) {
+      const float4 v = __ldcg(p.part_stat + (int64_t)row * p.slices + i);
+      st = stat_join(st, Stat{v.x, v.y, v.z});
+    }
+    st = warp_stat(st);
   }
-  st = warp_stat(st);
-  TopList top;
-  const int nk = p.slices * p.K;
-  // the slices' best keys first, then their second best, ...: the K-th value is high early on, and
-  // most of the rest is turned away by one vote
-  const Key* keys = p.part_keys + (int64_t)row * nk;
-  for (int i0 = 0; i0 < nk; i0 += 32) {
-    const int i = i0 + lane;
-    top.offer(i < nk ? __ldcg(keys + (i % p.slices) * p.K + i / p.slices) : 0, p.K);
+  if (p.K > 0) {
+    const Key* keys = p.part_keys + (int64_t)row * p.slices * p.K;
+    if (p.slices > p.K) {
+      for (int i = tid; i < p.slices; i += kJoinThreads) s_best[i] = __ldcg(keys + i * p.K);
+      __syncthreads();
+      for (int i = tid; i < p.slices; i += kJoinThreads) {
+        const Key mine = s_best[i];
+        int above = 0;
+        for (int j = 0; j < p.slices; ++j) above += s_best[j] > mine;
+        if (mine != 0 && above == p.K - 1) s_floor = mine;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.slices * p.K; i += kJoinThreads) {
+      const Key k = __ldcg(keys + i);
+      if (k >= s_floor) s_cand[atomicAdd(&s_n, 1)] = k;
+    }
+    __syncthreads();
+    for (int i = tid; i < s_n; i += kJoinThreads) {
+      const Key mine = s_cand[i];
+      int above = 0;
+      for (int j = 0; j < s_n; ++j) above += s_cand[j] > mine;
+      if (above < p.K) s_top[above] = mine;
+    }
+    __syncthreads();
   }
+  if (tid >= 32) return;
   if (state < 0 && lane == 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_TOKEN);
-  write_row(p, row, st, top.mine, given, state);
+  write_row(p, row, st, s_top[lane], given, state);
 }
 
 int logprob_slices(int N, int V) {
@@ -356,8 +409,8 @@ cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t stream) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.slices == 1) return e;
-  return p.bf16 ? launch_dependent(logprob_join<true>, dim3(p.N), dim3(32), 0, stream, 0u, p)
-                : launch_dependent(logprob_join<false>, dim3(p.N), dim3(32), 0, stream, 0u, p);
+  return p.bf16 ? launch_dependent(logprob_join<true>, dim3(p.N), dim3(kJoinThreads), 0, stream, 0u, p)
+                : launch_dependent(logprob_join<false>, dim3(p.N), dim3(kJoinThreads), 0, stream, 0u, p);
 }
 
 }  // namespace specv

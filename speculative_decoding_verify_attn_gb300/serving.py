@@ -98,27 +98,28 @@ def _dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def _check(**tensors) -> int:
-    """All on one CUDA device, with a contiguous innermost dimension; returns the device's index."""
-    index = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        at = t.get_device()
-        if at < 0 or not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors (host buffers: copy them to the device first)")
-        if index is None:
-            index = at
-        elif at != index:
-            raise ValueError(f"{name} is on cuda:{at}, not on cuda:{index}")
-        if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-            raise ValueError(f"{name}: innermost dimension must be contiguous")
+def _check(tensors) -> int:
+    """The index of the one CUDA device all tensors (None: not given) are on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or index < 0):
+            raise ValueError("all tensors must be CUDA tensors on one device (host buffers: copy them there first): "
+                             + ", ".join(str(x.device) for x in tensors if x is not None))
     return index
 
 
+def _rows(name, t):
+    """The strides of a tensor whose innermost dimension has to be contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: innermost dimension must be contiguous")
+    return st
+
+
 def _int32(name, t, *shape):
-    if t is not None and (t.dtype is not _t().int32 or t.shape != shape):
+    if t.dtype is not _t().int32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _rows(name, t)
 
 
 _sizes = {}
@@ -142,7 +143,7 @@ def _call(name, args, sizes, index, workspace, stream):
         if len(_sizes) > 4096:
             _sizes.clear()
         _sizes[(name, sizes)] = need
-    handle = torch.cuda.current_stream().cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
         given = need
@@ -177,31 +178,35 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
                     window: int = 0, scale: float = 0.0) -> SpecPagedArgs:
     """Fill SpecPagedArgs from tensors (no workspace yet)."""
     T, Hq, D = q.shape
-    pages, Hkv, page_size, D2 = k_pages.shape
+    shape = k_pages.shape
+    pages, Hkv, page_size, D2 = shape
     B, cols = page_table.shape
-    if D2 != D or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+    qs, ks, os_ = _rows("q", q), _rows("k_pages", k_pages), _rows("o", o)
+    if D2 != D or v_pages.shape != shape or v_pages.stride() != ks:
         raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with q's D and equal strides")
-    if v_pages.dtype != k_pages.dtype:
+    if v_pages.dtype is not k_pages.dtype:
         raise TypeError("k_pages and v_pages must share a dtype")
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
-    _int32("page_table", page_table, B, cols)
+    ts = _int32("page_table", page_table, B, cols)
     _int32("q_start", q_start, B + 1)
     _int32("kv_len", kv_len, B)
-    if (k_new is None) != (v_new is None):
-        raise ValueError("k_new and v_new go together")
-    if k_new is not None:
-        if tuple(k_new.shape) != (T, Hkv, D) or v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
+    kn = vn = None
+    ns = (0, 0)
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise ValueError("k_new and v_new go together")
+        ns = _rows("k_new", k_new)
+        if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or v_new.stride() != ns:
             raise ValueError("k_new, v_new must be [T, Hkv, D] with equal strides")
-        if k_new.dtype != k_pages.dtype or v_new.dtype != k_pages.dtype:
+        if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
             raise TypeError("k_new, v_new must have the cache's dtype")
+        kn, vn = k_new.data_ptr(), v_new.data_ptr()
     return SpecPagedArgs(
-        B, Hq, Hkv, D, T, int(max_q), _dtype_code(q), _dtype_code(k_pages), _dtype_code(o), page_size, pages, cols,
-        int(window), scale, q.data_ptr(), q.stride(0), q.stride(1), k_pages.data_ptr(), v_pages.data_ptr(),
-        k_pages.stride(0), k_pages.stride(1), k_pages.stride(2), page_table.data_ptr(), page_table.stride(0),
-        q_start.data_ptr(), kv_len.data_ptr(), None if k_new is None else k_new.data_ptr(),
-        None if v_new is None else v_new.data_ptr(), 0 if k_new is None else k_new.stride(0),
-        0 if k_new is None else k_new.stride(1), o.data_ptr(), o.stride(0), o.stride(1), None, 0)
+        B, Hq, Hkv, D, T, max_q, _dtype_code(q), _dtype_code(k_pages), _dtype_code(o), page_size, pages, cols, window,
+        scale, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2],
+        page_table.data_ptr(), ts[0], q_start.data_ptr(), kv_len.data_ptr(), kn, vn, ns[0], ns[1], o.data_ptr(),
+        os_[0], os_[1], None, 0)
 
 
 def spec_paged_attn_workspace(q, k_pages, page_table, o, *, max_q) -> int:
@@ -222,8 +227,7 @@ def spec_paged_attn(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
     max_q: an upper bound on the chunk lengths.  With k_new, v_new [T, Hkv, D] the call also writes
     them into the new tokens' slots.  window > 0: rows see the last `window` tokens only.  Writes o
     and returns it."""
-    index = _check(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, q_start=q_start, kv_len=kv_len,
-                   o=o, k_new=k_new, v_new=v_new)
+    index = _check((q, k_pages, v_pages, page_table, q_start, kv_len, o, k_new, v_new))
     a = paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, max_q=max_q, k_new=k_new, v_new=v_new,
                         window=window, scale=scale)
     _call("spec_paged_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.max_q, a.kv_dtype), index, workspace, stream)
@@ -234,18 +238,18 @@ def spec_paged_attn(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
 def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 0.0) -> SpecPrefillArgs:
     """Fill SpecPrefillArgs from tensors (no workspace yet)."""
     T, Hq, D = q.shape
-    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or v.stride() != k.stride():
+    qs, ks, os_ = _rows("q", q), _rows("k", k), _rows("o", o)
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or v.stride() != ks:
         raise ValueError("k, v must be [T, Hkv, D] with equal strides")
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise TypeError("k and v must share a dtype")
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
     B = seq_start.shape[0] - 1
     _int32("seq_start", seq_start, B + 1)
     return SpecPrefillArgs(
-        B, Hq, k.shape[1], D, T, int(window), _dtype_code(q), _dtype_code(k), _dtype_code(o), scale,
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-        seq_start.data_ptr(), o.data_ptr(), o.stride(0), o.stride(1), None, 0)
+        B, Hq, k.shape[1], D, T, window, _dtype_code(q), _dtype_code(k), _dtype_code(o), scale, q.data_ptr(), qs[0],
+        qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(), o.data_ptr(), os_[0], os_[1], None, 0)
 
 
 def spec_prefill_attn_workspace(q, k, seq_start, o) -> int:
@@ -262,7 +266,7 @@ def spec_prefill_attn(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     q, o [T, Hq, D]; k, v [T, Hkv, D]; seq_start [B + 1] int32, sequence b being rows seq_start[b] ..
     seq_start[b + 1] - 1.  window > 0: rows see the last `window` tokens only.  Writes o and returns
     it."""
-    index = _check(q=q, k=k, v=v, seq_start=seq_start, o=o)
+    index = _check((q, k, v, seq_start, o))
     a = prefill_attn_args(q, k, v, seq_start, o, window=window, scale=scale)
     _call("spec_prefill_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.kv_dtype), index, workspace, stream)
     return o
@@ -278,8 +282,10 @@ def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None,
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
     K = 0 if top_ids is None else top_ids.shape[1]
-    _int32("tokens", tokens, N)
-    _int32("top_ids", top_ids, N, K)
+    if tokens is not None:
+        _int32("tokens", tokens, N)
+    if top_ids is not None:
+        _int32("top_ids", top_ids, N, K)
     for name, t, shape in (("logprobs", logprobs, (N,)), ("entropy", entropy, (N,)), ("top_logprobs", top_logprobs, (N, K))):
         if t is not None and (t.dtype is not torch.float32 or t.shape != shape):
             raise ValueError(f"{name} must be float32 of shape {shape}")
@@ -288,8 +294,8 @@ def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None,
             raise ValueError("tokens and the outputs must be contiguous")
     ptr = [None if t is None or t.numel() == 0 else t.data_ptr() for t in (tokens, logprobs, entropy, top_ids, top_logprobs)]
     # the stride of a single row may be anything
-    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), logits.stride(0) if N > 1 else V, *ptr,
-                           None, 0)
+    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0] if N > 1 else V,
+                           *ptr, None, 0)
 
 
 def spec_token_logprobs_workspace(logits, K: int = 0) -> int:
@@ -305,8 +311,7 @@ def spec_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None,
     logits [N, V] fp32 or bf16; tokens [N] int32 and logprobs [N] fp32 (both or neither); entropy [N]
     fp32; top_ids [N, K] int32 and top_logprobs [N, K] fp32 (K <= 32, descending, lower ids first
     among equals).  Outputs not wanted are None.  Writes them and returns logprobs."""
-    index = _check(logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_ids=top_ids,
-                   top_logprobs=top_logprobs)
+    index = _check((logits, tokens, logprobs, entropy, top_ids, top_logprobs))
     a = token_logprobs_args(logits, tokens, logprobs, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs)
     _call("spec_token_logprobs", a, (a.N, a.V, a.K), index, workspace, stream)
     return logprobs
