@@ -37,16 +37,13 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
   const float* k = reinterpret_cast<const float*>(p.k);
   const float* v = reinterpret_cast<const float*>(p.v);
   pdl_wait();  // the plan, and appended rows
-  const int n_items = __ldcg(&p.plan->n_items) * p.Hkv;
-  for (int round = 0;; ++round) {
-    const int idx = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (round * (int)gridDim.x >= n_items) break;
-    if (idx >= n_items) continue;
-    const int g = idx % p.Hkv;
-    const int4* src = reinterpret_cast<const int4*>(p.items + idx / p.Hkv);
-    const int4 w0 = __ldcg(src), w1 = __ldcg(src + 1), w2 = __ldcg(src + 2);
-    const int b = w0.x, row0 = w0.y, u0 = w0.z, u1 = w0.w, slot = w1.x;
-    const SeqInfo s{w1.y, w1.z, w1.w, w2.x, 0u};
+  PieceList list;
+  list.init(p);
+  for (int round = 0; round < list.rounds; ++round) {
+    const PieceItem it = piece_item(list.fetch(p, round));
+    if (it.u0 >= it.u1) continue;
+    const int b = it.b, g = it.g, row0 = it.row0, u0 = it.u0, u1 = it.u1, slot = it.slot;
+    const SeqInfo s = it.s;
     const int rows = min(kF32Rows, s.n * p.G - row0);
     __syncthreads();
     for (int i = tid; i < kF32Rows * C4; i += kF32Threads) {
@@ -147,7 +144,7 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
     for (int r = 0; r < 2; ++r) {
       const int mrow = 2 * ty + r;
       if (slot >= 0) {
-        const int64_t rec = (int64_t)slot * p.Hkv + g;
+        const int64_t rec = slot;
         if (tx == 0) p.part_ml[rec * kF32Rows + mrow] = make_float2(m[r], l[r]);
         float* dst = p.part_o + rec * D * kF32Rows + mrow;
 #pragma unroll

@@ -56,38 +56,8 @@ struct Ct {
 __device__ __forceinline__ uint32_t ct_col_s(int w) { return 256u * w; }
 __device__ __forceinline__ uint32_t ct_col_o(int w) { return 256u * w + 128u; }
 
-struct CtItem {
-  int b, g, row0, u0, u1, slot;
-  SeqInfo s;
-};
-// The round's piece of this CTA (pieces sorted by size: forth and back over the CTAs), as it lies in
-// memory (u0 == u1: none).  Readers fetch a round ahead.
-struct CtRaw {
-  int4 a, b;
-  int lo, g;
-};
-__device__ __forceinline__ CtRaw ct_fetch(const ServeAttnParams& p, int n_items, int round) {
-  const int grid = gridDim.x, cta = blockIdx.x;
-  const int64_t idx = (int64_t)round * grid + ((round & 1) ? grid - 1 - cta : cta);
-  CtRaw r;
-  r.a = r.b = make_int4(0, 0, 0, 0);
-  r.lo = r.g = 0;
-  if (idx < n_items) {
-    const int4* src = reinterpret_cast<const int4*>(p.items + idx / p.Hkv);
-    r.a = __ldcg(src);
-    r.b = __ldcg(src + 1);
-    r.lo = __ldcg(reinterpret_cast<const int*>(src + 2));
-    r.g = (int)(idx % p.Hkv);
-  }
-  return r;
-}
-__device__ __forceinline__ CtItem ct_item(const CtRaw& r) {
-  return CtItem{r.a.x, r.g, r.a.y, r.a.z, r.a.w, r.b.x, SeqInfo{r.b.y, r.b.z, r.b.w, r.lo, 0u}};
-}
-__device__ __forceinline__ int ct_rounds(int n_items) { return (n_items + (int)gridDim.x - 1) / (int)gridDim.x; }
-
 // Units of the piece that block w's rows see: [b0, b1), empty for a block without rows.
-__device__ __forceinline__ void ct_block_units(const ServeAttnParams& p, const CtItem& it, int w, int& b0, int& b1) {
+__device__ __forceinline__ void ct_block_units(const ServeAttnParams& p, const PieceItem& it, int w, int& b0, int& b1) {
   const int rows = it.s.n * p.G, r0 = it.row0 + w * 128;
   b0 = b1 = it.u0;
   if (r0 >= rows) return;
@@ -137,8 +107,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   tc::fence_after();
   const uint32_t tmem = tmem_base;
   pdl_wait();  // the plan, and appended rows
-  const int n_items = __ldcg(&p.plan->n_items) * p.Hkv;
-  const int rounds = ct_rounds(n_items);
+  PieceList list;
+  list.init(p);
+  const int rounds = list.rounds;
 
   auto fail = [&]() {
     s_abort = 1;
@@ -163,10 +134,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[done % NS]);
     };
-    CtRaw ahead = ct_fetch(p, n_items, 0);
+    PieceRaw ahead = list.fetch(p, 0);
     for (int round = 0; ok && round < rounds; ++round) {
-      const CtItem it = ct_item(ahead);
-      ahead = ct_fetch(p, n_items, round + 1);
+      const PieceItem it = piece_item(ahead);
+      ahead = list.fetch(p, round + 1);
       for (int u = it.u0; ok && u < it.u1; ++u) {
         const int key0 = u * kTcKeys;
         // rows of the tile: offsets of this lane's two of the warp's 64 keys, -1 where zeros go
@@ -285,10 +256,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tc::commit(&sfull[w]);
       };
-      CtRaw ahead = ct_fetch(p, n_items, 0);
+      PieceRaw ahead = list.fetch(p, 0);
       for (int round = 0; ok && round < rounds; ++round) {
-        const CtItem it = ct_item(ahead);
-        ahead = ct_fetch(p, n_items, round + 1);
+        const PieceItem it = piece_item(ahead);
+        ahead = list.fetch(p, round + 1);
         if (it.u0 >= it.u1) continue;
         int b0[2], b1[2];
         ct_block_units(p, it, 0, b0[0], b1[0]);
@@ -356,21 +327,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     };
     // the next piece in which this block has tiles; pieces without leave an empty record
     int round = 0;
-    CtRaw ahead = ct_fetch(p, n_items, 0);
-    auto next_piece = [&](CtItem& n, int& nb0, int& nb1) -> bool {
+    PieceRaw ahead = list.fetch(p, 0);
+    auto next_piece = [&](PieceItem& n, int& nb0, int& nb1) -> bool {
       while (round < rounds) {
-        n = ct_item(ahead);
-        ahead = ct_fetch(p, n_items, ++round);
+        n = piece_item(ahead);
+        ahead = list.fetch(p, ++round);
         ct_block_units(p, n, w, nb0, nb1);
         if (nb1 > nb0) return true;
-        if (n.slot >= 0)
-          p.part_ml[((int64_t)n.slot * p.Hkv + n.g) * kTcRows + w * 128 + m] = make_float2(neg_inf(), 0.f);
+        if (n.slot >= 0) p.part_ml[(int64_t)n.slot * kTcRows + w * 128 + m] = make_float2(neg_inf(), 0.f);
       }
       return false;
     };
     // the warp's 32 rows of a piece into shared memory (K-major, 128-byte swizzle; zeros for padding
     // rows), asynchronously
-    auto start_q = [&](const CtItem& n) {
+    auto start_q = [&](const PieceItem& n) {
       constexpr int CH = D / 8, RPI = 32 / CH;
       const int r = n.row0 + w * 128 + m;
       const int64_t mine = r < n.s.n * p.G ? q_offset(p, n.s, n.g, r) : -1;
@@ -391,7 +361,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (lane == 0) mbar_arrive(&qfull[w]);
     };
 
-    CtItem it;
+    PieceItem it;
     int b0 = 0, b1 = 0;
     bool have = next_piece(it, b0, b1), ok = true;
     if (have) {
@@ -400,9 +370,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
     int t = 0, part = 0;
     while (have && ok) {
-      CtItem nx;
+      PieceItem nx;
       int nb0 = 0, nb1 = 0;
-      bool have_next = false;
+      bool have_next = false, looked = false;
       const int r = it.row0 + w * 128 + m;
       const bool real = r < it.s.n * p.G;
       // position of the row's token; padding rows see what the last row sees
@@ -410,7 +380,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float m_run = neg_inf(), l = 0.f;
       for (int u = b0; u < b1; ++u, ++t) {
-        if (u == b1 - 1) have_next = next_piece(nx, nb0, nb1);
+        if (u == b1 - 1 && !looked) have_next = next_piece(nx, nb0, nb1);
         if (!warp_wait(&sfull[w], t & 1)) { ok = false; break; }
         tc::fence_after();
         if (u == b1 - 1 && have_next) start_q(nx);  // the piece's last Q K^T has read its rows
@@ -434,9 +404,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           tc::ld_wait(s3);
           if (edge) {
             auto hide = [&](uint32_t(&v)[32], int c0) {
+              const int h = hi - c0, l = lo - c0;  // visible [l, h]
+              const uint32_t vis = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) & (l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c0 + e > hi || c0 + e < lo) v[e] = 0xff800000u;
+              for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xff800000u;
             };
             hide(s0, 0);
             hide(s1, 32);
@@ -500,18 +471,30 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[w]);
+        if (!looked && u + 1 < b1) {  // while this tile's products run
+          have_next = next_piece(nx, nb0, nb1);
+          looked = true;
+        }
       }
       if (!ok) break;
       if (have_next) finish_q();
-      // ---- epilogue, once the piece's last P V is done
+      // ---- epilogue, once the piece's last P V is done; meanwhile where the row goes.
+      // bf16 rows on 16-byte boundaries: four lanes turn their four rows' 64 bytes around, so that a
+      // store covers 64 bytes of a row instead of 16
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t off = real ? o_offset(p, it.s, it.g, r) : -1;
+      const bool quads = p.o_bf16 && __all_sync(0xffffffffu, !real || ((reinterpret_cast<uintptr_t>(p.o) + off * 2) & 15u) == 0);
+      int64_t quad_off[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) quad_off[i] = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
       if (!warp_wait(&pvdone[w], part & 1)) { ok = false; break; }
       ++part;
       tc::fence_after();
       if (it.slot >= 0) {
-        const int64_t rec = (int64_t)it.slot * p.Hkv + it.g;
+        const int64_t rec = it.slot;
         float* dst = p.part_o + rec * D * kTcRows + w * 128 + m;
         uint32_t v[32];
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           __syncwarp();
           tc::ld32(obuf + c * 32, v);
@@ -521,18 +504,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         p.part_ml[rec * kTcRows + w * 128 + m] = make_float2(m_run, l);
       } else {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t off = real ? o_offset(p, it.s, it.g, r) : -1;
-        // bf16 rows on 16-byte boundaries: four lanes turn their four rows' 64 bytes around, so that a
-        // store covers 64 bytes of a row instead of 16
-        const bool quads = p.o_bf16 && __all_sync(0xffffffffu, !real || ((reinterpret_cast<uintptr_t>(p.o) + off * 2) & 15u) == 0);
-        int64_t quad_off[4];
-        if (quads) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) quad_off[i] = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
-        }
+        // not unrolled: this code runs once per piece and its instructions come from far; 32 columns'
+        // worth of them, fetched once, halve the time of four times as many
         uint32_t v[32];
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           __syncwarp();
           tc::ld32(obuf + c * 32, v);

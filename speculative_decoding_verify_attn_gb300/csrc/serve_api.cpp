@@ -141,7 +141,7 @@ size_t spec_paged_attn_workspace(const spec_paged_args* a) {
   const int G = a->Hq / a->Hkv;
   return use_mma(a->kv_dtype, paged_shape(a).max_q, G)
              ? specv::mma_workspace_bytes(a->D)
-             : specv::chunk_workspace_bytes(a->T, G, a->B, a->Hkv, a->D, chunk_row_tile(a->kv_dtype));
+             : specv::chunk_workspace_bytes(a->T, G, a->B, a->D, chunk_row_tile(a->kv_dtype));
 }
 
 int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
@@ -196,7 +196,7 @@ static Shape prefill_shape(const spec_prefill_args* a) {
 
 size_t spec_prefill_attn_workspace(const spec_prefill_args* a) {
   if (!a || check_shape(prefill_shape(a)) != SPEC_OK) return 0;
-  return specv::chunk_workspace_bytes(a->T, a->Hq / a->Hkv, a->B, a->Hkv, a->D, chunk_row_tile(a->kv_dtype));
+  return specv::chunk_workspace_bytes(a->T, a->Hq / a->Hkv, a->B, a->D, chunk_row_tile(a->kv_dtype));
 }
 
 int spec_prefill_attn(const spec_prefill_args* a, spec_stream_t stream) {

@@ -72,4 +72,51 @@ __device__ __forceinline__ int64_t o_offset(const ServeAttnParams& p, const SeqI
   return (int64_t)(s.q0 + r / p.G) * p.o_st + (int64_t)(g * p.G + r % p.G) * p.o_sh;
 }
 
+// ------------------------------------------------------------------ pieces of the chunk kernels
+struct PieceItem {
+  int b, g, row0, u0, u1, slot;
+  SeqInfo s;
+};
+// A piece as it lies in memory (u0 == u1: none).  Readers fetch a piece ahead.
+struct PieceRaw {
+  int4 a, b, c;
+};
+// The pieces of a CTA: first its share of the cut tiles, then small tiles (sorted by size, dealt forth
+// and back over the CTAs from small_first on).
+struct PieceList {
+  int n_big, n_small, first, ctas, rounds;
+  __device__ __forceinline__ void init(const ServeAttnParams& p) {
+    const int4 h = __ldcg(reinterpret_cast<const int4*>(p.plan));
+    n_big = (int)blockIdx.x < h.z ? __ldcg(p.big_count + blockIdx.x) : 0;
+    n_small = h.x * p.Hkv;
+    first = h.w;
+    ctas = (int)gridDim.x - first;
+    rounds = n_big + ((int)blockIdx.x >= first ? (n_small + ctas - 1) / ctas : 0);
+  }
+  __device__ __forceinline__ PieceRaw fetch(const ServeAttnParams& p, int round) const {
+    PieceRaw r;
+    r.a = r.b = r.c = make_int4(0, 0, 0, 0);
+    if (round < n_big) {
+      const int4* src = reinterpret_cast<const int4*>(p.big + blockIdx.x * kBigPieces + round);
+      r.a = __ldcg(src);
+      r.b = __ldcg(src + 1);
+      r.c = __ldcg(src + 2);
+    } else if (round < rounds) {
+      const int k = round - n_big, at = (int)blockIdx.x - first;
+      const int64_t idx = (int64_t)k * ctas + ((k & 1) ? ctas - 1 - at : at);
+      if (idx < n_small) {
+        const int4* src = reinterpret_cast<const int4*>(p.items + idx / p.Hkv);
+        r.a = __ldcg(src);
+        r.b = __ldcg(src + 1);
+        r.c.x = __ldcg(reinterpret_cast<const int*>(src + 2));
+        r.c.y = (int)(idx % p.Hkv);
+      }
+    }
+    return r;
+  }
+};
+__device__ __forceinline__ PieceItem piece_item(const PieceRaw& r) {
+  return PieceItem{r.a.x, r.c.y, r.a.y, r.a.z, r.a.w, r.b.x, SeqInfo{r.b.y, r.b.z, r.b.w, r.c.x, 0u}};
+}
+
 }  // namespace specv

@@ -23,22 +23,25 @@ constexpr int kTmaMinPage = 32; // tokens per page from which the tcgen05 kernel
 constexpr int kF32Rows = 32;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 
-// One piece of work of a chunk kernel, for every kv head: the row tile starting at row `row0` of
-// sequence b (row r: token r / G of the chunk, head r % G of the group), key units [u0, u1).
-// slot < 0: the piece is the whole tile and writes o; else its record is slot * Hkv + g.
-// The sequence's own numbers (serve_common.cuh) come along, so that a piece costs its reader one trip
-// to memory.
+// One piece of work of a chunk kernel: the row tile starting at row `row0` of sequence b (row r: token
+// r / G of the chunk, head r % G of the group) of kv head g (small tiles: of every kv head), key units
+// [u0, u1).  slot < 0: the piece is the whole tile and writes o; else its record.  The sequence's own
+// numbers (serve_common.cuh) come along, so that a piece costs its reader one trip to memory.
 struct alignas(16) ChunkItem {
-  int32_t b, row0, u0, u1, slot, q0, n, len, lo, pad0, pad1, pad2;
+  int32_t b, row0, u0, u1, slot, q0, n, len, lo, g, pad0, pad1;
 };
-// A tile whose pieces were split: records slot .. slot + pieces - 1.
-struct ChunkSplit {
-  int32_t b, row0, slot, pieces;
+// A tile cut over CTAs c0 .. c1: its first record is 2 c0 + first, the others 2 c.
+struct alignas(16) ChunkSplit {
+  int32_t b, row0, g, c0, c1, first, pad0, pad1;
 };
-// Head of the plan in the workspace, after the status block.
+// Head of the plan in the workspace, after the status block (see chunk_plan.cu).
 struct ChunkPlan {
-  int32_t n_items, n_splits, pad0, pad1;
+  int32_t n_small, n_splits, big_ctas, small_first;
 };
+// Tiles of more than a quarter of a CTA's share are cut; such a share holds eight pieces at most.
+constexpr int kBigFraction = 4;
+constexpr int kBigPieces = 8;
+constexpr int kMaxBig = kBigFraction * kServeMaxGrid;
 
 struct ServeAttnParams {
   int B, Hq, Hkv, G, D, T, max_q, window;
@@ -63,23 +66,25 @@ struct ServeAttnParams {
   int grid;               // CTAs of the attention kernel
   int direct;             // mma.sync kernel: a CTA per segment, no records
   int row_tile, unit_keys;  // chunk kernels: rows per tile, keys per unit
-  int min_units;          // chunk kernels: units a piece of a split tile has at least
+  int min_units;          // chunk kernels: units a CTA's share of cut tiles has at least
   int use_tma;            // tcgen05 kernel: the tensor maps are valid
   int tma_page_keys;      // keys one copy brings (min(page_size, kTcKeys); packed: kTcKeys)
   int max_tiles;          // chunk kernels: tiles (per kv head) the plan has room for
   uint32_t* status;
   ChunkPlan* plan;
-  ChunkItem* items;
-  ChunkSplit* splits;
-  float2* part_ml;        // chunk kernels [slot * Hkv + g][row_tile]; mma: [2 * cta + s][kMmaMaxRows]
-  float* part_o;          // chunk kernels [slot * Hkv + g][D][row_tile]; mma: [..][kMmaMaxRows][D]
+  int32_t* big_count;     // [kServeMaxGrid]: pieces of cut tiles a CTA has
+  ChunkItem* big;         // [kServeMaxGrid][kBigPieces]
+  ChunkItem* items;       // small tiles, largest first
+  ChunkSplit* splits;     // [kServeMaxGrid]
+  float2* part_ml;        // chunk kernels [2 * cta + s][row_tile]; mma: [2 * cta + s][kMmaMaxRows]
+  float* part_o;          // chunk kernels [2 * cta + s][D][row_tile]; mma: [..][kMmaMaxRows][D]
 };
 
 // Upper bounds on what the plan can hold.
 inline int64_t chunk_max_tiles(int64_t T, int G, int B, int row_tile) { return T * G / row_tile + B; }
 
 size_t mma_workspace_bytes(int D);
-size_t chunk_workspace_bytes(int64_t T, int G, int B, int Hkv, int D, int row_tile);
+size_t chunk_workspace_bytes(int64_t T, int G, int B, int D, int row_tile);
 void mma_workspace_carve(void* ws, ServeAttnParams* p);
 void chunk_workspace_carve(void* ws, ServeAttnParams* p);
 
