@@ -4,7 +4,7 @@
 // of 16 x 16 holds the scores of rows 2 ty, 2 ty + 1 and keys tx + 16 j, and the output columns
 // 4 tx + 64 j of those rows.  fp32 throughout: scores by fp32 FMA, 2^x of the fused difference
 // s * scale - m (the rounding of m is the same for the whole row and cancels in the normalisation),
-// running maximum, sum and output in fp32.  Bound: the FMA pipes for long chunks (the tensor cores
+// running maximum, sum and output in fp32.  Tiles come by cp.async, one ahead.  Bound: the FMA pipes for long chunks (the tensor cores
 // have no fp32 type), HBM for few rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -20,7 +20,7 @@ constexpr int kF32Threads = 256;
 
 template <int D>
 constexpr size_t f32_smem_bytes() {
-  return sizeof(float) * (kF32Rows * (D + 4) + kF32Keys * (D + 4) + kF32Keys * D + kF32Rows * (kF32Keys + 4));
+  return sizeof(float) * (kF32Rows * (D + 4) + 2 * kF32Keys * (D + 4) + 2 * kF32Keys * D + kF32Rows * (kF32Keys + 4));
 }
 
 template <int D>
@@ -28,9 +28,10 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
   pdl_launch_dependents();
   extern __shared__ __align__(16) float sm[];
   float* qs = sm;                                // [32][D + 4]
-  float* ks = qs + kF32Rows * (D + 4);           // [64][D + 4]
-  float* vs = ks + kF32Keys * (D + 4);           // [64][D]
-  float* ps = vs + kF32Keys * D;                 // [32][64 + 4]
+  float* ks2 = qs + kF32Rows * (D + 4);          // [2][64][D + 4]
+  float* vs2 = ks2 + 2 * kF32Keys * (D + 4);     // [2][64][D]
+  float* ps = vs2 + 2 * kF32Keys * D;            // [32][64 + 4]
+  __shared__ int64_t s_off[2][kF32Keys];         // where the keys of a unit lie, -1: zeros
   constexpr int C4 = D / 4, OC = D / 64;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const float* q = reinterpret_cast<const float*>(p.q);
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
     const int b = it.b, g = it.g, row0 = it.row0, u0 = it.u0, u1 = it.u1, slot = it.slot;
     const SeqInfo s = it.s;
     const int rows = min(kF32Rows, s.n * p.G - row0);
+    const int warp_row = (tid >> 5) * 4;  // the warp's first row
     __syncthreads();
     for (int i = tid; i < kF32Rows * C4; i += kF32Threads) {
       const int r = i / C4, c = i % C4;
@@ -57,18 +59,43 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int c = 0; c < OC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // unit u + 1 is on its way while unit u is computed; its keys were looked up a unit earlier still
+    auto look_up = [&](int u) {
+      if (u < u1 && tid < kF32Keys) {
+        const int key = u * kF32Keys + tid;
+        int64_t off = -1;
+        if (key >= s.lo && key < s.len) {
+          off = key_offset(p, s, b, g, key);
+          if (off < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+        }
+        s_off[u & 1][tid] = off;
+      }
+    };
+    auto issue = [&](int u) {
+      if (u < u1) {
+        float *kd = ks2 + (u & 1) * kF32Keys * (D + 4), *vd = vs2 + (u & 1) * kF32Keys * D;
+        for (int i = tid; i < kF32Keys * C4; i += kF32Threads) {
+          const int r = i / C4, c = i % C4;
+          const int64_t off = s_off[u & 1][r];
+          cp_async16(smem_u32(kd + r * (D + 4) + c * 4), k + (off < 0 ? 0 : off) + c * 4, off >= 0);
+          cp_async16(smem_u32(vd + r * D + c * 4), v + (off < 0 ? 0 : off) + c * 4, off >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+    look_up(u0);
+    __syncthreads();
+    issue(u0);
+    look_up(u0 + 1);
     for (int u = u0; u < u1; ++u) {
       const int key0 = u * kF32Keys;
-      __syncthreads();
-      for (int i = tid; i < kF32Keys * C4; i += kF32Threads) {
-        const int r = i / C4, c = i % C4, t = key0 + r;
-        const bool in = t >= s.lo && t < s.len;
-        const int64_t off = in ? key_offset(p, s, b, g, t) : -1;
-        if (in && off < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
-        *reinterpret_cast<float4*>(ks + r * (D + 4) + c * 4) = off >= 0 ? *reinterpret_cast<const float4*>(k + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(vs + r * D + c * 4) = off >= 0 ? *reinterpret_cast<const float4*>(v + off + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      __syncthreads();
+      const float *ks = ks2 + (u & 1) * kF32Keys * (D + 4), *vs = vs2 + (u & 1) * kF32Keys * D;
+      __syncthreads();  // unit u + 1 looked up; the buffers of unit u - 1 are free
+      issue(u + 1);
+      cp_async_wait<1>();
+      __syncthreads();  // unit u has landed, its offsets are free
+      look_up(u + 2);
+      if (warp_row >= rows) continue;  // rows of padding only
       float x[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -140,6 +167,7 @@ __global__ void __launch_bounds__(kF32Threads) chunk_attn_f32(const __grid_const
       }
       __syncwarp();
     }
+    cp_async_wait<0>();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int mrow = 2 * ty + r;

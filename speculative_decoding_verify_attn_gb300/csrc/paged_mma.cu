@@ -468,12 +468,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
 }
 
 // Joins the records of the segments that were split over CTAs; zeros for rows of a bad length.
-// One CTA per segment, a warp per row.
+// grid (segments, rows / 8), a warp per row; a batch of records' statistics and values are all in flight
+// at once.
+constexpr int kMmaMergeBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_constant__ ServeAttnParams p) {
   __shared__ int64_t s_scan[kMmaWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
+  const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv, r = blockIdx.y * kMmaWarps + warp;
   int64_t before = 0, all = 0;
   for (int i = tid; i < p.B; i += kMmaThreads) {
     const int u = mma_units(seq_info(p, i));
@@ -483,47 +485,55 @@ __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_cons
   const int64_t total = block_sum(all, s_scan) * p.Hkv;
   before = block_sum(before, s_scan) * p.Hkv;
   const SeqInfo s = seq_info(p, b);
-  const int nu = mma_units(s), rows = s.n * p.G;
+  const int nu = mma_units(s);
+  if (r >= s.n * p.G) return;
   const int64_t per = mma_per_cta(total, p.grid);
   const int64_t start = before + (int64_t)g * nu;
-  const int64_t c0 = start / per, c1 = nu > 0 ? (start + nu - 1) / per : c0;
-  pdl_wait();
-  if (nu > 0 && c0 == c1) return;  // written by its CTA
+  const int64_t c0 = start / per;
+  const int n = nu > 0 ? (int)((start + nu - 1) / per - c0) + 1 : 0;
+  if (n == 1) return;  // written by its CTA
+  // record i: CTA c0 + i's first, but for c0's second where the segment does not start where c0 does
+  const int64_t first = 2 * c0 + (nu > 0 && start % per == 0 ? 0 : 1);
   constexpr int E = D / 32;
-  for (int r = warp; r < rows; r += kMmaWarps) {
-    float acc[E];
+  float acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float L = 0.f;
-    if (nu > 0) {
-      // the first record is its CTA's second unless the segment starts where that CTA starts
-      const int64_t first = 2 * c0 + (start % per == 0 ? 0 : 1);
-      float M = neg_inf();
-      for (int64_t c = c0 + lane; c <= c1; c += 32) {
-        const int64_t rec = c == c0 ? first : 2 * c;
-        M = fmaxf(M, __ldcg(&p.part_ml[rec * kMmaMaxRows + r]).x);
-      }
-      M = warp_max(M);
-      if (M != neg_inf()) {
-#pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-          const int64_t rec = c == c0 ? first : 2 * c;
-          const float2 ml = __ldcg(&p.part_ml[rec * kMmaMaxRows + r]);
-          const float w = ml.x == neg_inf() ? 0.f : exp2f(ml.x - M);
-          L += w * ml.y;
-          const float* src = p.part_o + (rec * kMmaMaxRows + r) * D + lane * E;
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  float M = neg_inf(), L = 0.f;
+  pdl_wait();
+  for (int i0 = 0; i0 < n; i0 += kMmaMergeBatch) {
+    float2 ml[kMmaMergeBatch];
+    float v[kMmaMergeBatch][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __ldcg(src + e), acc[e]);
-        }
-      }
+    for (int u = 0; u < kMmaMergeBatch; ++u) {
+      const int i = i0 + u;
+      const int64_t at = (i == 0 ? first : 2 * (c0 + i)) * kMmaMaxRows + r;
+      ml[u] = i < n ? __ldcg(&p.part_ml[at]) : make_float2(neg_inf(), 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[u][e] = i < n ? __ldcg(p.part_o + at * D + lane * E + e) : 0.f;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int64_t off = o_offset(p, s, g, r) + lane * E;
+    float m = M;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off + e] = __float2bfloat16_rn(acc[e] * inv);
-      else reinterpret_cast<float*>(p.o)[off + e] = acc[e] * inv;
+    for (int u = 0; u < kMmaMergeBatch; ++u) m = fmaxf(m, ml[u].x);
+    if (m == neg_inf()) continue;
+    const float a = M == neg_inf() ? 0.f : exp2f(M - m);
+    M = m;
+    L *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+    for (int u = 0; u < kMmaMergeBatch; ++u) {
+      const float w = ml[u].x == neg_inf() ? 0.f : exp2f(ml[u].x - m);
+      L += w * ml[u].y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
     }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int64_t off = o_offset(p, s, g, r) + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off + e] = __float2bfloat16_rn(acc[e] * inv);
+    else reinterpret_cast<float*>(p.o)[off + e] = acc[e] * inv;
   }
 }
 
@@ -547,7 +557,8 @@ static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.direct) return e;
-  return launch_dependent(paged_mma_merge<D>, dim3(p.B * p.Hkv), dim3(kMmaThreads), 0, stream, 0u, p);
+  const unsigned rows = (unsigned)(p.max_q * p.G + kMmaWarps - 1) / kMmaWarps;
+  return launch_dependent(paged_mma_merge<D>, dim3(p.B * p.Hkv, rows), dim3(kMmaThreads), 0, stream, 0u, p);
 }
 
 template <int D>
