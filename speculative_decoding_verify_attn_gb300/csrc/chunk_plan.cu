@@ -24,13 +24,11 @@
 
 namespace specv {
 
-constexpr int kPlanThreads = 1024;
+// Few threads: every instruction of the plan is paid by each of its warps, and its steps are short (four
+// fp32 sequences with cut tiles: 13 800 cycles, 18 900 with 1024 threads).
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBins = 256;
-// What a piece costs beside its units (its rows, its first maximum, its epilogue), and what cutting
-// costs a CTA (the second cut tile's piece, the merge), in units: measured 7000 cycles on the tcgen05
-// kernel, whose units take 2700.
-constexpr float kPieceCost = 3.f;
-constexpr float kCutCost = 7.f;
 
 __device__ __forceinline__ int chunk_tiles(const ServeAttnParams& p, const SeqInfo& s) {
   return s.len > 0 ? (int)(((int64_t)s.n * p.G + p.row_tile - 1) / p.row_tile) : 0;
@@ -40,7 +38,7 @@ struct PlanTile {
   int b, row0, u0, u1;
 };
 
-__device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, int* s_n, int* s_len) {
+__device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, int* s_n, int* s_len, int* s_q0) {
   __shared__ uint32_t s_warp[32];
   __shared__ int64_t s_sum[32];
   __shared__ int s_bin[kPlanBins];
@@ -54,7 +52,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     s_splits = 0;
     s_waves = kBigPieces;
   }
-  if (tid < kPlanBins) s_bin[tid] = 0;
+  for (int i = tid; i < kPlanBins; i += kPlanThreads) s_bin[i] = 0;
 
   // ---- tiles per sequence, and their prefix s_pre.  Overlapping ranges can add up to more rows than
   // there are; sums are capped where the plan has no room for them anyway.
@@ -68,6 +66,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
       n = (uint32_t)chunk_tiles(p, s);
       s_n[b] = s.n;
       s_len[b] = s.len;
+      s_q0[b] = s.q0;
       if (s.bad) status_report(p.status, s.bad);
     }
     uint32_t x = n;  // at most 2^22 each
@@ -78,7 +77,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     }
     if (lane == 31) s_warp[warp] = min(x, kCap);
     __syncthreads();
-    const uint32_t sums = s_warp[lane];
+    const uint32_t sums = lane < kPlanWarps ? s_warp[lane] : 0u;
     const uint32_t pre = run + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
     run = min(run + __reduce_add_sync(0xffffffffu, sums), kCap);
     if (b < p.B) s_pre[b] = (int)min(pre + x - n, kCap);
@@ -129,18 +128,18 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     s_warp[warp] = longest;
   }
   __syncthreads();
-  int64_t total = s_sum[lane];
+  int64_t total = lane < kPlanWarps ? s_sum[lane] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  longest = __reduce_max_sync(0xffffffffu, s_warp[lane]);
+  longest = __reduce_max_sync(0xffffffffu, lane < kPlanWarps ? s_warp[lane] : 0u);
   const int64_t all = total * p.Hkv;
   const int per = (int)max((int64_t)p.min_units, (all + p.grid - 1) / p.grid);
-  // cut only where that beats dealing whole tiles, in units with kPieceCost for every piece: whole tiles
+  // cut only where that beats dealing whole tiles, in units with piece_cost for every piece: whole tiles
   // take the longest one, or as many average ones as waves; shares take the mean, a second cut tile and
   // the merge
-  const float items = (float)tiles * p.Hkv, mean = (float)all / p.grid + kPieceCost * items / p.grid;
-  const float whole_cost = fmaxf((float)longest + kPieceCost, ceilf(items / p.grid) * (mean * p.grid / fmaxf(items, 1.f)));
-  const bool cut = mean + kCutCost < 0.95f * whole_cost;
+  const float items = (float)tiles * p.Hkv, mean = (float)all / p.grid + p.piece_cost * items / p.grid;
+  const float whole_cost = fmaxf((float)longest + p.piece_cost, ceilf(items / p.grid) * (mean * p.grid / fmaxf(items, 1.f)));
+  const bool cut = mean + p.cut_cost < 0.95f * whole_cost;
   auto is_big = [&](int n) { return cut && n > per / kBigFraction; };
 
   // ---- big tiles in the batch's order, with the units before each; small tiles by size
@@ -170,8 +169,8 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
       s_sum[warp] = x;
     }
     __syncthreads();
-    const uint32_t counts = s_warp[lane];
-    int64_t pre_units = lane < warp ? s_sum[lane] : 0, sum_units = s_sum[lane];
+    const uint32_t counts = lane < kPlanWarps ? s_warp[lane] : 0u;
+    int64_t pre_units = lane < warp ? s_sum[lane] : 0, sum_units = lane < kPlanWarps ? s_sum[lane] : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       pre_units += __shfl_xor_sync(0xffffffffu, pre_units, o);
@@ -276,11 +275,11 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     start = s_big_at[lo] * p.Hkv + (int64_t)g * n;
   };
   auto write_item = [&](ChunkItem* item, const PlanTile& r, int u0, int u1, int slot, int g) {
-    const SeqInfo s = seq_info(p, r.b);
+    const int n = s_n[r.b], len = s_len[r.b];
     int4* dst = reinterpret_cast<int4*>(item);
     dst[0] = make_int4(r.b, r.row0, u0, u1);
-    dst[1] = make_int4(slot, s.q0, s.n, s.len);
-    dst[2] = make_int4(s.lo, g, 0, 0);
+    dst[1] = make_int4(slot, s_q0[r.b], n, len);
+    dst[2] = make_int4(p.window > 0 ? max(0, len - n + 1 - min(p.window, len)) : 0, g, 0, 0);
   };
   if (tid < ctas) {
     int k = 0;
@@ -337,9 +336,9 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
 // thread per 16-byte chunk of a row.
 __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_constant__ ServeAttnParams p, int elem) {
   pdl_launch_dependents();
-  extern __shared__ int s_seq[];  // [B + 1], [B], [B]
+  extern __shared__ int s_seq[];  // [B + 1], [B], [B], [B]
   if (blockIdx.x == 0) {
-    plan_body(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1);
+    plan_body(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1, s_seq + 3 * p.B + 1);
     return;
   }
   const int b = (blockIdx.x - 1) % p.B, y = (blockIdx.x - 1) / p.B, ny = (gridDim.x - 1) / p.B;
@@ -483,13 +482,13 @@ void chunk_workspace_carve(void* ws, ServeAttnParams* p) {
 }
 
 cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
-  const int smem = (3 * p.B + 1) * (int)sizeof(int);
+  const int smem = (4 * p.B + 1) * (int)sizeof(int);
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(chunk_prepare), smem);
   if (e != cudaSuccess) return e;
   unsigned grid = 1;
-  if (p.k_new) {  // about 600 CTAs at most, one per sequence at least
+  if (p.k_new) {  // about 2400 CTAs at most, one per sequence at least
     const int64_t want = ((int64_t)p.max_q * p.Hkv * (p.D * elem_bytes / 16) + kPlanThreads - 1) / kPlanThreads;
-    const int64_t most = (600 + p.B - 1) / p.B;
+    const int64_t most = (2400 + p.B - 1) / p.B;
     grid += (unsigned)p.B * (unsigned)(want < most ? want : most);
   }
   chunk_prepare<<<grid, kPlanThreads, smem, stream>>>(p, elem_bytes);

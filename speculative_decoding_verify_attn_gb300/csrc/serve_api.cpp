@@ -100,6 +100,10 @@ int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream
   p.row_tile = chunk_row_tile(kv_dtype);
   p.unit_keys = bf16 ? specv::kTcKeys : specv::kF32Keys;
   p.min_units = 2;
+  // measured 7000 cycles a piece on the tcgen05 kernel, whose units take 2700; the fp32 kernel's units take
+  // as long and its pieces start and end faster
+  p.piece_cost = bf16 ? 3.f : 1.f;
+  p.cut_cost = bf16 ? 7.f : 3.f;
   specv::chunk_workspace_carve(ws, &p);
   CUtensorMap tm[2];
   if (bf16) {

@@ -20,7 +20,7 @@ constexpr int kMmaDirectKeys = 4 * kMmaUnit;
 constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
 constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
 constexpr int kTmaMinPage = 32; // tokens per page from which the tcgen05 kernel copies pages by TMA
-constexpr int kF32Rows = 32;    // query rows per tile of the fp32 kernel
+constexpr int kF32Rows = 64;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 
 // One piece of work of a chunk kernel: the row tile starting at row `row0` of sequence b (row r: token
@@ -66,6 +66,9 @@ struct ServeAttnParams {
   int grid;               // CTAs of the attention kernel
   int direct;             // mma.sync kernel: a CTA per segment, no records
   int row_tile, unit_keys;  // chunk kernels: rows per tile, keys per unit
+  // chunk kernels: what a piece costs beside its units (its rows, its first maximum, its epilogue), and
+  // what cutting costs a CTA (a second cut tile's piece, the merge), in units
+  float piece_cost, cut_cost;
   int min_units;          // chunk kernels: units a CTA's share of cut tiles has at least
   int use_tma;            // tcgen05 kernel: the tensor maps are valid
   int tma_page_keys;      // keys one copy brings (min(page_size, kTcKeys); packed: kTcKeys)
