@@ -44,8 +44,9 @@ enum {
  * over t in (p - window, p] (window > 0) or [0, p] (window == 0).  Token t of sequence b is slot
  * t % page_size of page page_table[b, t / page_size].
  *   k_new / v_new set (both or neither): the call also writes the new tokens' rows into their
- *   slots; the attention uses them.  Pages written to must belong to one sequence each.  NULL: the
- *   caller has written them.
+ *   slots; the attention uses them.  A slot written to must be one new token's and seen by its
+ *   sequence alone (pages that sequences share hold earlier tokens only).  NULL: the caller has
+ *   written them.
  *   window: K/V of tokens below kv_len[b] - n_b + 1 - window are not read, nor are their table
  *   entries, so their pages may have been given back.
  *
@@ -58,19 +59,21 @@ enum {
  *   aligned) and the int32 ones are 16-byte aligned.
  * Limits: D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 32; 1 <= B <= 4096; 0 <= T <= 2^22 (T == 0:
  *   nothing is launched); max_q >= 1; 1 <= page_size <= 65536; table_cols >= 1;
- *   table_cols * page_size < 2^31; window >= 0; scale >= 0 and finite.  max_q is an upper bound on
+ *   table_cols * page_size <= 2^30; window >= 0; scale >= 0 and finite.  max_q is an upper bound on
  *   every n_b and chooses the kernel; a tight one is faster.
+ * No output overlaps an input: not o, nor the pages with k_new / v_new.
  * Rows of q at or past q_start[B], or before q_start[0], are not read and their o is left as it was.
  * Data errors: a sequence whose q_start is out of order (SPEC_STATUS_BAD_RANGE) has no rows, and
- *   its o is left as it was; kv_len[b] < n_b or > table_cols * page_size (SPEC_STATUS_BAD_KV_LEN)
+ *   its o is left as it was (ranges that overlap, so that they add up to more than T rows, can cost the
+ *   others theirs too); kv_len[b] < n_b or > table_cols * page_size (SPEC_STATUS_BAD_KV_LEN)
  *   gives zeros and no append; a needed page id out of range (SPEC_STATUS_BAD_PAGE) is never
  *   followed: its tokens read as zeros (o of the rows that see them is not meaningful) and are not
  *   written (appended rows then take part from k_new / v_new, or as zeros).
  * K and V of the tokens that some row of the chunk sees have to be finite; slots past kv_len and
  *   pages before the window may hold anything.
  * Accumulation is fp32 (scores, softmax statistics, P.V); for bf16 K/V the probabilities are
- *   rounded to bf16 before P.V, as in spec_verify_attn.  Results do not depend on the order in
- *   which CTAs run.
+ *   rounded to bf16 before P.V, as in spec_verify_attn.  A call's result is the same every time; it
+ *   can differ in the last bits between batches (and devices), whose work is cut differently.
  * ---------------------------------------------------------------------------------------- */
 typedef struct spec_paged_args {
   int32_t B, Hq, Hkv, D, T, max_q;
@@ -108,8 +111,8 @@ int spec_paged_attn(const spec_paged_args* args, spec_stream_t stream);
  * sequence, the last `window` of them if window > 0 (what spec_draft_window_attn later sees of its
  * ring).  Sequences of length 0 are allowed.
  * Layout: q, o [T, Hq, D]; k, v [T, Hkv, D] with equal strides; seq_start [B + 1] int32.
- * Types, alignment, limits, rows outside the sequences, finiteness and accumulation as
- *   spec_paged_attn; a sequence whose seq_start is out of order is skipped
+ * Types, alignment, limits, overlap, rows outside the sequences, finiteness (of a sequence's own
+ *   rows: neighbours may hold anything) and accumulation as spec_paged_attn; a sequence whose seq_start is out of order is skipped
  *   (SPEC_STATUS_BAD_RANGE).
  * ---------------------------------------------------------------------------------------- */
 typedef struct spec_prefill_args {

@@ -14,6 +14,10 @@
 // cp.async rather than TMA: a page may be any number of tokens in any layout, and the copies of an
 // SM's tensor-memory-access unit complete at a rate set by their number, which small pages multiply.
 //
+// Measured, 8 sequences of 16K-32K, 32/8 heads of 128: one token each 115 us (6.2 TB/s), five 155 us
+// (6.0 TB/s), eight 157 us (5.2 TB/s, the two warps of a scheduler no longer hide each other's latency);
+// 8 segments of 300 keys 7.5 us of device time.
+//
 // Append: a new token's row is read from k_new / v_new and also stored into its slot by the warp
 // that owns the key; no CTA reads that slot in this call, so nothing has to be ordered.
 #include <cuda_bf16.h>

@@ -59,8 +59,10 @@ int serve_grid() {
   return sms < specv::kServeMaxGrid ? sms : specv::kServeMaxGrid;
 }
 
-// Few query rows per kv head: the mma.sync kernel reads the cache at the HBM rate; more rows need
-// the tensor cores' larger tiles.
+// Few query rows per kv head: the mma.sync kernel; more rows need the tcgen05 kernel's tiles.  Measured at
+// 8 sequences of 16K-32K, 32/8 heads, mma.sync against tcgen05: 4 rows 115 and 150 us, 16 rows 122 and
+// 151 us, 24 rows 142 and 164 us, 32 rows 157 and 165 us; one sequence of 2000 tokens, where launches
+// count (1 against 3 at least): 27-29 and 31-36 us.
 bool use_mma(int kv_dtype, int max_q, int G) {
   return kv_dtype == SPEC_BF16 && (int64_t)max_q * G <= specv::kMmaMaxRows;
 }
@@ -154,7 +156,7 @@ int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
   int st = check_shape(s);
   if (st != SPEC_OK) return st;
   if (a->page_size < 1 || a->page_size > 65536 || a->num_pages < 1 || a->table_cols < 1 || a->table_stride < 0 ||
-      (int64_t)a->table_cols * a->page_size > 0x7fffffff)
+      (int64_t)a->table_cols * a->page_size > (1 << 30))
     return SPEC_ERR_INVALID_ARG;
   if (!isfinite(a->scale) || a->scale < 0.f) return SPEC_ERR_INVALID_ARG;
   if ((a->k_new == nullptr) != (a->v_new == nullptr)) return SPEC_ERR_INVALID_ARG;

@@ -15,11 +15,15 @@ constexpr int kServeMaxGrid = 160;
 // runs.
 constexpr int kMmaMaxRows = 32;
 constexpr int kMmaUnit = 128;   // keys per unit of work of the mma.sync kernel (16 per warp)
-// Segments of at most this many keys are one CTA of the mma.sync kernel each (no merge launch).
+// Segments of at most this many keys are one CTA of the mma.sync kernel each (no merge launch).  Device
+// time with and without: 8 segments of 128 keys 5.2 and 6.9 us, 256 segments of 512 keys 15.4 and 17.5;
+// past it 8 segments of 1024 keys take 11.3 and 8.4.
 constexpr int kMmaDirectKeys = 4 * kMmaUnit;
 constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
 constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
-constexpr int kTmaMinPage = 32; // tokens per page from which the tcgen05 kernel copies pages by TMA
+// Tokens per page from which the tcgen05 kernel copies pages by TMA, below cp.async.  A 2048-token chunk at
+// 32K by TMA and by cp.async: pages of 16 961 and 781 us, of 32 754 and 767, of 64 681 and 751.
+constexpr int kTmaMinPage = 32;
 constexpr int kF32Rows = 64;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 

@@ -225,6 +225,69 @@ def test_many_sequences(sv, q, page):
     Paged(q_len, kv_len, 4, 2, 64, page, append=True, seed=70).verify(sv)
 
 
+@pytest.mark.parametrize("q", [1, 40])
+def test_most_sequences(sv, q):
+    """4096 sequences, most of them resting, and a bound on the chunk lengths that is far too wide."""
+    rng = np.random.default_rng(8)
+    q_len = [0] * 4096
+    for b in rng.integers(0, 4096, 150):
+        q_len[b] = int(rng.integers(1, q + 1))
+    q_len[0] = q_len[4095] = q
+    kv_len = [n + int(x) for n, x in zip(q_len, rng.integers(0, 3, 4096))]
+    p = Paged(q_len, kv_len, 1, 1, 64, 4, seed=75)
+    p.verify(sv)
+    p.verify(sv, max_q=10 ** 6)
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("rows", [16, 17, 32, 33, 128, 129, 256, 257])
+def test_row_boundaries(sv, rows, G):
+    """One row more or less than each tile of the kernels holds."""
+    n = -(-rows // G)
+    Paged([n, 1], [n + 200, 77], G, 1, 64, 32, append=True, seed=rows + G).verify(sv)
+
+
+@pytest.mark.parametrize("q_len", [[1, 3], [50, 20]])
+def test_shared_prefix_and_large_pages(sv, q_len):
+    """Two sequences whose first pages are the same ones; a page much longer than the sequences."""
+    torch = torch_mod()
+    p = Paged(q_len, [400, 380], 8, 2, 64, 64, seed=77)
+    p.table[1, :4] = p.table[0, :4]
+    p.d_table = torch.from_numpy(p.table).cuda()
+    p.verify(sv)
+    Paged(q_len, [400, 380], 8, 2, 64, 1000, append=True, seed=78).verify(sv)
+
+
+def test_binding_refusals(sv):
+    torch = torch_mod()
+    p = Paged([3], [40], 4, 2, 64, 16, seed=79)
+    o = torch.empty(p.q.shape, device="cuda")
+    call = lambda **kw: sv.spec_paged_attn(**dict(dict(q=p.d_q, k_pages=p.k, v_pages=p.v, page_table=p.d_table,  # noqa: E731
+                                                      q_start=p.d_start, kv_len=p.d_len, o=o, max_q=3), **kw))
+    with pytest.raises(ValueError):
+        call(kv_len=p.d_len.long())
+    with pytest.raises(ValueError):
+        call(kv_len=p.d_len.cpu())
+    with pytest.raises(ValueError):
+        call(workspace=torch.empty(100, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        call(q=p.d_q.transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(TypeError):
+        call(q=p.d_q.half())
+    for bad in (dict(q=p.d_q.float()), dict(window=-1), dict(max_q=0), dict(scale=float("inf"))):
+        with pytest.raises(sv.SpecError):
+            call(**bad)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    with pytest.raises(sv.SpecError):
+        call(workspace=ws[8:])
+    call(workspace=ws)
+    empty = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    zeros = torch.zeros(2, dtype=torch.int32, device="cuda")
+    sv.spec_paged_attn(empty, p.k, p.v, p.d_table, zeros, p.d_len, empty, max_q=1)
+    sv.spec_prefill_attn(empty, empty, empty, zeros, empty)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("q_len", [[2, 3, 1, 4], [40, 3, 1, 20]])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_data_is_flagged_and_contained(sv, q_len, dtype):

@@ -57,7 +57,7 @@ def test_struct_sizes(L):
     (dict(T=-1), -1), (dict(T=(1 << 22) + 1, max_q=5), -2), (dict(max_q=0), -1), (dict(max_q=-1), -1),
     (dict(Hq=66, Hkv=2), -2), (dict(q_dtype=0), -2), (dict(kv_dtype=5, q_dtype=5), -1), (dict(o_dtype=2), -1),
     (dict(page_size=0), -1), (dict(page_size=65537), -1), (dict(num_pages=0), -1), (dict(table_cols=0), -1),
-    (dict(table_cols=1 << 28, page_size=16), -1), (dict(table_stride=-1), -1), (dict(window=-1), -1),
+    (dict(table_cols=1 << 28, page_size=16), -1), (dict(table_cols=(1 << 26) + 1, page_size=16), -1), (dict(table_stride=-1), -1), (dict(window=-1), -1),
     (dict(scale=float("nan")), -1), (dict(scale=-1.0), -1), (dict(q=None), -1), (dict(q=FAKE + 8), -1),
     (dict(q_stride_t=1028), -1), (dict(k_pages=None), -1), (dict(v_pages=FAKE + 4), -1), (dict(kv_stride_t=132), -1),
     (dict(kv_stride_p=-8), -1), (dict(k_new=FAKE), -1), (dict(v_new=FAKE), -1),
