@@ -344,10 +344,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     };
     // the warp's 32 rows of a piece into shared memory (K-major, 128-byte swizzle; zeros for padding
     // rows), asynchronously
-    auto start_q = [&](const PieceItem& n) {
+    // (token and head of the thread's own row in `tok` and `head`, tok < 0 for padding)
+    auto start_q = [&](const PieceItem& n, int& tok, int& head) {
       constexpr int CH = D / 8, RPI = 32 / CH;
       const int r = n.row0 + w * 128 + m;
-      const int64_t mine = r < n.s.n * p.G ? q_offset(p, n.s, n.g, r) : -1;
+      tok = r / p.G;
+      head = n.g * p.G + r - tok * p.G;
+      if (r >= n.s.n * p.G) tok = -1;
+      const int64_t mine = tok >= 0 ? (int64_t)(n.s.q0 + tok) * p.q_st + (int64_t)head * p.q_sh : -1;
       const int c = lane % CH;
 #pragma unroll
       for (int i = 0; i < 32 / RPI; ++i) {
@@ -366,28 +370,27 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     };
 
     PieceItem it;
-    int b0 = 0, b1 = 0;
+    int b0 = 0, b1 = 0, tok = -1, head = 0;
     bool have = next_piece(it, b0, b1), ok = true;
     if (have) {
-      start_q(it);
+      start_q(it, tok, head);
       finish_q();
     }
     int t = 0, part = 0;
     while (have && ok) {
       PieceItem nx;
-      int nb0 = 0, nb1 = 0;
+      int nb0 = 0, nb1 = 0, ntok = -1, nhead = 0;
       bool have_next = false, looked = false;
-      const int r = it.row0 + w * 128 + m;
-      const bool real = r < it.s.n * p.G;
+      const bool real = tok >= 0;
       // position of the row's token; padding rows see what the last row sees
-      const int pos = it.s.len - it.s.n + (real ? r / p.G : it.s.n - 1);
+      const int pos = it.s.len - it.s.n + (real ? tok : it.s.n - 1);
       const int wlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float m_run = neg_inf(), l = 0.f;
       for (int u = b0; u < b1; ++u, ++t) {
         if (u == b1 - 1 && !looked) have_next = next_piece(nx, nb0, nb1);
         if (!warp_wait(&sfull[w], t & 1)) { ok = false; break; }
         tc::fence_after();
-        if (u == b1 - 1 && have_next) start_q(nx);  // the piece's last Q K^T has read its rows
+        if (u == b1 - 1 && have_next) start_q(nx, ntok, nhead);  // the piece's last Q K^T has read its rows
         const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
         // P = 2^(s * scale - mu) against the present reference, as bf16 pairs; only where a row's sum
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       // bf16 rows on 16-byte boundaries: four lanes turn their four rows' 64 bytes around, so that a
       // store covers 64 bytes of a row instead of 16
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t off = real ? o_offset(p, it.s, it.g, r) : -1;
+      const int64_t off = real ? (int64_t)(it.s.q0 + tok) * p.o_st + (int64_t)head * p.o_sh : -1;
       const bool quads = p.o_bf16 && __all_sync(0xffffffffu, !real || ((reinterpret_cast<uintptr_t>(p.o) + off * 2) & 15u) == 0);
       int64_t quad_off[4];
 #pragma unroll
@@ -570,6 +573,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       it = nx;
       b0 = nb0;
       b1 = nb1;
+      tok = ntok;
+      head = nhead;
     }
     if (!ok) fail();
   }
