@@ -77,25 +77,28 @@ def _serve_lib():
 
 
 # ---------------------------------------------------------------------------- helpers
-_torch = None
+# A decode step's kernel is done in a few microseconds, so what happens here per call is kept short:
+# torch's objects are looked up once, sizes and strides are read once per tensor.
+_torch = _i32 = _f32 = None
+_codes = {}
 
 
 def _t():
     """torch, imported on first use."""
-    global _torch
+    global _torch, _i32, _f32
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _i32, _f32 = torch, torch.int32, torch.float32
+        _codes[torch.bfloat16], _codes[torch.float32] = SPEC_BF16, SPEC_F32
     return _torch
 
 
 def _dtype_code(t) -> int:
-    torch = _t()
-    if t.dtype is torch.bfloat16:
-        return SPEC_BF16
-    if t.dtype is torch.float32:
-        return SPEC_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    _torch or _t()
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _check(tensors) -> int:
@@ -116,10 +119,10 @@ def _rows(name, t):
     return st
 
 
-def _int32(name, t, *shape):
-    if t.dtype is not _t().int32 or t.shape != shape:
-        raise ValueError(f"{name} must be int32 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _rows(name, t)
+def _vector(name, t, n, dtype):
+    """Checks a contiguous vector of n elements."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n}, got {t.dtype} {tuple(t.shape)}")
 
 
 _sizes = {}
@@ -128,13 +131,13 @@ _sizes = {}
 def _call(name, args, sizes, index, workspace, stream):
     """Sizes the workspace, fills it in and makes the call on the tensors' device.  `sizes` is what the
     workspace's size depends on: the library is asked once for each."""
-    torch = _t()
-    if index != torch.cuda.current_device():
+    torch = _torch or _t()
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _call(name, args, sizes, index, workspace, stream)
     L = _lib or _serve_lib()
     ref = byref(args)
-    need = _sizes.get((name, sizes))
+    need = _sizes.get(sizes)
     if need is None:
         need = getattr(L, name + "_workspace")(ref)
         if need == 0:
@@ -142,7 +145,7 @@ def _call(name, args, sizes, index, workspace, stream):
             raise SpecError(getattr(L, name)(ref, None) or SPEC_ERR_INVALID_ARG, name)
         if len(_sizes) > 4096:
             _sizes.clear()
-        _sizes[(name, sizes)] = need
+        _sizes[sizes] = need
     handle = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -177,20 +180,22 @@ def _workspace_bytes(name, args) -> int:
 def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_q, k_new=None, v_new=None,
                     window: int = 0, scale: float = 0.0) -> SpecPagedArgs:
     """Fill SpecPagedArgs from tensors (no workspace yet)."""
-    T, Hq, D = q.shape
-    shape = k_pages.shape
+    _torch or _t()
+    q_shape, shape = q.shape, k_pages.shape
+    T, Hq, D = q_shape
     pages, Hkv, page_size, D2 = shape
     B, cols = page_table.shape
-    qs, ks, os_ = _rows("q", q), _rows("k_pages", k_pages), _rows("o", o)
+    qs, ks, os_, ts = _rows("q", q), _rows("k_pages", k_pages), _rows("o", o), _rows("page_table", page_table)
     if D2 != D or v_pages.shape != shape or v_pages.stride() != ks:
         raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with q's D and equal strides")
     if v_pages.dtype is not k_pages.dtype:
         raise TypeError("k_pages and v_pages must share a dtype")
-    if o.shape != q.shape:
+    if o.shape != q_shape:
         raise ValueError("o must have q's shape")
-    ts = _int32("page_table", page_table, B, cols)
-    _int32("q_start", q_start, B + 1)
-    _int32("kv_len", kv_len, B)
+    if page_table.dtype is not _i32:
+        raise ValueError(f"page_table must be int32, got {page_table.dtype}")
+    _vector("q_start", q_start, B + 1, _i32)
+    _vector("kv_len", kv_len, B, _i32)
     kn = vn = None
     ns = (0, 0)
     if k_new is not None or v_new is not None:
@@ -230,13 +235,14 @@ def spec_paged_attn(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
     index = _check((q, k_pages, v_pages, page_table, q_start, kv_len, o, k_new, v_new))
     a = paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, max_q=max_q, k_new=k_new, v_new=v_new,
                         window=window, scale=scale)
-    _call("spec_paged_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.max_q, a.kv_dtype), index, workspace, stream)
+    _call("spec_paged_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.max_q, a.kv_dtype, "paged"), index, workspace, stream)
     return o
 
 
 # ---------------------------------------------------------------------------- packed prompts
 def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 0.0) -> SpecPrefillArgs:
     """Fill SpecPrefillArgs from tensors (no workspace yet)."""
+    _torch or _t()
     T, Hq, D = q.shape
     qs, ks, os_ = _rows("q", q), _rows("k", k), _rows("o", o)
     if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or v.stride() != ks:
@@ -246,7 +252,7 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     if o.shape != q.shape:
         raise ValueError("o must have q's shape")
     B = seq_start.shape[0] - 1
-    _int32("seq_start", seq_start, B + 1)
+    _vector("seq_start", seq_start, B + 1, _i32)
     return SpecPrefillArgs(
         B, Hq, k.shape[1], D, T, window, _dtype_code(q), _dtype_code(k), _dtype_code(o), scale, q.data_ptr(), qs[0],
         qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(), o.data_ptr(), os_[0], os_[1], None, 0)
@@ -268,34 +274,38 @@ def spec_prefill_attn(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     it."""
     index = _check((q, k, v, seq_start, o))
     a = prefill_attn_args(q, k, v, seq_start, o, window=window, scale=scale)
-    _call("spec_prefill_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.kv_dtype), index, workspace, stream)
+    _call("spec_prefill_attn", a, (a.B, a.Hq, a.Hkv, a.D, a.T, a.kv_dtype, "prefill"), index, workspace, stream)
     return o
 
 
 # ---------------------------------------------------------------------------- log probabilities
 def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None) -> SpecLogprobArgs:
     """Fill SpecLogprobArgs from tensors (no workspace yet)."""
-    torch = _t()
+    _torch or _t()
     N, V = logits.shape
-    if (tokens is None) != (logprobs is None):
-        raise ValueError("tokens and logprobs go together")
-    if (top_ids is None) != (top_logprobs is None):
-        raise ValueError("top_ids and top_logprobs go together")
-    K = 0 if top_ids is None else top_ids.shape[1]
-    if tokens is not None:
-        _int32("tokens", tokens, N)
-    if top_ids is not None:
-        _int32("top_ids", top_ids, N, K)
-    for name, t, shape in (("logprobs", logprobs, (N,)), ("entropy", entropy, (N,)), ("top_logprobs", top_logprobs, (N, K))):
-        if t is not None and (t.dtype is not torch.float32 or t.shape != shape):
-            raise ValueError(f"{name} must be float32 of shape {shape}")
-    for t in (tokens, logprobs, entropy, top_ids, top_logprobs):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tokens and the outputs must be contiguous")
-    ptr = [None if t is None or t.numel() == 0 else t.data_ptr() for t in (tokens, logprobs, entropy, top_ids, top_logprobs)]
+    K = 0
+    lp = ent = tok = ids = top = None
+    if tokens is not None or logprobs is not None:
+        if tokens is None or logprobs is None:
+            raise ValueError("tokens and logprobs go together")
+        _vector("tokens", tokens, N, _i32)
+        _vector("logprobs", logprobs, N, _f32)
+        tok, lp = tokens.data_ptr(), logprobs.data_ptr()
+    if entropy is not None:
+        _vector("entropy", entropy, N, _f32)
+        ent = entropy.data_ptr()
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_logprobs is None:
+            raise ValueError("top_ids and top_logprobs go together")
+        K = top_ids.shape[1]
+        for name, x, dtype in (("top_ids", top_ids, _i32), ("top_logprobs", top_logprobs, _f32)):
+            if x.dtype is not dtype or x.shape != (N, K) or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} of shape {(N, K)}")
+        if K:
+            ids, top = top_ids.data_ptr(), top_logprobs.data_ptr()
     # the stride of a single row may be anything
     return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0] if N > 1 else V,
-                           *ptr, None, 0)
+                           tok, lp, ent, ids, top, None, 0)
 
 
 def spec_token_logprobs_workspace(logits, K: int = 0) -> int:
@@ -313,5 +323,5 @@ def spec_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None,
     among equals).  Outputs not wanted are None.  Writes them and returns logprobs."""
     index = _check((logits, tokens, logprobs, entropy, top_ids, top_logprobs))
     a = token_logprobs_args(logits, tokens, logprobs, entropy=entropy, top_ids=top_ids, top_logprobs=top_logprobs)
-    _call("spec_token_logprobs", a, (a.N, a.V, a.K), index, workspace, stream)
+    _call("spec_token_logprobs", a, (a.N, a.V, a.K, "logprobs"), index, workspace, stream)
     return logprobs
