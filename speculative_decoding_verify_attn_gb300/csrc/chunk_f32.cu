@@ -29,7 +29,7 @@ constexpr size_t f32_smem_bytes() {
   return sizeof(float) * (kF32Rows * (D + 4) + 2 * kF32Keys * (D + 4) + 2 * kF32Keys * D + kF32Rows * (kF32Keys + 4));
 }
 
-template <int D>
+template <int D, bool LIGHT>
 __global__ void __launch_bounds__(kF32Threads, 1) chunk_attn_f32(const __grid_constant__ ServeAttnParams p) {
   pdl_launch_dependents();
   extern __shared__ __align__(16) float sm[];
@@ -44,9 +44,11 @@ __global__ void __launch_bounds__(kF32Threads, 1) chunk_attn_f32(const __grid_co
   const float* q = reinterpret_cast<const float*>(p.q);
   const float* k = reinterpret_cast<const float*>(p.k);
   const float* v = reinterpret_cast<const float*>(p.v);
+  __shared__ LightSeqs s_light;
   pdl_wait();  // the plan, and appended rows
-  PieceList list;
-  list.init(p);
+  if (LIGHT) light_init(p, s_light);
+  PieceList<LIGHT> list;
+  list.init(p, &s_light);
   for (int round = 0; round < list.rounds; ++round) {
     const PieceItem it = piece_item(list.fetch(p, round));
     if (it.u0 >= it.u1) continue;
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) chunk_attn_f32(const __grid_co
         int64_t off = -1;
         if (key >= s.lo && key < s.len) {
           off = key_offset(p, s, b, g, key);
-          if (off < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+          if (off < 0) chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_BAD_PAGE);
         }
         s_off[u & 1][tid] = off;
       }
@@ -319,17 +321,22 @@ __global__ void __launch_bounds__(kF32Threads, 1) chunk_attn_f32(const __grid_co
   }
 }
 
-template <int D>
+template <int D, bool LIGHT>
 static cudaError_t launch_f32(const ServeAttnParams& p, cudaStream_t stream) {
-  auto kern = chunk_attn_f32<D>;
+  auto kern = chunk_attn_f32<D, LIGHT>;
   const size_t smem = f32_smem_bytes<D>();
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)smem);
   if (e != cudaSuccess) return e;
+  if (p.first) {
+    kern<<<p.grid, kF32Threads, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
   return launch_dependent(kern, dim3(p.grid), dim3(kF32Threads), smem, stream, 0u, p);
 }
 
 cudaError_t launch_chunk_f32(const ServeAttnParams& p, cudaStream_t stream) {
-  return p.D == 128 ? launch_f32<128>(p, stream) : launch_f32<64>(p, stream);
+  if (p.light) return p.D == 128 ? launch_f32<128, true>(p, stream) : launch_f32<64, true>(p, stream);
+  return p.D == 128 ? launch_f32<128, false>(p, stream) : launch_f32<64, false>(p, stream);
 }
 
 }  // namespace specv

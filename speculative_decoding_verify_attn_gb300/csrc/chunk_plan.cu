@@ -30,10 +30,6 @@ constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBins = 256;
 
-__device__ __forceinline__ int chunk_tiles(const ServeAttnParams& p, const SeqInfo& s) {
-  return s.len > 0 ? (int)(((int64_t)s.n * p.G + p.row_tile - 1) / p.row_tile) : 0;
-}
-
 struct PlanTile {
   int b, row0, u0, u1;
 };
@@ -99,12 +95,8 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     }
     PlanTile r;
     r.b = lo;
-    const int n = s_n[lo], len = s_len[lo], base = len - n;
     r.row0 = (t - s_pre[lo]) * p.row_tile;
-    const int last = min(n * p.G, r.row0 + p.row_tile) - 1;
-    const int first_key = p.window > 0 ? max(0, base + r.row0 / p.G + 1 - min(p.window, len)) : 0;
-    r.u0 = first_key / p.unit_keys;
-    r.u1 = (base + last / p.G) / p.unit_keys + 1;
+    tile_units(p, s_n[lo], s_len[lo], r.row0, r.u0, r.u1);
     return r;
   };
   // the usual plan has a tile per thread at most
@@ -279,7 +271,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     int4* dst = reinterpret_cast<int4*>(item);
     dst[0] = make_int4(r.b, r.row0, u0, u1);
     dst[1] = make_int4(slot, s_q0[r.b], n, len);
-    dst[2] = make_int4(p.window > 0 ? max(0, len - n + 1 - min(p.window, len)) : 0, g, 0, 0);
+    dst[2] = make_int4(first_key_of(p, n, len), g, 0, 0);
   };
   if (tid < ctas) {
     int k = 0;
@@ -332,11 +324,19 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     *reinterpret_cast<int4*>(p.plan) = make_int4(small, s_splits, ctas, ctas < p.grid ? ctas : 0);
 }
 
-// CTA 0 makes the plan; the others (if there are new rows) append: CTA 1 + b + B y takes sequence b, a
+// CTA 0 makes the plan (but for light calls); the others (if there are new rows) append: CTA 1 + b + B y takes sequence b, a
 // thread per 16-byte chunk of a row.
 __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_constant__ ServeAttnParams p, int elem) {
   pdl_launch_dependents();
   extern __shared__ int s_seq[];  // [B + 1], [B], [B], [B]
+  if (blockIdx.x == 0 && p.light) {  // no plan: the status only
+    if (threadIdx.x == 0) status_clear_for_launch(p.status);
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
+      const SeqInfo s = seq_info(p, b);
+      if (s.bad) status_report(p.status, s.bad);
+    }
+    return;
+  }
   if (blockIdx.x == 0) {
     plan_body(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1, s_seq + 3 * p.B + 1);
     return;

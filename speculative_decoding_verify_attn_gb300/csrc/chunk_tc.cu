@@ -71,7 +71,7 @@ __device__ __forceinline__ void ct_block_units(const ServeAttnParams& p, const P
   b1 = max(b0, min(it.u1, (base + rl / p.G) / kTcKeys + 1));
 }
 
-template <int D>
+template <int D, bool LIGHT>
 __global__ void __launch_bounds__(kCtThreads, 1)
     chunk_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ ServeAttnParams p) {
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
+  __shared__ LightSeqs s_light;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* qs = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // [block][half][128 rows][128 B]
   uint8_t* stages = qs + 2 * C::kTile;
@@ -111,13 +112,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   tc::fence_after();
   const uint32_t tmem = tmem_base;
   pdl_wait();  // the plan, and appended rows
-  PieceList list;
-  list.init(p);
+  if (LIGHT) light_init(p, s_light);
+  PieceList<LIGHT> list;
+  list.init(p, &s_light);
   const int rounds = list.rounds;
 
   auto fail = [&]() {
     s_abort = 1;
-    atomicOr(p.status, (uint32_t)SPEC_STATUS_TIMEOUT);
+    chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_TIMEOUT);
   };
 
   // registers: 128 x 88 + 256 x 208 = 384 x 168, what the block was launched with
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             const int t = key0 + warp * 64 + i * 32 + lane;
             if (t >= it.s.lo && t < it.s.len) {
               off[i] = key_offset(p, it.s, it.b, it.g, t);
-              if (off[i] < 0) atomicOr(p.status, (uint32_t)SPEC_STATUS_BAD_PAGE);
+              if (off[i] < 0) chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_BAD_PAGE);
             }
           }
         }
@@ -588,18 +590,23 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool LIGHT>
 static cudaError_t launch_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                              cudaStream_t stream) {
-  auto kern = chunk_attn_tc<D>;
+  auto kern = chunk_attn_tc<D, LIGHT>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), (int)Ct<D>::kSmem);
   if (e != cudaSuccess) return e;
+  if (p.first) {
+    kern<<<p.grid, kCtThreads, Ct<D>::kSmem, stream>>>(*tmK, *tmV, p);
+    return cudaGetLastError();
+  }
   return launch_dependent(kern, dim3(p.grid), dim3(kCtThreads), Ct<D>::kSmem, stream, 0u, *tmK, *tmV, p);
 }
 
 cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             cudaStream_t stream) {
-  return p.D == 128 ? launch_tc<128>(p, tmK, tmV, stream) : launch_tc<64>(p, tmK, tmV, stream);
+  if (p.light) return p.D == 128 ? launch_tc<128, true>(p, tmK, tmV, stream) : launch_tc<64, true>(p, tmK, tmV, stream);
+  return p.D == 128 ? launch_tc<128, false>(p, tmK, tmV, stream) : launch_tc<64, false>(p, tmK, tmV, stream);
 }
 
 }  // namespace specv

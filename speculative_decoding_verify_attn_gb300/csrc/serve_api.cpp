@@ -97,7 +97,8 @@ bool encode_kv(CUtensorMap* m, const void* base, const ServeAttnParams& p) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream) {
+// `keys`: more keys than this no row sees.
+int launch_chunk(ServeAttnParams& p, int kv_dtype, int64_t keys, void* ws, cudaStream_t stream) {
   const bool bf16 = kv_dtype == SPEC_BF16;
   p.row_tile = chunk_row_tile(kv_dtype);
   p.unit_keys = bf16 ? specv::kTcKeys : specv::kF32Keys;
@@ -116,10 +117,14 @@ int launch_chunk(ServeAttnParams& p, int kv_dtype, void* ws, cudaStream_t stream
     // a copy of a packed tile is never issued where T < kTcKeys
     p.use_tma = p.tma_page_keys > 0 && encode_kv(&tm[0], p.k, p) && encode_kv(&tm[1], p.v, p);
   }
-  if (specv::launch_chunk_prepare(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  // a tile's rows see at most `keys` keys and those that its tokens lie apart
+  const int64_t span = keys + (p.row_tile + p.G - 1) / p.G;
+  p.light = p.B <= specv::kLightMaxB && span / p.unit_keys + 2 <= specv::kLightUnits;
+  p.first = p.light && !p.k_new;
+  if (!p.first && specv::launch_chunk_prepare(p, elem_bytes(kv_dtype), stream) != cudaSuccess) return SPEC_ERR_CUDA;
   const cudaError_t e = bf16 ? specv::launch_chunk_tc(p, &tm[0], &tm[1], stream) : specv::launch_chunk_f32(p, stream);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
-  return specv::launch_chunk_merge(p, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return p.light || specv::launch_chunk_merge(p, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -186,9 +191,10 @@ int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
   p.o = a->o; p.o_st = a->o_stride_t; p.o_sh = a->o_stride_h;
   if ((p.grid = serve_grid()) < 1) return SPEC_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (!use_mma(a->kv_dtype, s.max_q, p.G)) return launch_chunk(p, a->kv_dtype, a->workspace, cs);
-  // the longest segment a sequence can have: the table's capacity, or its window
   int64_t keys = (int64_t)a->table_cols * a->page_size;
+  if (!use_mma(a->kv_dtype, s.max_q, p.G))
+    return launch_chunk(p, a->kv_dtype, a->window > 0 && a->window < keys ? a->window : keys, a->workspace, cs);
+  // the longest segment a sequence can have: the table's capacity, or its window
   if (a->window > 0 && keys > (int64_t)a->window + s.max_q + 15) keys = (int64_t)a->window + s.max_q + 15;
   p.direct = keys <= specv::kMmaDirectKeys;
   specv::mma_workspace_carve(a->workspace, &p);
@@ -225,7 +231,8 @@ int spec_prefill_attn(const spec_prefill_args* a, spec_stream_t stream) {
   p.kv_st = a->kv_stride_t; p.kv_sh = a->kv_stride_h;
   p.o = a->o; p.o_st = a->o_stride_t; p.o_sh = a->o_stride_h;
   if ((p.grid = serve_grid()) < 1) return SPEC_ERR_CUDA;
-  return launch_chunk(p, a->kv_dtype, a->workspace, reinterpret_cast<cudaStream_t>(stream));
+  return launch_chunk(p, a->kv_dtype, a->window > 0 && a->window < a->T ? a->window : a->T, a->workspace,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ spec_token_logprobs

@@ -73,6 +73,70 @@ __device__ __forceinline__ int64_t o_offset(const ServeAttnParams& p, const SeqI
 }
 
 // ------------------------------------------------------------------ pieces of the chunk kernels
+__device__ __forceinline__ int chunk_tiles(const ServeAttnParams& p, const SeqInfo& s) {
+  return s.len > 0 ? (int)(((int64_t)s.n * p.G + p.row_tile - 1) / p.row_tile) : 0;
+}
+// The key units [u0, u1) that the rows of a tile see, row0 its first, in a chunk of n tokens over len keys.
+__device__ __forceinline__ void tile_units(const ServeAttnParams& p, int n, int len, int row0, int& u0, int& u1) {
+  const int base = len - n, last = min(n * p.G, row0 + p.row_tile) - 1;
+  const int first_key = p.window > 0 ? max(0, base + row0 / p.G + 1 - min(p.window, len)) : 0;
+  u0 = first_key / p.unit_keys;
+  u1 = (base + last / p.G) / p.unit_keys + 1;
+}
+__device__ __forceinline__ int first_key_of(const ServeAttnParams& p, int n, int len) {
+  return p.window > 0 ? max(0, len - n + 1 - min(p.window, len)) : 0;
+}
+// An attention kernel's report: in the call's first kernel only after this launch's clear.
+template <bool LIGHT>
+__device__ __forceinline__ void chunk_report(const ServeAttnParams& p, uint32_t bits) {
+  if (LIGHT && p.first) status_report(p.status, bits);
+  else atomicOr(p.status, bits);
+}
+
+// A light call's sequences, in shared memory: tiles before each, and its numbers.
+struct LightSeqs {
+  int pre[kLightMaxB + 1], q0[kLightMaxB], n[kLightMaxB], len[kLightMaxB];
+};
+// Whole CTA, after the grid-dependency wait: reads the sequences, clears the status where this kernel is
+// the call's first, reports bad sequences and zeros the rows of a bad kv_len.
+__device__ __forceinline__ void light_init(const ServeAttnParams& p, LightSeqs& l) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (p.first && blockIdx.x == 0 && tid == 0) status_clear_for_launch(p.status);
+  if (tid < 32) {
+    int run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < p.B) {
+        const SeqInfo s = seq_info(p, b);
+        n = chunk_tiles(p, s);
+        l.q0[b] = s.q0;
+        l.n[b] = s.n;
+        l.len[b] = s.len;
+        if (p.first && blockIdx.x == 0 && s.bad) status_report(p.status, s.bad);
+      }
+      int x = n;  // at most 2^22 each
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < p.B) l.pre[b] = run + x - n;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) l.pre[p.B] = run;
+  }
+  __syncthreads();
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (l.len[b] > 0 || l.n[b] == 0) continue;
+    for (int64_t i = tid; i < (int64_t)l.n[b] * p.Hq * p.D; i += blockDim.x) {
+      const int64_t r = i / p.D;
+      const int64_t off = (l.q0[b] + r / p.Hq) * p.o_st + (r % p.Hq) * p.o_sh + i % p.D;
+      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(0.f);
+      else reinterpret_cast<float*>(p.o)[off] = 0.f;
+    }
+  }
+}
 struct PieceItem {
   int b, g, row0, u0, u1, slot;
   SeqInfo s;
@@ -83,9 +147,19 @@ struct PieceRaw {
 };
 // The pieces of a CTA: first its share of the cut tiles, then small tiles (sorted by size, dealt forth
 // and back over the CTAs from small_first on).
+template <bool LIGHT>
 struct PieceList {
   int n_big, n_small, first, ctas, rounds;
-  __device__ __forceinline__ void init(const ServeAttnParams& p) {
+  const LightSeqs* light;
+  __device__ __forceinline__ void init(const ServeAttnParams& p, const LightSeqs* seqs) {
+    light = seqs;
+    if (LIGHT) {
+      n_big = first = 0;
+      ctas = (int)gridDim.x;
+      n_small = light->pre[p.B];  // tiles; pieces are that times Hkv
+      rounds = (int)(((int64_t)n_small * p.Hkv + ctas - 1) / ctas);
+      return;
+    }
     const int4 h = __ldcg(reinterpret_cast<const int4*>(p.plan));
     n_big = (int)blockIdx.x < h.z ? __ldcg(p.big_count + blockIdx.x) : 0;
     n_small = h.x * p.Hkv;
@@ -96,7 +170,25 @@ struct PieceList {
   __device__ __forceinline__ PieceRaw fetch(const ServeAttnParams& p, int round) const {
     PieceRaw r;
     r.a = r.b = r.c = make_int4(0, 0, 0, 0);
-    if (round < n_big) {
+    if (LIGHT) {
+      const int64_t idx = (int64_t)round * ctas + blockIdx.x;
+      if (idx < (int64_t)n_small * p.Hkv) {
+        const int t = (int)(idx / p.Hkv);
+        int lo = 0, hi = p.B;  // the last sequence that begins at tile t or before
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (light->pre[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+        const int n = light->n[lo], len = light->len[lo];
+        r.a.x = lo;
+        r.a.y = (t - light->pre[lo]) * p.row_tile;
+        tile_units(p, n, len, r.a.y, r.a.z, r.a.w);
+        r.b = make_int4(-1, light->q0[lo], n, len);
+        r.c.x = first_key_of(p, n, len);
+        r.c.y = (int)(idx - (int64_t)t * p.Hkv);
+      }
+    } else if (round < n_big) {
       const int4* src = reinterpret_cast<const int4*>(p.big + blockIdx.x * kBigPieces + round);
       r.a = __ldcg(src);
       r.b = __ldcg(src + 1);

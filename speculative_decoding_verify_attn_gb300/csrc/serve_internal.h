@@ -47,6 +47,13 @@ constexpr int kBigFraction = 4;
 constexpr int kBigPieces = 8;
 constexpr int kMaxBig = kBigFraction * kServeMaxGrid;
 
+// Light calls: no tile has more than this many units and the batch this many sequences at most, so tiles
+// are not cut, and every CTA works its tiles out by itself: no plan, no merge launch.  Planned and light:
+// 32 chunks over a window of 512 26 and 20 us of device time (with append 26 and 22), a 16K prompt with
+// that window 190 and 173 us.
+constexpr int kLightUnits = 8;
+constexpr int kLightMaxB = 64;
+
 struct ServeAttnParams {
   int B, Hq, Hkv, G, D, T, max_q, window;
   int paged, page_size, num_pages, table_cols;
@@ -70,6 +77,8 @@ struct ServeAttnParams {
   int grid;               // CTAs of the attention kernel
   int direct;             // mma.sync kernel: a CTA per segment, no records
   int row_tile, unit_keys;  // chunk kernels: rows per tile, keys per unit
+  int light;              // chunk kernels: a light call (above)
+  int first;              // chunk kernels: the attention kernel is the call's first and clears the status
   // chunk kernels: what a piece costs beside its units (its rows, its first maximum, its epilogue), and
   // what cutting costs a CTA (a second cut tile's piece, the merge), in units
   float piece_cost, cut_cost;

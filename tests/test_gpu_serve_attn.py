@@ -288,18 +288,23 @@ def test_binding_refusals(sv):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("cols", [0, 200])
 @pytest.mark.parametrize("q_len", [[2, 3, 1, 4], [40, 3, 1, 20]])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_bad_data_is_flagged_and_contained(sv, q_len, dtype):
+def test_bad_data_is_flagged_and_contained(sv, q_len, dtype, cols):
+    """cols: table columns beyond what the sequences need (a larger capacity takes other kernels)."""
     torch = torch_mod()
     kv_len = [300, 200, 500, 250]
     p = Paged(q_len, kv_len, 8, 2, 64, 16, dtype=dtype, append=True, seed=80)
+    p.table = np.concatenate([p.table, np.full((4, cols), -9, dtype=np.int32)], axis=1)
+    p.d_table = torch.from_numpy(p.table).cuda()
+    capacity = 16 * p.table.shape[1]
     (ref, A, S), kp, vp = p.oracle()
     rows = lambda b: slice(p.start[b], p.start[b + 1])  # noqa: E731
     good = p.run(sv)[0]
     check(good[rows(0)], ref[rows(0)], A[rows(0)], S, 64, 500, dtype, "f32")
     # a length above the table's capacity, and one below the chunk's
-    for bad in (32 * 16 + 1, q_len[1] - 1, -4):
+    for bad in (capacity + 1, q_len[1] - 1, -4):
         p.d_len[1] = bad
         before = np64(p.k)
         o, st = p.run(sv)
@@ -309,6 +314,17 @@ def test_bad_data_is_flagged_and_contained(sv, q_len, dtype):
         for b in (0, 2, 3):
             assert np.max(np.abs(o[rows(b)] - good[rows(b)])) < 1e-2
     p.d_len[1] = 200
+    # the same with no append, where a call has the least kernels
+    new, p.d_new = p.d_new, {}
+    p.d_len[1] = capacity + 1
+    o, st = p.run(sv)
+    assert st == sv.SPEC_STATUS_BAD_KV_LEN and np.all(o[rows(1)] == 0)
+    p.d_len[1] = 200
+    p.d_table[2, 3] = -1
+    o, st = p.run(sv)
+    assert st == sv.SPEC_STATUS_BAD_PAGE and np.all(np.isfinite(o[p.start[0]:p.start[-1]]))
+    p.d_table[2, 3] = int(p.table[2, 3])
+    p.d_new = new
     # page ids out of range
     for bad in (-1, p.k.shape[0], 2 ** 31 - 1):
         p.d_table[2, 3] = bad
