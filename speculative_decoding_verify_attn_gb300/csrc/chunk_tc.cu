@@ -12,6 +12,7 @@
 //                 wholly inside the sequence comes by TMA; edges (the sequence's end, tokens before the
 //                 window, bad page ids) and pages too small for TMA by cp.async with zeros in the gaps,
 //                 so nothing outside [lo, len) reaches the tensor core, NaN or not.
+//   warp 3        relay of cp.async tiles to the tensor core.
 //   warp 2        MMA issuer (one lane): P V of a tile and Q K^T of the next for block 0, then for block
 //                 1.  One issuer, because products of two issuers interleave in the tensor pipe: both
 //                 blocks' scores are then ready at the same time, and the blocks run in step instead
@@ -45,7 +46,6 @@ constexpr int kCtHalf = 128 * 128;  // 128 rows of one 64-column half: 16 KB
 // A row's sum over one tile up to which its reference stays (P is then below it, far inside bf16's and
 // fp32's range, and the final division removes the reference).
 constexpr float kCtMaxSum = 1048576.f;
-constexpr int kCtLag = 2;           // steps a loader's cp.async tiles may be in flight
 
 template <int D>
 struct Ct {
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   constexpr int NS = C::kStages;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ uint64_t full[NS], empty[NS], landed[NS];
   __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 2);   // one arrival per loader warp
+      mbar_init(&full[i], 2);     // warp 0 (with the bytes of a TMA copy) and the relay
+      mbar_init(&landed[i], 64);  // every loader thread, once its copies have landed
       mbar_init(&empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -132,14 +133,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const __nv_bfloat16* kv[2] = {reinterpret_cast<const __nv_bfloat16*>(p.k),
                                   reinterpret_cast<const __nv_bfloat16*>(p.v)};
     int step = 0;
-    uint32_t by_copy = 0;  // bit i: the step i + 1 before the current one was filled by cp.async
     bool ok = true;
-    // the step kCtLag before has landed: hand its stage over if it was filled by cp.async
-    auto hand_over = [&](int done) {
-      tc::fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[done % NS]);
-    };
     PieceRaw ahead = list.fetch(p, 0);
     for (int round = 0; ok && round < rounds; ++round) {
       const PieceItem it = piece_item(ahead);
@@ -183,9 +177,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
           const uint32_t dst = stages_u32 + s * C::kTile;
           if (tma) {
-            if (warp == 1) {
-              if (lane == 0) mbar_arrive(&full[s]);
-            } else {
+            if (warp == 0) {
               if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)C::kTile);
               __syncwarp();
               // whole tiles in one copy; pages below a tile in one copy per page and half
@@ -230,22 +222,43 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                          kv[x] + (so < 0 ? 0 : so) + c * 8, so >= 0);
             }
           }
-          cp_async_commit();
-          cp_async_wait<kCtLag>();
-          if ((by_copy >> (kCtLag - 1)) & 1u) hand_over(step - kCtLag);
-          by_copy = (by_copy << 1) | (tma ? 0u : 1u);
+          if (tma) {
+            mbar_arrive(&landed[s]);  // after warp 0 has announced the bytes
+          } else {
+            cp_async_track(&landed[s]);
+            if (warp == 0 && lane == 0) mbar_arrive(&full[s]);
+          }
         }
       }
     }
+    cp_async_commit();
     cp_async_wait<0>();
-#pragma unroll
-    for (int i = kCtLag; i >= 1; --i)
-      if ((by_copy >> (i - 1)) & 1u) hand_over(step - i);
     if (!ok || s_abort) {
       // copies still in flight into this CTA
       for (int i = 1; i <= min(step, NS); ++i) mbar_wait_spin(&full[(step - i) % NS], ((step - i) / NS) & 1, nullptr);
     }
   } else if (warp < 4) {
+    if (warp == 3 && elect_one()) {
+      // ---------------------------------------------------------------- relay: cp.async tiles that have landed
+      // are made visible to the tensor core, which reads them through the async proxy, so that neither the
+      // loaders nor the issuer wait for that
+      int step = 0;
+      bool ok = true;
+      PieceRaw ahead = list.fetch(p, 0);
+      for (int round = 0; ok && round < rounds; ++round) {
+        const int steps = 2 * (ahead.a.w - ahead.a.z);
+        ahead = list.fetch(p, round + 1);
+        for (int i = 0; i < steps; ++i, ++step) {
+          if (!mbar_wait_spin(&landed[step % NS], (step / NS) & 1, &s_abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_proxy_async_smem();
+          mbar_arrive(&full[step % NS]);
+        }
+      }
+      if (!ok) fail();
+    }
     // ------------------------------------------------------------------ MMA issuer (warp 2, one lane)
     if (warp == 2 && elect_one()) {
       int step = 0, part[2] = {0, 0}, t[2] = {0, 0};  // pieces and tiles so far, by block
