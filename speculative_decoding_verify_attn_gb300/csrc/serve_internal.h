@@ -22,8 +22,8 @@ constexpr int kMmaDirectKeys = 4 * kMmaUnit;
 constexpr int kTcRows = 256;    // query rows per tile of the tcgen05 kernel (two blocks of 128)
 constexpr int kTcKeys = 128;    // keys per unit of work of the tcgen05 kernel
 // Tokens per page from which the tcgen05 kernel copies pages by TMA, below cp.async.  A 2048-token chunk at
-// 32K by TMA and by cp.async: pages of 16 961 and 781 us, of 32 754 and 767, of 64 681 and 751.
-constexpr int kTmaMinPage = 32;
+// 32K by TMA and by cp.async: pages of 16 961 and 753 us, of 32 763 and 722, of 64 674 and 706.
+constexpr int kTmaMinPage = 64;
 constexpr int kF32Rows = 64;    // query rows per tile of the fp32 kernel
 constexpr int kF32Keys = 64;    // keys per unit of work of the fp32 kernel
 
