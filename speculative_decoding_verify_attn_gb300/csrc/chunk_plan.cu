@@ -4,9 +4,9 @@
 // A row tile (row_tile consecutive rows of one sequence's chunk, for one kv head) needs the key units
 // its rows see; under the causal mask these differ from tile to tile, and lengths are known on the
 // device only.  One CTA therefore plans each call.  With U units in all a CTA's share is
-// per = U / grid.  If cutting pays (see `cut` below), tiles of more than per / 4 units ("big") go to as many CTAs as they fill: first whole
-// tiles, one per CTA and wave, for as many waves as leave every CTA short of its share; the rest is
-// laid end to end and cut so as to fill each CTA up to its share.  Shares are thus equal to a unit,
+// per = U / grid.  If cutting pays (see `cut` below), tiles of more than per / 4 units ("big") go to as many
+// CTAs as they fill: first whole tiles, one per CTA and wave, for as many waves as leave every CTA short
+// of its share; the rest is laid end to end and cut so as to fill each CTA up to its share.  Shares are thus equal to a unit,
 // leave at most two records each (a cut tile at either end), and CTAs on the same keys (row tiles of
 // one sequence and head) start on them together, which keeps those keys in L2: with everything cut at
 // equal distances, a 2048-token chunk at 32K ran at the HBM rate of its 134 MB of keys.  The other tiles

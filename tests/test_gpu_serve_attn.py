@@ -445,7 +445,8 @@ def test_streams_and_determinism(sv, q_len):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D,Hq,Hkv,lens,window", [
     (64, 4, 1, [7, 130, 1, 0, 65], 0), (128, 8, 2, [300], 0), (128, 6, 2, [1, 1, 2, 257], 0),
-    (64, 8, 8, [129, 400], 64), (128, 32, 4, [20, 0, 33], 1), (64, 32, 1, [90], 0)])
+    (64, 8, 8, [129, 400], 64), (128, 32, 4, [20, 0, 33], 1), (64, 32, 1, [90], 0), (128, 2, 1, [700, 3, 0, 300], 0),
+    (64, 4, 2, [900], 200)])
 def test_prefill(sv, dtype, D, Hq, Hkv, lens, window):
     torch = torch_mod()
     g = torch.Generator().manual_seed(sum(lens) + D)
@@ -467,6 +468,30 @@ def test_prefill(sv, dtype, D, Hq, Hkv, lens, window):
         got, r = np64(o), slice(lead, start[-1])
         check(got[r], ref[r], A[r], S, D, max(lens), dtype, o_dtype)
         assert np.all(got[:lead] == SENTINEL) and np.all(got[start[-1]:] == SENTINEL)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [300, 1500])
+def test_prefill_bad_ranges(sv, T, dtype):
+    """Sequences whose range is out of order have no output; their neighbours' is right."""
+    torch = torch_mod()
+    g = torch.Generator().manual_seed(T)
+    q, k, v = (torch.randn(T, h, 64, generator=g).to(dt(dtype)) for h in (2, 1, 1))
+    good = np.array([0, 90, 200, 260], dtype=np.int32)
+    ref, A, S = os_.prefill_attn(np64(q)[:260], np64(k)[:260], np64(v)[:260], good)
+    for bad, rows, none in (([0, 90, 200, T + 1], slice(0, 200), slice(200, T)),
+                            ([0, 90, 40, 260], slice(0, 40), slice(260, T)),
+                            ([-1, 90, 200, 260], slice(90, 260), slice(0, 90))):
+        o = torch.full((T, 2, 64), SENTINEL, device="cuda")
+        start = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        dq, dk = q.cuda(), k.cuda()
+        ws = torch.empty(sv.spec_prefill_attn_workspace(dq, dk, start, o), dtype=torch.uint8, device="cuda")
+        sv.spec_prefill_attn(dq, dk, v.cuda(), start, o, workspace=ws)
+        torch.cuda.synchronize()
+        got = np64(o)
+        assert sv.read_status(ws) == sv.SPEC_STATUS_BAD_RANGE
+        check(got[rows], ref[rows], A[rows], S, 64, 200, dtype, "f32")
+        assert np.all(got[none] == SENTINEL)
 
 
 def test_prefill_neighbours_do_not_leak(sv):
