@@ -145,7 +145,7 @@ struct PieceItem {
   int b, g, row0, u0, u1, slot;
   SeqInfo s;
 };
-// A piece as it lies in memory (u0 == u1: none).  Readers fetch a piece ahead.
+// A piece as it lies in memory (u0 == u1: none, and no record).  Readers fetch a piece ahead.
 struct PieceRaw {
   int4 a, b, c;
 };
@@ -173,7 +173,8 @@ struct PieceList {
   }
   __device__ __forceinline__ PieceRaw fetch(const ServeAttnParams& p, int round) const {
     PieceRaw r;
-    r.a = r.b = r.c = make_int4(0, 0, 0, 0);
+    r.a = r.c = make_int4(0, 0, 0, 0);
+    r.b = make_int4(-1, 0, 0, 0);
     if (LIGHT) {
       const int64_t idx = (int64_t)round * ctas + blockIdx.x;
       if (idx < (int64_t)n_small * p.Hkv) {

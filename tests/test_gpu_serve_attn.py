@@ -239,6 +239,18 @@ def test_most_sequences(sv, q):
     p.verify(sv, max_q=10 ** 6)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+def test_cut_tile_beside_uneven_rounds(sv, page, D):
+    # a long sequence whose tiles are cut, the first piece on CTA 0 early, and 900 small tiles that do not fill
+    # their last round: the CTAs that go without leave the cut tiles' records alone
+    case = Paged([64] + [64] * 450, [16384] + [64] * 450, 8, 2, D, page, append=True, seed=41)
+    first = case.verify(sv)
+    for _ in range(4):
+        o, st = case.run(sv)
+        assert st == 0 and np.array_equal(o, first, equal_nan=True)
+
+
 @pytest.mark.parametrize("G", [1, 4, 16])
 @pytest.mark.parametrize("rows", [16, 17, 32, 33, 128, 129, 256, 257])
 def test_row_boundaries(sv, rows, G):
