@@ -125,6 +125,11 @@ def _vector(name, t, n, dtype):
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n}, got {t.dtype} {tuple(t.shape)}")
 
 
+def _handle(stream) -> int:
+    """A stream as its raw handle."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 _sizes = {}
 
 
@@ -147,8 +152,18 @@ def _call(name, args, sizes, index, workspace, stream):
             _sizes.clear()
         _sizes[sizes] = need
     handle = torch._C._cuda_getCurrentRawStream(index)
+    other = None  # a stream other than the current one
+    if stream is not None:
+        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream))
+        if own.cuda_stream != handle:
+            other, handle = own, own.cuda_stream
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        if other is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        else:
+            # from the launching stream's pool: a block of the current stream's may still be in use there
+            with torch.cuda.stream(other):
+                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
         given = need
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
@@ -156,12 +171,9 @@ def _call(name, args, sizes, index, workspace, stream):
         given = workspace.numel() * workspace.element_size()
         if given < need:
             raise ValueError(f"workspace too small: need {need} bytes")
-    if stream is not None:
-        own = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        if own.cuda_stream != handle:
+        if other is not None:
             # its memory is not handed out again before the other stream has passed this call
-            workspace.record_stream(own)
-        handle = own.cuda_stream
+            workspace.record_stream(other)
     args.workspace = workspace.data_ptr()
     args.workspace_bytes = given
     st = getattr(L, name)(ref, handle)
