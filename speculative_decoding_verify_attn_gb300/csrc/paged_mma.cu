@@ -490,12 +490,14 @@ __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_cons
   before = block_sum(before, s_scan) * p.Hkv;
   const SeqInfo s = seq_info(p, b);
   const int nu = mma_units(s);
-  if (r >= s.n * p.G) return;
   const int64_t per = mma_per_cta(total, p.grid);
   const int64_t start = before + (int64_t)g * nu;
   const int64_t c0 = start / per;
   const int n = nu > 0 ? (int)((start + nu - 1) / per - c0) + 1 : 0;
-  if (n == 1) return;  // written by its CTA
+  // every CTA waits, those with nothing to join too: what follows in the stream is ordered behind this grid
+  // alone, and a grid that has not waited can be over before the attention kernel is
+  pdl_wait();
+  if (r >= s.n * p.G || n == 1) return;  // n == 1: written by its CTA
   // record i: CTA c0 + i's first, but for c0's second where the segment does not start where c0 does
   const int64_t first = 2 * c0 + (nu > 0 && start % per == 0 ? 0 : 1);
   constexpr int E = D / 32;
@@ -503,7 +505,6 @@ __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_cons
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   float M = neg_inf(), L = 0.f;
-  pdl_wait();
   for (int i0 = 0; i0 < n; i0 += kMmaMergeBatch) {
     float2 ml[kMmaMergeBatch];
     float v[kMmaMergeBatch][E];
