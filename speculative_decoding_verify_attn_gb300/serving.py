@@ -112,10 +112,13 @@ def _check(tensors) -> int:
 
 
 def _rows(name, t):
-    """The strides of a tensor whose innermost dimension has to be contiguous."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    """The strides of a tensor whose innermost dimension has to be contiguous.  A dimension of one element
+    is never stepped over, so its stride may be anything; a row's length stands in its place."""
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: innermost dimension must be contiguous")
+    if 1 in shape:
+        return tuple(shape[-1] if n == 1 else x for n, x in zip(shape, st))
     return st
 
 
@@ -198,7 +201,7 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
     pages, Hkv, page_size, D2 = shape
     B, cols = page_table.shape
     qs, ks, os_, ts = _rows("q", q), _rows("k_pages", k_pages), _rows("o", o), _rows("page_table", page_table)
-    if D2 != D or v_pages.shape != shape or v_pages.stride() != ks:
+    if D2 != D or v_pages.shape != shape or _rows("v_pages", v_pages) != ks:
         raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with q's D and equal strides")
     if v_pages.dtype is not k_pages.dtype:
         raise TypeError("k_pages and v_pages must share a dtype")
@@ -214,7 +217,7 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
         if k_new is None or v_new is None:
             raise ValueError("k_new and v_new go together")
         ns = _rows("k_new", k_new)
-        if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or v_new.stride() != ns:
+        if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or _rows("v_new", v_new) != ns:
             raise ValueError("k_new, v_new must be [T, Hkv, D] with equal strides")
         if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
             raise TypeError("k_new, v_new must have the cache's dtype")
@@ -257,7 +260,7 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     _torch or _t()
     T, Hq, D = q.shape
     qs, ks, os_ = _rows("q", q), _rows("k", k), _rows("o", o)
-    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or v.stride() != ks:
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or _rows("v", v) != ks:
         raise ValueError("k, v must be [T, Hkv, D] with equal strides")
     if v.dtype is not k.dtype:
         raise TypeError("k and v must share a dtype")
@@ -315,9 +318,8 @@ def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None,
                 raise ValueError(f"{name} must be contiguous {dtype} of shape {(N, K)}")
         if K:
             ids, top = top_ids.data_ptr(), top_logprobs.data_ptr()
-    # the stride of a single row may be anything
-    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0] if N > 1 else V,
-                           tok, lp, ent, ids, top, None, 0)
+    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0], tok, lp, ent,
+                           ids, top, None, 0)
 
 
 def spec_token_logprobs_workspace(logits, K: int = 0) -> int:

@@ -1,0 +1,58 @@
+"""What the serving binding makes of its tensors, on the host: the argument structs are filled without a GPU."""
+
+import pytest
+import torch
+
+from speculative_decoding_verify_attn_gb300 import serving as s
+
+I32 = torch.int32
+
+
+def odd(*shape, dtype=torch.bfloat16):
+    """A tensor whose dimensions of one element have strides that no vector access could use."""
+    strides, at = [], 1
+    for n in reversed(shape):
+        strides.insert(0, at if n > 1 or not strides else 3 * at + 1)
+        at *= n
+    strides[-1] = 1
+    return torch.empty_strided(shape, strides, dtype=dtype)
+
+
+def aligned(args, names, dtype):
+    per = 16 // dtype.itemsize
+    return [x for x in names if getattr(args, x) % per or getattr(args, x) < 1]
+
+
+PAGED = ["q_stride_t", "q_stride_h", "kv_stride_p", "kv_stride_h", "kv_stride_t", "new_stride_t", "new_stride_h"]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,Hq,Hkv,pages,page", [(1, 4, 2, 3, 16), (1, 1, 1, 1, 1), (5, 1, 1, 3, 16), (5, 4, 2, 1, 16),
+                                                 (1, 32, 1, 8, 1)])
+def test_strides_of_single_elements_do_not_matter(T, Hq, Hkv, pages, page, dtype):
+    q, o = odd(T, Hq, 64, dtype=dtype), odd(T, Hq, 64, dtype=torch.float32)
+    k, v = odd(pages, Hkv, page, 64, dtype=dtype), torch.empty(pages, Hkv, page, 64, dtype=dtype)
+    kn, vn = odd(T, Hkv, 64, dtype=dtype), torch.empty(T, Hkv, 64, dtype=dtype)
+    table, start, lens = torch.zeros((1, 4), dtype=I32), torch.zeros(2, dtype=I32), torch.zeros(1, dtype=I32)
+    a = s.paged_attn_args(q, k, v, table, start, lens, o, max_q=T, k_new=kn, v_new=vn)
+    assert aligned(a, PAGED, dtype) == []
+    # the others are as they were
+    assert T == 1 or a.q_stride_t == q.stride(0)
+    assert page == 1 or a.kv_stride_t == k.stride(2)
+    assert pages == 1 or a.kv_stride_p == k.stride(0)
+    a = s.prefill_attn_args(q, odd(T, Hkv, 64, dtype=dtype), torch.empty(T, Hkv, 64, dtype=dtype), start, o)
+    assert aligned(a, ["q_stride_t", "q_stride_h", "kv_stride_t", "kv_stride_h"], dtype) == []
+
+
+def test_unequal_strides_are_still_refused():
+    z = torch.zeros
+    ok = dict(q=z(4, 4, 64), k_pages=z(3, 2, 16, 64), v_pages=z(3, 2, 16, 64), page_table=z((1, 2), dtype=I32),
+              q_start=z(2, dtype=I32), kv_len=z(1, dtype=I32), o=z(4, 4, 64), max_q=4)
+    with pytest.raises(ValueError):
+        s.paged_attn_args(**dict(ok, v_pages=z(3, 16, 2, 64).transpose(1, 2)))
+    with pytest.raises(ValueError):
+        s.paged_attn_args(**dict(ok, k_new=z(4, 2, 64), v_new=z(4, 3, 64)[:, :2]))
+    with pytest.raises(ValueError):
+        s.prefill_attn_args(ok["q"], z(4, 2, 64), z(4, 3, 64)[:, :2], ok["q_start"], ok["o"])
+    with pytest.raises(ValueError):
+        s.paged_attn_args(**dict(ok, q=z(4, 64, 4).transpose(1, 2)))
