@@ -9,6 +9,7 @@ device (or on ``stream``).  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 from ctypes import POINTER, Structure, byref, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 from .binding import SPEC_BF16, SPEC_ERR_INVALID_ARG, SPEC_F32, SPEC_OK, SpecError, lib
@@ -122,6 +123,21 @@ def _rows(name, t):
     return st
 
 
+_TOP = 2 ** 31 - 1
+
+
+def _whole(x) -> int:
+    """A caller's whole number for a 32-bit field: what lies past 32 bits stays as large (or below zero) as the
+    field can say, which for a window or a bound on lengths is the same."""
+    x = operator.index(x)
+    return x if -1 <= x <= _TOP else _TOP if x > 0 else -1
+
+
+def _size(n) -> int:
+    """A tensor's size for a 32-bit field; the largest value is above every limit of the calls."""
+    return n if n <= _TOP else _TOP
+
+
 def _vector(name, t, n, dtype):
     """Checks a contiguous vector of n elements."""
     if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
@@ -223,16 +239,16 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
             raise TypeError("k_new, v_new must have the cache's dtype")
         kn, vn = k_new.data_ptr(), v_new.data_ptr()
     return SpecPagedArgs(
-        B, Hq, Hkv, D, T, max_q, _dtype_code(q), _dtype_code(k_pages), _dtype_code(o), page_size, pages, cols, window,
-        scale, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2],
-        page_table.data_ptr(), ts[0], q_start.data_ptr(), kv_len.data_ptr(), kn, vn, ns[0], ns[1], o.data_ptr(),
-        os_[0], os_[1], None, 0)
+        _size(B), Hq, Hkv, D, _size(T), _whole(max_q), _dtype_code(q), _dtype_code(k_pages), _dtype_code(o),
+        _size(page_size), _size(pages), _size(cols), _whole(window), scale, q.data_ptr(), qs[0], qs[1],
+        k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], page_table.data_ptr(), ts[0], q_start.data_ptr(),
+        kv_len.data_ptr(), kn, vn, ns[0], ns[1], o.data_ptr(), os_[0], os_[1], None, 0)
 
 
 def spec_paged_attn_workspace(q, k_pages, page_table, o, *, max_q) -> int:
     """Bytes of workspace spec_paged_attn needs for tensors of these shapes."""
     T, Hq, D = q.shape
-    a = SpecPagedArgs(B=page_table.shape[0], Hq=Hq, Hkv=k_pages.shape[1], D=D, T=T, max_q=int(max_q),
+    a = SpecPagedArgs(B=_size(page_table.shape[0]), Hq=Hq, Hkv=k_pages.shape[1], D=D, T=_size(T), max_q=_whole(max_q),
                       q_dtype=_dtype_code(q), kv_dtype=_dtype_code(k_pages), o_dtype=_dtype_code(o))
     return _workspace_bytes("spec_paged_attn", a)
 
@@ -269,14 +285,15 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     B = seq_start.shape[0] - 1
     _vector("seq_start", seq_start, B + 1, _i32)
     return SpecPrefillArgs(
-        B, Hq, k.shape[1], D, T, window, _dtype_code(q), _dtype_code(k), _dtype_code(o), scale, q.data_ptr(), qs[0],
-        qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(), o.data_ptr(), os_[0], os_[1], None, 0)
+        _size(B), Hq, k.shape[1], D, _size(T), _whole(window), _dtype_code(q), _dtype_code(k), _dtype_code(o), scale,
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(), o.data_ptr(),
+        os_[0], os_[1], None, 0)
 
 
 def spec_prefill_attn_workspace(q, k, seq_start, o) -> int:
     """Bytes of workspace spec_prefill_attn needs for tensors of these shapes."""
     T, Hq, D = q.shape
-    a = SpecPrefillArgs(B=seq_start.shape[0] - 1, Hq=Hq, Hkv=k.shape[1], D=D, T=T, q_dtype=_dtype_code(q),
+    a = SpecPrefillArgs(B=_size(seq_start.shape[0] - 1), Hq=Hq, Hkv=k.shape[1], D=D, T=_size(T), q_dtype=_dtype_code(q),
                         kv_dtype=_dtype_code(k), o_dtype=_dtype_code(o))
     return _workspace_bytes("spec_prefill_attn", a)
 
@@ -318,14 +335,14 @@ def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None,
                 raise ValueError(f"{name} must be contiguous {dtype} of shape {(N, K)}")
         if K:
             ids, top = top_ids.data_ptr(), top_logprobs.data_ptr()
-    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0], tok, lp, ent,
-                           ids, top, None, 0)
+    return SpecLogprobArgs(_size(N), _size(V), _size(K), _dtype_code(logits), logits.data_ptr(),
+                           _rows("logits", logits)[0], tok, lp, ent, ids, top, None, 0)
 
 
 def spec_token_logprobs_workspace(logits, K: int = 0) -> int:
     """Bytes of workspace spec_token_logprobs needs for these logits and K alternatives."""
-    return _workspace_bytes("spec_token_logprobs", SpecLogprobArgs(N=logits.shape[0], V=logits.shape[1], K=K,
-                                                                   dtype=_dtype_code(logits)))
+    return _workspace_bytes("spec_token_logprobs", SpecLogprobArgs(N=_size(logits.shape[0]), V=_size(logits.shape[1]),
+                                                                   K=_whole(K), dtype=_dtype_code(logits)))
 
 
 def spec_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None, workspace=None,

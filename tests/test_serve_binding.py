@@ -56,3 +56,49 @@ def test_unequal_strides_are_still_refused():
         s.prefill_attn_args(ok["q"], z(4, 2, 64), z(4, 3, 64)[:, :2], ok["q_start"], ok["o"])
     with pytest.raises(ValueError):
         s.paged_attn_args(**dict(ok, q=z(4, 64, 4).transpose(1, 2)))
+
+
+def paged(**kw):
+    z = torch.zeros
+    return dict(dict(q=z(4, 4, 64), k_pages=z(3, 2, 16, 64), v_pages=z(3, 2, 16, 64), page_table=z((1, 2), dtype=I32),
+                     q_start=z(2, dtype=I32), kv_len=z(1, dtype=I32), o=z(4, 4, 64), max_q=4), **kw)
+
+
+@pytest.mark.parametrize("value,kept", [(3, 3), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
+                                        (2 ** 32 + 1, 2 ** 31 - 1), (2 ** 63 - 1, 2 ** 31 - 1), (2 ** 70 + 5, 2 ** 31 - 1),
+                                        (-1, -1), (-2 ** 31 - 1, -1), (-2 ** 32 + 5, -1)])
+def test_numbers_past_32_bits(value, kept):
+    """A window or a bound on the chunk lengths past 32 bits is more than any sequence has, a negative one stays
+    negative (and is refused by the call)."""
+    a = s.paged_attn_args(**paged(window=value, max_q=value))
+    assert (a.window, a.max_q) == (kept, kept)
+    z = torch.zeros
+    assert s.prefill_attn_args(z(4, 2, 64), z(4, 2, 64), z(4, 2, 64), z(2, dtype=I32), z(4, 2, 64),
+                               window=value).window == kept
+
+
+def test_numbers_that_are_not_whole():
+    for bad in (2.0, "3", None):
+        for name in ("window", "max_q"):
+            with pytest.raises(TypeError):
+                s.paged_attn_args(**paged(**{name: bad}))
+        with pytest.raises(TypeError):
+            s.spec_paged_attn_workspace(*(paged()[x] for x in ("q", "k_pages", "page_table", "o")), max_q=bad)
+
+
+def test_sizes_past_32_bits_stay_too_large():
+    """Rows and vocabularies past 32 bits keep a size that the call refuses (shapes without memory)."""
+    big = 2 ** 32 + 5
+    logits = torch.empty(1, device="meta").expand(big, 3)
+    for x, K in ((logits, 2), (logits.T, 2), (logits[:2], big)):
+        with pytest.raises(s.SpecError):
+            s.spec_token_logprobs_workspace(x, K)
+    q = torch.empty(1, device="meta", dtype=torch.bfloat16).expand(big, 4, 64)
+    kp = torch.empty(1, device="meta", dtype=torch.bfloat16).expand(big, 2, 16, 64)
+    table = torch.empty(1, device="meta", dtype=I32).expand(big, 3)
+    with pytest.raises(s.SpecError):
+        s.spec_paged_attn_workspace(q, kp, table[:1], q, max_q=4)
+    with pytest.raises(s.SpecError):
+        s.spec_paged_attn_workspace(q[:4], kp, table, q, max_q=4)
+    with pytest.raises(s.SpecError):
+        s.spec_prefill_attn_workspace(q, q[:, :2], torch.zeros(2, dtype=I32), q)
