@@ -59,8 +59,8 @@ enum {
  *   aligned) and the int32 ones are 16-byte aligned.
  * Limits: D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 32; 1 <= B <= 4096; 0 <= T <= 2^22 (T == 0:
  *   nothing is launched); max_q >= 1; 1 <= page_size <= 65536; table_cols >= 1;
- *   table_cols * page_size <= 2^30; window >= 0; scale >= 0 and finite.  max_q is an upper bound on
- *   every n_b and chooses the kernel; a tight one is faster.
+ *   table_cols * page_size <= 2^30; window >= 0; scale >= 0, scale * log2(e) finite.  max_q is an upper
+ *   bound on every n_b and chooses the kernel; a tight one is faster.
  * No output overlaps an input: not o, nor the pages with k_new / v_new.
  * Rows of q at or past q_start[B], or before q_start[0], are not read and their o is left as it was.
  * Data errors: a sequence whose q_start is out of order (SPEC_STATUS_BAD_RANGE) has no rows, and
@@ -69,8 +69,9 @@ enum {
  *   gives zeros and no append; a needed page id out of range (SPEC_STATUS_BAD_PAGE) is never
  *   followed: its tokens read as zeros (o of the rows that see them is not meaningful) and are not
  *   written (appended rows then take part from k_new / v_new, or as zeros).
- * K and V of the tokens that some row of the chunk sees have to be finite; slots past kv_len and
- *   pages before the window may hold anything.
+ * K and V of the tokens that some row of the chunk sees have to be finite, and so do a row's scores times
+ *   scale * log2(e) in fp32 (else that row's o is unspecified); slots past kv_len and pages before the
+ *   window may hold anything.
  * Accumulation is fp32 (scores, softmax statistics, P.V); for bf16 K/V the probabilities are
  *   rounded to bf16 before P.V, as in spec_verify_attn.  A call's result is the same every time; it
  *   can differ in the last bits between batches (and devices), whose work is cut differently.

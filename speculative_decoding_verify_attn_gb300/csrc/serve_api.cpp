@@ -68,13 +68,17 @@ bool use_mma(int kv_dtype, int max_q, int G) {
 }
 int chunk_row_tile(int kv_dtype) { return kv_dtype == SPEC_BF16 ? specv::kTcRows : specv::kF32Rows; }
 
+constexpr float kLog2e = 1.4426950408889634f;
+// what multiplies the scores, scale * log2(e), has to be finite as well
+bool good_scale(float scale) { return scale >= 0.f && isfinite(scale * kLog2e); }
+
 ServeAttnParams base_params(const Shape& s, float scale) {
   ServeAttnParams p;
   memset(&p, 0, sizeof(p));
   p.B = s.B; p.Hq = s.Hq; p.Hkv = s.Hkv; p.G = s.Hq / s.Hkv; p.D = s.D; p.T = s.T; p.max_q = s.max_q;
   p.window = s.window;
   p.o_bf16 = s.o_dtype == SPEC_BF16;
-  p.scale_log2 = (scale != 0.f ? scale : 1.0f / sqrtf((float)s.D)) * 1.4426950408889634f;
+  p.scale_log2 = (scale != 0.f ? scale : 1.0f / sqrtf((float)s.D)) * kLog2e;
   return p;
 }
 
@@ -163,7 +167,7 @@ int spec_paged_attn(const spec_paged_args* a, spec_stream_t stream) {
   if (a->page_size < 1 || a->page_size > 65536 || a->num_pages < 1 || a->table_cols < 1 || a->table_stride < 0 ||
       (int64_t)a->table_cols * a->page_size > (1 << 30))
     return SPEC_ERR_INVALID_ARG;
-  if (!isfinite(a->scale) || a->scale < 0.f) return SPEC_ERR_INVALID_ARG;
+  if (!good_scale(a->scale)) return SPEC_ERR_INVALID_ARG;
   if ((a->k_new == nullptr) != (a->v_new == nullptr)) return SPEC_ERR_INVALID_ARG;
   if (a->T == 0) return SPEC_OK;
   if (!vector_layout(a->q, a->q_dtype, a->q_stride_t, a->q_stride_h) ||
@@ -216,7 +220,7 @@ int spec_prefill_attn(const spec_prefill_args* a, spec_stream_t stream) {
   const Shape s = prefill_shape(a);
   int st = check_shape(s);
   if (st != SPEC_OK) return st;
-  if (!isfinite(a->scale) || a->scale < 0.f) return SPEC_ERR_INVALID_ARG;
+  if (!good_scale(a->scale)) return SPEC_ERR_INVALID_ARG;
   if (a->T == 0) return SPEC_OK;
   if (!vector_layout(a->q, a->q_dtype, a->q_stride_t, a->q_stride_h) ||
       !vector_layout(a->k, a->kv_dtype, a->kv_stride_t, a->kv_stride_h) || !vector_layout(a->v, a->kv_dtype, 0, 0) ||

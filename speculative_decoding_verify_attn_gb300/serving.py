@@ -133,6 +133,13 @@ def _whole(x) -> int:
     return x if -1 <= x <= _TOP else _TOP if x > 0 else -1
 
 
+def _scale(x) -> float:
+    """A caller's scale; one that is 0 in 32 bits would be taken for the default."""
+    if x and c_float(x).value == 0:
+        raise ValueError(f"scale {x} is 0 in 32 bits")
+    return x
+
+
 def _size(n) -> int:
     """A tensor's size for a 32-bit field; the largest value is above every limit of the calls."""
     return n if n <= _TOP else _TOP
@@ -240,7 +247,7 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
         kn, vn = k_new.data_ptr(), v_new.data_ptr()
     return SpecPagedArgs(
         _size(B), Hq, Hkv, D, _size(T), _whole(max_q), _dtype_code(q), _dtype_code(k_pages), _dtype_code(o),
-        _size(page_size), _size(pages), _size(cols), _whole(window), scale, q.data_ptr(), qs[0], qs[1],
+        _size(page_size), _size(pages), _size(cols), _whole(window), _scale(scale), q.data_ptr(), qs[0], qs[1],
         k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], page_table.data_ptr(), ts[0], q_start.data_ptr(),
         kv_len.data_ptr(), kn, vn, ns[0], ns[1], o.data_ptr(), os_[0], os_[1], None, 0)
 
@@ -285,9 +292,9 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     B = seq_start.shape[0] - 1
     _vector("seq_start", seq_start, B + 1, _i32)
     return SpecPrefillArgs(
-        _size(B), Hq, k.shape[1], D, _size(T), _whole(window), _dtype_code(q), _dtype_code(k), _dtype_code(o), scale,
-        q.data_ptr(), qs[0], qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(), o.data_ptr(),
-        os_[0], os_[1], None, 0)
+        _size(B), Hq, k.shape[1], D, _size(T), _whole(window), _dtype_code(q), _dtype_code(k), _dtype_code(o),
+        _scale(scale), q.data_ptr(), qs[0], qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(),
+        o.data_ptr(), os_[0], os_[1], None, 0)
 
 
 def spec_prefill_attn_workspace(q, k, seq_start, o) -> int:

@@ -1,11 +1,22 @@
 """What the serving binding makes of its tensors, on the host: the argument structs are filled without a GPU."""
 
+import ctypes
+
 import pytest
 import torch
 
+from speculative_decoding_verify_attn_gb300 import build
 from speculative_decoding_verify_attn_gb300 import serving as s
 
+from .test_serve_abi import paged as paged_struct
+from .test_serve_abi import prefill as prefill_struct
+
 I32 = torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
 
 
 def odd(*shape, dtype=torch.bfloat16):
@@ -102,3 +113,23 @@ def test_sizes_past_32_bits_stay_too_large():
         s.spec_paged_attn_workspace(q[:4], kp, table, q, max_q=4)
     with pytest.raises(s.SpecError):
         s.spec_prefill_attn_workspace(q, q[:, :2], torch.zeros(2, dtype=I32), q)
+
+
+def test_scales_that_32_bits_cannot_hold():
+    """0 stands for 1 / sqrt(D), so a scale that rounds to it is refused and not replaced."""
+    z = torch.zeros
+    for bad in (1e-50, -1e-50, 1e-46):
+        with pytest.raises(ValueError):
+            s.paged_attn_args(**paged(scale=bad))
+        with pytest.raises(ValueError):
+            s.prefill_attn_args(z(4, 2, 64), z(4, 2, 64), z(4, 2, 64), z(2, dtype=I32), z(4, 2, 64), scale=bad)
+    for good in (0, 0.0, 1e-40, 0.125, 2):
+        assert s.paged_attn_args(**paged(scale=good)).scale == pytest.approx(good, rel=1e-4)
+
+
+@pytest.mark.parametrize("scale", [3e38, 2.4e38])
+def test_scales_whose_binary_exponent_factor_is_infinite(scale):
+    """scale log2(e) multiplies every score in fp32.  (Refused before any launch.)"""
+    L = s._serve_lib()
+    assert L.spec_paged_attn(ctypes.byref(paged_struct(scale=scale)), None) == -1
+    assert L.spec_prefill_attn(ctypes.byref(prefill_struct(scale=scale)), None) == -1
