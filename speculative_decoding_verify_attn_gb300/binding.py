@@ -205,13 +205,19 @@ def _stream_handle(stream) -> Optional[int]:
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 
-def _workspace(nbytes: int, device, workspace):
+def _workspace(nbytes: int, device, workspace, stream):
     torch = _torch()
     if workspace is not None:
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"workspace too small: need {nbytes} bytes")
         return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    # from the launching stream's pool: a block of the current stream's may still be in use there, and would be
+    # handed out again before the other stream is done with it
+    own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream))
+    with torch.cuda.stream(own):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _host_i32(seq: Optional[Sequence[int]]):
@@ -274,7 +280,7 @@ def spec_verify_attn(q, k, v, kv_len, o, *, tree_parent=None, scale: float = 0.0
     need = spec_verify_attn_workspace(q, k, o)
     if need == 0:
         raise SpecError(SPEC_ERR_INVALID_ARG, "spec_verify_attn_workspace")
-    ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace, stream)
     a, keep = verify_attn_args(q, k, v, kv_len, o, tree_parent, scale, ws, k_new, v_new, debug_flags)
     st = lib().spec_verify_attn(byref(a), _stream_handle(stream))
     del keep
@@ -322,7 +328,7 @@ def spec_draft_window_attn(q, k_ring, v_ring, pos, o, *, k_new=None, v_new=None,
     need = spec_draft_window_attn_workspace(q, k_ring, o)
     if need == 0:
         raise SpecError(SPEC_ERR_INVALID_ARG, "spec_draft_window_attn_workspace")
-    ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace, stream)
     a = window_attn_args(q, k_ring, v_ring, pos, o, k_new, v_new, scale, ws, n_sinks)
     st = lib().spec_draft_window_attn(byref(a), _stream_handle(stream))
     if st != SPEC_OK:
@@ -372,7 +378,7 @@ def spec_sample(mode, target_logits, out_tokens, out_num_accepted, *, draft_logi
     need = spec_sample_workspace(mode, target_logits, tree_parent)
     if need == 0:
         raise SpecError(SPEC_ERR_INVALID_ARG, "spec_sample_workspace")
-    ws = _workspace(need, target_logits.device, workspace)
+    ws = _workspace(need, target_logits.device, workspace, stream)
     a, keep = sample_args(mode, target_logits, out_tokens, out_num_accepted, draft_logits=draft_logits,
                           draft_tokens=draft_tokens, uniforms=uniforms, tree_parent=tree_parent,
                           out_path_nodes=out_path_nodes, workspace=ws)
@@ -432,7 +438,7 @@ def spec_lmhead_sample(mode, hidden, weight, out_tokens, out_num_accepted, *, dr
     need = spec_lmhead_sample_workspace(mode, hidden, weight, out_logits)
     if need == 0:
         raise SpecError(SPEC_ERR_INVALID_ARG, "spec_lmhead_sample_workspace")
-    ws = _workspace(need, hidden.device, workspace)
+    ws = _workspace(need, hidden.device, workspace, stream)
     a, keep = lmhead_args(mode, hidden, weight, out_tokens, out_num_accepted, draft_tokens=draft_tokens,
                           tree_parent=tree_parent, out_path_nodes=out_path_nodes, workspace=ws,
                           draft_logits=draft_logits, uniforms=uniforms, out_logits=out_logits)
@@ -502,7 +508,7 @@ def spec_commit(mode, kv_len, num_accepted, nq, *, k=None, v=None, path_nodes=No
     path's K/V (k, v [B, Hkv, Lmax, D], path_nodes [B, path_cols] int32, e.g. spec_sample's
     out_path_nodes)."""
     _check_cuda(kv_len, num_accepted, k, v, path_nodes)
-    ws = _workspace(256, kv_len.device, workspace)
+    ws = _workspace(256, kv_len.device, workspace, stream)
     a = commit_args(mode, kv_len, num_accepted, nq, k=k, v=v, path_nodes=path_nodes, workspace=ws)
     st = lib().spec_commit(byref(a), _stream_handle(stream))
     if st != SPEC_OK:

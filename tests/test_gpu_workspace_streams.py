@@ -97,3 +97,48 @@ def test_a_dropped_tensor_still_being_read(sv, name, raw):
     call(out=o, stream=side.cuda_stream if raw else side)
     torch.cuda.synchronize()
     assert bool((seen == 3).all()) and torch.equal(o, want)
+
+
+def round_calls(sv):
+    """The calls of the speculative round: name -> (call(stream) -> outputs, bytes of workspace)."""
+    torch = torch_mod()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    norm = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    b16 = lambda *s: norm(*s).to(torch.bfloat16)  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, k, v, lens = b16(2, 5, 8, 128), b16(2, 2, 4096, 128), b16(2, 2, 4096, 128), i32([4000, 1500])
+    wq, wk, wv, pos = b16(2, 8, 128), b16(2, 2, 512, 128), b16(2, 2, 512, 128), i32([700, 300])
+    logits, hidden, weight = norm(2, 5, 32000), b16(2, 5, 256), b16(32000, 256)
+    drafts = torch.randint(0, 32000, (2, 4), generator=g, device="cuda", dtype=torch.int32)
+    o, wo = torch.empty((2, 5, 8, 128), device="cuda"), torch.empty((2, 8, 128), device="cuda")
+    tok, acc = torch.empty((2, 5), dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    none, mode = i32([0, 0]), sv.SPEC_SAMPLE_CHAIN_GREEDY
+    return {
+        "verify": (lambda s: [sv.spec_verify_attn(q, k, v, lens, o, stream=s)], sv.spec_verify_attn_workspace(q, k, o)),
+        "window": (lambda s: [sv.spec_draft_window_attn(wq, wk, wv, pos, wo, stream=s)],
+                   sv.spec_draft_window_attn_workspace(wq, wk, wo)),
+        "sample": (lambda s: sv.spec_sample(mode, logits, tok, acc, draft_tokens=drafts, stream=s),
+                   sv.spec_sample_workspace(mode, logits)),
+        "lmhead": (lambda s: sv.spec_lmhead_sample(mode, hidden, weight, tok, acc, draft_tokens=drafts, stream=s),
+                   sv.spec_lmhead_sample_workspace(mode, hidden, weight)),
+        "commit": (lambda s: [sv.spec_commit(sv.SPEC_COMMIT_CHAIN, lens, none, 1, stream=s)[:4]], 256),
+    }
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ["verify", "window", "sample", "lmhead", "commit"])
+def test_round_calls_and_a_dropped_tensor_still_being_read(sv, name, raw):
+    torch = torch_mod()
+    call, need = round_calls(sv)[name]
+    want = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    temp = torch.full((need,), 3, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    seen = temp.clone()
+    del temp
+    got = call(side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert bool((seen == 3).all()) and all(torch.equal(a, b) for a, b in zip(got, want))

@@ -6,8 +6,9 @@ torch and the library; the same on a GPU in test_gpu_workspace_streams.py."""
 import contextlib
 
 import pytest
+import torch as real
 
-from speculative_decoding_verify_attn_gb300 import serving
+from speculative_decoding_verify_attn_gb300 import binding, serving
 
 MAIN, SIDE = 0x1000, 0x2000
 
@@ -44,7 +45,7 @@ class FakeTensor:
 class FakeTorch:
     """The parts of torch that the bindings' calls use, with the current stream as plain state."""
 
-    uint8 = "uint8"
+    uint8, float32, bfloat16 = "uint8", real.float32, real.bfloat16
 
     def __init__(self):
         self.current, self.made = MAIN, []
@@ -116,3 +117,44 @@ def test_serving_callers_workspace_is_kept_for_the_launching_stream(fakes):
     mine = FakeTensor(torch, 8192)
     serving._call("spec_paged_attn", serving.SpecPagedArgs(), ("sizes",), 0, mine, FakeStream(SIDE))
     assert lib.handles == [SIDE] and torch.made == [mine] and mine.recorded == [SIDE]
+
+
+class FakeRoundLib:
+    """Every *_workspace function says 4096, every call notes its stream."""
+
+    def __init__(self):
+        self.handles = []
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace"):
+            return lambda ref: 4096
+        return lambda ref, handle: self.handles.append(handle) or 0
+
+
+def round_call(name, stream):
+    z, i32 = real.zeros, real.int32
+    ints = z(2, dtype=i32)
+    if name == "spec_verify_attn":
+        return binding.spec_verify_attn(z(2, 3, 4, 8), z(2, 2, 16, 8), z(2, 2, 16, 8), ints, z(2, 3, 4, 8), stream=stream)
+    if name == "spec_draft_window_attn":
+        return binding.spec_draft_window_attn(z(2, 4, 8), z(2, 2, 16, 8), z(2, 2, 16, 8), ints, z(2, 4, 8), stream=stream)
+    if name == "spec_sample":
+        return binding.spec_sample(binding.SPEC_SAMPLE_CHAIN_GREEDY, z(2, 3, 10), z((2, 3), dtype=i32), ints,
+                                   draft_tokens=z((2, 2), dtype=i32), stream=stream)
+    if name == "spec_lmhead_sample":
+        return binding.spec_lmhead_sample(binding.SPEC_SAMPLE_CHAIN_GREEDY, z(2, 3, 8), z(10, 8), z((2, 3), dtype=i32),
+                                          ints, draft_tokens=z((2, 2), dtype=i32), stream=stream)
+    return binding.spec_commit(binding.SPEC_COMMIT_CHAIN, ints, ints, 3, stream=stream)
+
+
+@pytest.mark.parametrize("stream,handle", [(FakeStream(SIDE), SIDE), (SIDE, SIDE), (FakeStream(MAIN), MAIN), (None, MAIN)])
+@pytest.mark.parametrize("name", ["spec_verify_attn", "spec_draft_window_attn", "spec_sample", "spec_lmhead_sample",
+                                  "spec_commit"])
+def test_round_workspace_comes_from_the_launching_stream(monkeypatch, name, stream, handle):
+    torch, lib = FakeTorch(), FakeRoundLib()
+    monkeypatch.setattr(binding, "_torch", lambda: torch)
+    monkeypatch.setattr(binding, "_check_cuda", lambda *ts: None)
+    monkeypatch.setattr(binding, "lib", lambda: lib)
+    round_call(name, stream)
+    assert lib.handles == [handle] and [x.pool for x in torch.made] == [handle]
+    assert torch.current == MAIN
