@@ -4,8 +4,8 @@
 // With m the running maximum, s = sum e^(x - m) and w = sum (x - m) e^(x - m), a row needs
 //     lse = m + log s,    log p(v) = x_v - m - log s,    H = log s - w / s,
 // and (m, s, w) of two parts of a row join as s' = s a + ..., w' = (w + (m - m') s) a + ..., a =
-// e^(m - m').  Every thread keeps its own (m, s, w) in fp32 over 16-byte vectors (a few hundred
-// elements each), joined by a fixed tree, so results do not depend on scheduling.
+// e^(m - m').  Every thread keeps its own (m, s, w) in fp32 over 16-byte vectors (V / 128 elements where a
+// row is one CTA, 1002 at 128256), joined by a fixed tree, so results do not depend on scheduling.
 //
 // Top alternatives: an id's key is (order of its logit, lower id first) as one 64-bit number; each
 // warp keeps its K best keys sorted over its lanes.  A batch of vectors is looked at one by one only
