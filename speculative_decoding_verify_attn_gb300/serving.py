@@ -113,14 +113,16 @@ def _check(tensors) -> int:
 
 
 def _rows(name, t):
-    """The strides of a tensor whose innermost dimension has to be contiguous.  A dimension of one element
-    is never stepped over, so its stride may be anything; a row's length stands in its place."""
-    st, shape = t.stride(), t.shape
-    if st[-1] != 1 and shape[-1] > 1:
+    """The strides of a tensor whose innermost dimension has to be contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: innermost dimension must be contiguous")
-    if 1 in shape:
-        return tuple(shape[-1] if n == 1 else x for n, x in zip(shape, st))
     return st
+
+
+def _equal(a, b) -> bool:
+    """Whether two tensors of one shape step alike: dimensions of one element are never stepped over."""
+    return all(x == y or n == 1 for n, x, y in zip(a.shape, a.stride(), b.stride()))
 
 
 _TOP = 2 ** 31 - 1
@@ -224,7 +226,7 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
     pages, Hkv, page_size, D2 = shape
     B, cols = page_table.shape
     qs, ks, os_, ts = _rows("q", q), _rows("k_pages", k_pages), _rows("o", o), _rows("page_table", page_table)
-    if D2 != D or v_pages.shape != shape or _rows("v_pages", v_pages) != ks:
+    if D2 != D or v_pages.shape != shape or not (v_pages.stride() == ks or _equal(v_pages, k_pages)):
         raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with q's D and equal strides")
     if v_pages.dtype is not k_pages.dtype:
         raise TypeError("k_pages and v_pages must share a dtype")
@@ -240,16 +242,25 @@ def paged_attn_args(q, k_pages, v_pages, page_table, q_start, kv_len, o, *, max_
         if k_new is None or v_new is None:
             raise ValueError("k_new and v_new go together")
         ns = _rows("k_new", k_new)
-        if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or _rows("v_new", v_new) != ns:
+        if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or not (
+                v_new.stride() == ns or _equal(v_new, k_new)):
             raise ValueError("k_new, v_new must be [T, Hkv, D] with equal strides")
         if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
             raise TypeError("k_new, v_new must have the cache's dtype")
         kn, vn = k_new.data_ptr(), v_new.data_ptr()
+    if max_q.__class__ is not int or not 0 <= max_q <= _TOP:
+        max_q = _whole(max_q)
+    if window.__class__ is not int or not 0 <= window <= _TOP:
+        window = _whole(window)
+    if B > _TOP or T > _TOP or page_size > _TOP or pages > _TOP or cols > _TOP:
+        raise ValueError("sizes past 32 bits")
+    # the stride of a dimension of one element may be anything: D stands in its place
     return SpecPagedArgs(
-        _size(B), Hq, Hkv, D, _size(T), _whole(max_q), _dtype_code(q), _dtype_code(k_pages), _dtype_code(o),
-        _size(page_size), _size(pages), _size(cols), _whole(window), _scale(scale), q.data_ptr(), qs[0], qs[1],
-        k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], page_table.data_ptr(), ts[0], q_start.data_ptr(),
-        kv_len.data_ptr(), kn, vn, ns[0], ns[1], o.data_ptr(), os_[0], os_[1], None, 0)
+        B, Hq, Hkv, D, T, max_q, _dtype_code(q), _dtype_code(k_pages), _dtype_code(o), page_size, pages, cols,
+        window, _scale(scale) if scale else 0.0, q.data_ptr(), qs[0] if T > 1 else D, qs[1] if Hq > 1 else D,
+        k_pages.data_ptr(), v_pages.data_ptr(), ks[0] if pages > 1 else D, ks[1] if Hkv > 1 else D,
+        ks[2] if page_size > 1 else D, page_table.data_ptr(), ts[0], q_start.data_ptr(), kv_len.data_ptr(), kn, vn,
+        ns[0] if T > 1 else D, ns[1] if Hkv > 1 else D, o.data_ptr(), os_[0], os_[1], None, 0)
 
 
 def spec_paged_attn_workspace(q, k_pages, page_table, o, *, max_q) -> int:
@@ -283,7 +294,8 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
     _torch or _t()
     T, Hq, D = q.shape
     qs, ks, os_ = _rows("q", q), _rows("k", k), _rows("o", o)
-    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or _rows("v", v) != ks:
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or not (
+            v.stride() == ks or _equal(v, k)):
         raise ValueError("k, v must be [T, Hkv, D] with equal strides")
     if v.dtype is not k.dtype:
         raise TypeError("k and v must share a dtype")
@@ -291,10 +303,15 @@ def prefill_attn_args(q, k, v, seq_start, o, *, window: int = 0, scale: float = 
         raise ValueError("o must have q's shape")
     B = seq_start.shape[0] - 1
     _vector("seq_start", seq_start, B + 1, _i32)
+    Hkv = k.shape[1]
+    if B > _TOP or T > _TOP:
+        raise ValueError("sizes past 32 bits")
+    # the stride of a dimension of one element may be anything: D stands in its place
     return SpecPrefillArgs(
-        _size(B), Hq, k.shape[1], D, _size(T), _whole(window), _dtype_code(q), _dtype_code(k), _dtype_code(o),
-        _scale(scale), q.data_ptr(), qs[0], qs[1], k.data_ptr(), v.data_ptr(), ks[0], ks[1], seq_start.data_ptr(),
-        o.data_ptr(), os_[0], os_[1], None, 0)
+        B, Hq, Hkv, D, T, _whole(window), _dtype_code(q), _dtype_code(k), _dtype_code(o),
+        _scale(scale) if scale else 0.0, q.data_ptr(), qs[0] if T > 1 else D, qs[1] if Hq > 1 else D, k.data_ptr(),
+        v.data_ptr(), ks[0] if T > 1 else D, ks[1] if Hkv > 1 else D, seq_start.data_ptr(), o.data_ptr(), os_[0],
+        os_[1], None, 0)
 
 
 def spec_prefill_attn_workspace(q, k, seq_start, o) -> int:
@@ -342,8 +359,11 @@ def token_logprobs_args(logits, tokens, logprobs, *, entropy=None, top_ids=None,
                 raise ValueError(f"{name} must be contiguous {dtype} of shape {(N, K)}")
         if K:
             ids, top = top_ids.data_ptr(), top_logprobs.data_ptr()
-    return SpecLogprobArgs(_size(N), _size(V), _size(K), _dtype_code(logits), logits.data_ptr(),
-                           _rows("logits", logits)[0], tok, lp, ent, ids, top, None, 0)
+    if N > _TOP or V > _TOP or K > _TOP:
+        raise ValueError("sizes past 32 bits")
+    # the stride of a single row may be anything
+    return SpecLogprobArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), _rows("logits", logits)[0] if N > 1 else V,
+                           tok, lp, ent, ids, top, None, 0)
 
 
 def spec_token_logprobs_workspace(logits, K: int = 0) -> int:
