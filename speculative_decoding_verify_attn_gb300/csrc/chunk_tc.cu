@@ -484,7 +484,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           if (exact || !__any_sync(0xffffffffu, !(sum <= kCtMaxSum) || m_run == neg_inf())) break;
           exact = true;
         }
-        if (!ok) break;
         l += sum;
         __syncwarp();
         tc::st32(sbuf, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
