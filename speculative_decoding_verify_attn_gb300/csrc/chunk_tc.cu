@@ -23,10 +23,11 @@
 // Why 128-key tiles: an operand in shared memory is read anew by every instruction; per pair of blocks
 // and 128 keys that is 192 KB of reads with 128-key scores and 256 KB with 64-key ones, against 2048
 // cycles of products at 128 B per cycle.
-// Measured (32/8 heads of 128): one 16K prompt 1.34 ms, 1.64 PFLOP/s, 84% of the measured matrix rate
-// (without any softmax arithmetic it takes 1.28); a 2048-token chunk at 32K 0.68 ms, 1.56 PFLOP/s; 16
-// packed prompts of 60-2000 tokens 0.20 ms, 0.90 PFLOP/s (a piece costs 7000 cycles beside its 128-key
-// steps of 2600); 16 sequences of 64K-128K with 56 rows 0.975 ms, 6.7 TB/s.
+// Measured (32/8 heads of 128), from a cool GPU to one at its power cap: one 16K prompt 1.34-1.46 ms,
+// 1.64-1.51 PFLOP/s, 84-78% of the measured matrix rate (without any softmax arithmetic 1.28 ms on the cool
+// one); a 2048-token chunk at 32K 0.67-0.74 ms, 1.6-1.45 PFLOP/s; 16 packed prompts of 60-2000 tokens 0.20 ms,
+// 0.90 PFLOP/s (a piece costs 7000 cycles beside its 128-key steps of 2600); 16 sequences of 64K-128K with 56
+// rows 0.96-0.975 ms, 6.75-6.65 TB/s.
 // TMEM columns (512): block w at 256 w: S [0, 128), P over [0, 64), O [128, 128 + D).
 #include <cuda.h>
 #include <cuda_bf16.h>

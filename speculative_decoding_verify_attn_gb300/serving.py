@@ -3,7 +3,8 @@ paged KV cache, attention over packed prompts, and token log probabilities.
 
 Same names as the C ABI and the same manner as ``binding``: every function checks its tensors,
 marshals them into the argument struct and calls the library on the current stream of the tensors'
-device (or on ``stream``).  There is no fallback.
+device (or on ``stream``, which the caller orders behind whatever wrote the tensors).  There is no
+fallback.
 """
 
 from __future__ import annotations
