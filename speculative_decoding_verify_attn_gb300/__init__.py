@@ -19,3 +19,10 @@ from .serving import (  # noqa: F401,E402
     spec_paged_attn_workspace, spec_prefill_attn, spec_prefill_attn_workspace, spec_token_logprobs,
     spec_token_logprobs_workspace,
 )
+from .cache import (  # noqa: F401,E402
+    SPEC_ROTARY_BANDS, SPEC_ROTARY_HALF, SPEC_ROTARY_LINEAR, SPEC_ROTARY_NTK, SPEC_ROTARY_PAIRS, SPEC_ROTARY_PLAIN,
+    SPEC_ROTARY_YARN, SPEC_STATUS_NO_PAGE, SpecKv8AppendArgs, SpecPageArray, SpecPageCompactArgs, SpecPageForkArgs,
+    SpecPaged8Args, SpecRotaryArgs, spec_kv8_append, spec_kv8_append_workspace, spec_page_compact,
+    spec_page_compact_workspace, spec_page_fork, spec_page_fork_workspace, spec_paged_attn8, spec_paged_attn8_workspace,
+    spec_rotary, spec_rotary_steps, spec_rotary_workspace,
+)

@@ -23,10 +23,11 @@ LIBPATH = os.path.join(LIBDIR, LIBNAME)
 
 SOURCES = ["attn.cu", "attn_tc.cu", "attn_tc_pair.cu", "sample.cu", "sample_tree.cu", "lmhead.cu", "commit.cu",
            "api.cpp", "noalloc.cu", "launch_cache.cpp", "serve_api.cpp", "paged_mma.cu", "chunk_plan.cu", "chunk_f32.cu",
-           "chunk_tc.cu", "logprobs.cu"]
+           "chunk_tc.cu", "logprobs.cu", "cache_api.cpp", "rotary.cu", "kv8_append.cu", "paged8_mma.cu", "chunk8_tc.cu",
+           "pages.cu"]
 HEADERS = ["common.cuh", "attn_common.cuh", "tcgen05.cuh", "ff.cuh", "attn_internal.h", "sample_internal.h",
            "commit_internal.h", "lmhead_internal.h", "launch_cache.h", "serve_internal.h", "serve_common.cuh",
-           "tensor_map.h"]
+           "tensor_map.h", "mma_walk.cuh", "cache_internal.h", "kv8_common.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -39,7 +40,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_serve.h")]
+    files += [os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_serve.h", "spec_cache.h")]
     files.append(os.path.abspath(__file__))
     return files
 

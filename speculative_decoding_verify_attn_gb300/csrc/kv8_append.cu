@@ -1,0 +1,189 @@
+// New K/V rows into the pages of an 8-bit cache.
+//
+// A warp takes one block of tokens of one head, of K or of V: the largest magnitude of the block's new rows
+// gives the exponent the block needs; if the block holds earlier tokens of the sequence it keeps at least
+// its own, and where that grows the earlier rows are brought to it; then the new rows are scaled
+// (exactly: a power of two), rounded and stored.  A block's rows are therefore in one warp's hands, and
+// nothing has to be ordered between warps.
+// A lane holds 16 values of a row, so that a store is 16 bytes; the second pass over the rows reads L1.
+// Bound: HBM for prompts (2 or 4 bytes read and 1 written per value), latency for a round's few rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "cache_internal.h"
+#include "common.cuh"
+#include "kv8_common.cuh"
+
+namespace specv {
+
+constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = kAppendThreads / 32;
+
+template <bool F32>
+__device__ __forceinline__ void load16(const void* src, int64_t at, float (&v)[16]) {
+  if constexpr (F32) {
+    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(src) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = __ldg(s + i);
+      v[4 * i] = __uint_as_float(w.x);
+      v[4 * i + 1] = __uint_as_float(w.y);
+      v[4 * i + 2] = __uint_as_float(w.z);
+      v[4 * i + 3] = __uint_as_float(w.w);
+    }
+  } else {
+    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 w = __ldg(s + i);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
+        v[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+// Blocks that get new tokens.
+__device__ __forceinline__ int touched_blocks(const Kv8Params& p, const SeqInfo& s) {
+  return s.len > 0 ? (s.len - 1) / p.block - (s.len - s.n) / p.block + 1 : 0;
+}
+
+template <bool F32, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_constant__ Kv8Params p, int first) {
+  pdl_launch_dependents();
+  constexpr int LANES = D / 16, ROWS = 32 / LANES;  // lanes of a row, rows of an instruction
+  extern __shared__ int s_pre[];  // [B + 1] blocks before each sequence
+  __shared__ int s_sum[kAppendWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!first) pdl_wait();
+  if (first && blockIdx.x == 0 && tid == 0) status_clear_for_launch(p.status);
+  auto report = [&](uint32_t bits) {
+    if (first) status_report(p.status, bits);
+    else atomicOr(p.status, bits);
+  };
+  // prefix sums over the sequences: T rows make at most T blocks, but sequences that overlap can claim more
+  int run = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kAppendThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.B) {
+      const SeqInfo s = seq_info(p, b);
+      n = touched_blocks(p, s);
+      if (s.bad && blockIdx.x == 0) report(s.bad);
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int pre = run;
+#pragma unroll
+    for (int w = 0; w < kAppendWarps; ++w) {
+      if (w < warp) pre += s_sum[w];
+      run += s_sum[w];
+    }
+    if (b < p.B) s_pre[b] = pre + x - n;
+    run = min(run, 1 << 26);  // at most 2^22 per sequence: no overflow; nothing valid comes near
+  }
+  if (tid == 0) s_pre[p.B] = run;
+  __syncthreads();
+
+  const int64_t units = (int64_t)run * p.Hkv * 2;
+  const int c = lane % LANES, rl = lane / LANES;
+  for (int64_t unit = (int64_t)blockIdx.x * kAppendWarps + warp; unit < units; unit += (int64_t)gridDim.x * kAppendWarps) {
+    const bool is_v = unit & 1;
+    const int g = (int)(unit / 2 % p.Hkv), blk = (int)(unit / 2 / p.Hkv);
+    int lo = 0, hi = p.B;  // the last sequence that begins at blk or before
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid] <= blk) lo = mid;
+      else hi = mid;
+    }
+    const SeqInfo s = seq_info(p, lo);
+    const int fresh = s.len - s.n;  // the first new token
+    const int t0 = (fresh / p.block + blk - s_pre[lo]) * p.block;
+    const int begin = max(t0, fresh), end = min(t0 + p.block, s.len);
+    if (blk < s_pre[lo] || begin >= end) continue;  // sequences that overlap by more rows than there can be
+    int page, slot;
+    page_slot(p, lo, t0, page, slot);
+    if (page < 0) {
+      if (lane == 0) report((uint32_t)SPEC_STATUS_BAD_PAGE);
+      continue;
+    }
+    const void* src = is_v ? p.v_new : p.k_new;
+    const int64_t from = (int64_t)(s.q0 + begin - fresh) * p.new_st + (int64_t)g * p.new_sh + c * 16;
+    uint8_t* exp = (is_v ? p.v_exp : p.k_exp) + (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
+    uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? p.v : p.k) + (int64_t)page * p.kv_sp + (int64_t)g * p.kv_sh + c * 16;
+    const int old = begin > t0 ? clamp_exp(*exp) : 0;
+    float amax = 0.f;
+    for (int r = rl; r < end - begin; r += ROWS) {
+      float v[16];
+      load16<F32>(src, from + (int64_t)r * p.new_st, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float a = fabsf(v[i]);
+        amax = fmaxf(amax, a <= 3.402823466e38f ? a : 0.f);
+      }
+    }
+    amax = warp_max(amax);
+    const int e = max(old, needed_exp(amax));
+    if (begin > t0 && e > old) {
+      const float down = exp2_whole(old - e >= -126 ? old - e : -126);
+      for (int r = rl; r < begin - t0; r += ROWS) {
+        uint4* at = reinterpret_cast<uint4*>(dst + (int64_t)(slot + r) * p.kv_st);
+        uint4 w = *at;
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a, b;
+          e4m3x4_to_f16x4(u[i], a, b);
+          const float2 x = f16x2_to_f32x2(a), y = f16x2_to_f32x2(b);
+          u[i] = f32x4_to_e4m3x4(x.x * down, x.y * down, y.x * down, y.y * down);
+        }
+        *at = w;
+      }
+    }
+    const float scale = exp2_whole(127 - e);
+    for (int r = rl; r < end - begin; r += ROWS) {
+      float v[16];
+      load16<F32>(src, from + (int64_t)r * p.new_st, v);
+      uint4 w;
+      uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        u[i] = f32x4_to_e4m3x4(v[4 * i] * scale, v[4 * i + 1] * scale, v[4 * i + 2] * scale, v[4 * i + 3] * scale);
+      *reinterpret_cast<uint4*>(dst + (int64_t)(slot + begin - t0 + r) * p.kv_st) = w;
+    }
+    __syncwarp();
+    if (lane == 0) *exp = (uint8_t)e;
+  }
+  // see pdl_wait above: a grid that is not the call's first has waited in every CTA
+}
+
+template <bool F32, int D>
+static cudaError_t launch_append(const Kv8Params& p, bool first, cudaStream_t stream) {
+  const int smem = (p.B + 1) * (int)sizeof(int);
+  // at most T / block + 2 per sequence with tokens
+  const int64_t blocks = p.T / p.block + 2 * (int64_t)(p.B < p.T ? p.B : p.T);
+  const int64_t want = (blocks * p.Hkv * 2 + kAppendWarps - 1) / kAppendWarps;
+  const unsigned grid = (unsigned)(want < 8 * p.grid ? want : 8 * p.grid);
+  if (first) {
+    kv8_append<F32, D><<<grid, kAppendThreads, smem, stream>>>(p, 1);
+    return cudaGetLastError();
+  }
+  return launch_dependent(kv8_append<F32, D>, dim3(grid), dim3(kAppendThreads), smem, stream, 0u, p, 0);
+}
+
+cudaError_t launch_kv8_append(const Kv8Params& p, bool first, cudaStream_t stream) {
+  if (p.src_f32) return p.D == 128 ? launch_append<true, 128>(p, first, stream) : launch_append<true, 64>(p, first, stream);
+  return p.D == 128 ? launch_append<false, 128>(p, first, stream) : launch_append<false, 64>(p, first, stream);
+}
+
+}  // namespace specv

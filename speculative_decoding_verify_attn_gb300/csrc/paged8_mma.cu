@@ -1,0 +1,420 @@
+// Attention of small chunks (up to kMmaMaxRows query rows per sequence and kv head) over a paged cache in
+// 8 bits: the work of paged_mma.cu, with keys of half the bytes.
+//
+// Bound: HBM, one read of every visible key's bytes; the units, the warps' private rings, the records and the
+// kernel that joins them are paged_mma.cu's.  What differs is how a tile of 16 keys gets to mma.sync:
+//   e4m3 is brought to fp16 (exactly) in registers, with one conversion per pair of values, and the products
+//   are fp16 x fp16 into fp32.  bf16 would take three instructions a pair and round probabilities to 8 bits
+//   instead of 11.
+//   K: ldmatrix sees pairs of bytes as 16-bit elements, so a lane gets four neighbouring values of a key's row;
+//   the dot product does not mind the order of its terms, so they serve as the columns 2 t, 2 t + 1, 2 t + 8,
+//   2 t + 9 of a step of 16, and the query is laid out alike.
+//   V: a transposed ldmatrix brings two neighbouring columns of two keys; one byte permutation pairs the keys,
+//   and columns 2 r, 2 r + 1 take the places r and r + 8 of the 16 rows of the product.
+//   A block's K scale multiplies the tile's scores.  Its V scale 2^ev goes into the exponent of the
+//   probabilities, p' = 2^(s + ev - R), with R kept near the largest s + ev: p' then fits fp16 for whatever
+//   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev.
+//   fp16 holds p' <= 2^15 and rounds to steps of 2^-24, so R is set 2^7 below the maximum: what a
+//   probability of the largest key's size loses is then below 2^-32 of it.
+//   Query rows are scaled to fp16 row by row by a power of two, undone on the scores.
+#include <cuda_runtime.h>
+
+#include "cache_internal.h"
+#include "common.cuh"
+#include "kv8_common.cuh"
+#include "launch_cache.h"
+#include "mma_walk.cuh"
+
+namespace specv {
+
+// How far a score may lie above the reference, and where the reference is set below the maximum.
+constexpr float kRescaleLog2 = 15.0f;
+constexpr float kHeadroomLog2 = 7.0f;
+
+template <int D>
+struct Mma8 {
+  static constexpr int kStage = 16 * D * 2;             // a warp's K and V
+  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr size_t kSmem = (size_t)kMmaWarps * kStages * kStage + kMmaCmbBytes;
+  // Place of chunk c (16 bytes) of row r: eight rows' chunks c lie in eight different groups of banks.
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return r * D + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4);
+  }
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    paged8_mma(const __grid_constant__ Kv8Params p) {
+  pdl_launch_dependents();
+  if (!p.first) pdl_wait();  // the append
+  constexpr int KS = D / 16;        // k steps of K Q^T, m tiles of V^T P^T, 16-byte chunks of a row
+  constexpr int RPI = 32 / KS;      // rows one cp.async instruction of the warp covers
+  constexpr int NS = Mma8<D>::kStages;
+  constexpr int STAGE = Mma8<D>::kStage;
+  extern __shared__ __align__(256) uint8_t smem[];
+  __shared__ int64_t s_scan[kMmaWarps];
+  __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
+  __shared__ uint16_t s_exp[kMmaWarps][NS][16];  // K and V exponent bytes of a stage's keys
+  __shared__ int s_b;
+  __shared__ int64_t s_cum;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  float* cmb = reinterpret_cast<float*>(smem + (size_t)kMmaWarps * NS * STAGE);
+  if (p.first && cta == 0 && tid == 0) status_clear_for_launch(p.status);
+  auto report = [&](uint32_t bits) {
+    if (p.first) status_report(p.status, bits);
+    else atomicOr(p.status, bits);
+  };
+
+  MmaWalk ld;
+  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) return;
+
+  // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
+  const uint32_t ring_u32 = smem_u32(smem + (size_t)warp * NS * STAGE);
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k);
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v);
+  MmaWalk cw = ld;  // the unit in compute
+  int page = -1;
+  auto look_up = [&]() {  // page id of this lane's key (lanes 16-31 repeat lanes 0-15)
+    const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
+    page = -1;
+    if (ld.left > 0 && t >= ld.s.lo && t < ld.s.len)
+      page = __ldg(p.table + (int64_t)ld.b * p.table_stride + page_of(p, t));
+  };
+  // for rows i * RPI + lane / KS the lane's part of the place is constant and i changes it by XOR and offset
+  const int c = lane % KS, rl = lane / KS;
+  uint8_t k_byte = 127, v_byte = 127;  // of this lane's key of the unit issued last; they reach s_exp one unit later
+  int exps_stage = -1;
+  auto issue = [&](int stage) {
+    if (exps_stage >= 0 && lane < 16) s_exp[warp][exps_stage][lane] = (uint16_t)(k_byte | v_byte << 8);
+    exps_stage = -1;
+    if (ld.left > 0) {
+      const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
+      const uint32_t dst = ring_u32 + stage * STAGE;
+      const bool in = t >= ld.s.lo && t < ld.s.len;
+      const bool good = in && page >= 0 && page < p.num_pages;
+      const int slot = t - page_of(p, t) * p.page_size;
+      const int64_t row = good ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)ld.g * p.kv_sh : -1;
+      k_byte = v_byte = 127;
+      exps_stage = stage;
+      if (good) {
+        const int64_t at = (int64_t)page * p.exp_sp + (int64_t)ld.g * p.exp_sh + block_of(p, slot);
+        k_byte = p.k_exp[at];
+        v_byte = p.v_exp[at];
+      } else if (in) {
+        report((uint32_t)SPEC_STATUS_BAD_PAGE);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + rl;
+        const int64_t so = __shfl_sync(0xffffffffu, row, r);
+        const uint32_t at = dst + Mma8<D>::at(r, c);
+        cp_async16(at, kb + (so < 0 ? 0 : so) + c * 16, so >= 0);
+        cp_async16(at + 16 * D, vb + (so < 0 ? 0 : so) + c * 16, so >= 0);
+      }
+      ld.step(p);
+      look_up();
+    }
+    cp_async_commit();
+  };
+  look_up();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) issue(i);
+
+  // ---- compute
+  const int gid = lane >> 2, tq = lane & 3;
+  // places of the fragments' rows: K: matrices (keys 0-7, 8-15) x (chunk, chunk + 1); V alike
+  const int frag_row = lane & 15, frag_chunk = lane >> 4;
+  uint32_t qf[NR][KS][2];
+  float o[NR][KS][4];  // columns d = ks * 16 + 2 gid (e < 2), + 1 (e >= 2) of rows nr * 8 + 2 tq + (e & 1)
+  float qs[NR][2];     // what the scores of those rows are multiplied by
+  float m_run[NR][2], l_run[NR][2];  // the reference R, and the sum of 2^(s - R)
+  int stage = 0;
+  bool fresh_part = true;
+  bool starts_at_begin = true;  // the current part starts where the CTA's range starts
+  int part_u0 = cw.u;
+  while (true) {
+    const int rows = cw.s.n * p.G;
+    if (fresh_part) {
+      fresh_part = false;
+      part_u0 = cw.u;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = nr * 8 + gid;
+        const bool real = r < rows;
+        // four neighbouring values of each step of 16, as K's rows come
+        const uint2* src = reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                          (real ? q_offset(p, cw.s, cw.g, r) : 0));
+        uint2 raw[KS];
+        float amax = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          raw[ks] = real ? __ldg(src + ks * 4 + tq) : make_uint2(0u, 0u);
+          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float undo;
+        const float up = f16_row_scale(amax, undo);
+        qs[nr][0] = q_factor(__shfl_sync(0xffffffffu, undo, tq * 8), p.scale_log2);
+        qs[nr][1] = q_factor(__shfl_sync(0xffffffffu, undo, tq * 8 + 4), p.scale_log2);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[nr][ks][i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nr][ks][e] = 0.f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          m_run[nr][h] = neg_inf();
+          l_run[nr][h] = 0.f;
+        }
+      }
+    }
+    issue(stage == 0 ? NS - 1 : stage - 1);  // NS - 1 units ahead
+    cp_async_wait<NS - 1>();
+    __syncwarp();
+    const uint32_t ks_u32 = ring_u32 + stage * STAGE;
+    const int key0 = (cw.s.lo & ~15) + cw.u * kMmaUnit + warp * 16;
+
+    // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
+    // few query rows are padded to 8 instead of 16
+    float s[NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nr][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      uint32_t w[4];
+      ldmatrix_x4(ks_u32 + Mma8<D>::at(frag_row, ks + frag_chunk), w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t a[4];
+        e4m3x4_to_f16x4(w[2 * i], a[0], a[2]);
+        e4m3x4_to_f16x4(w[2 * i + 1], a[1], a[3]);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) mma_f16_16816(s[nr], a, qf[nr][ks + i][0], qf[nr][ks + i][1]);
+      }
+    }
+    // the scales of keys gid and gid + 8: the scores become s + ev, to the base of 2
+    float kscale[2], ev[2], vinv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = s_exp[warp][stage][gid + 8 * i];
+      const int ke = clamp_exp(e & 255), ve = clamp_exp(e >> 8);
+      kscale[i] = exp2_whole(ke - 127);
+      ev[i] = (float)(ve - 127);
+      vinv[i] = exp2_whole(127 - ve);
+    }
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nr][e] = fmaf(s[nr][e], qs[nr][e & 1] * kscale[e >> 1], ev[e >> 1]);
+    // keys some row must not see: past the first new token, below the last row's window, or slots
+    // outside [lo, len)
+    const int first_new = cw.s.len - cw.s.n;
+    if (key0 + 16 > first_new || key0 < cw.s.lo || (p.window > 0 && key0 < cw.s.len - p.window)) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int pos = first_new + (nr * 8 + tq * 2 + (e & 1)) / p.G;
+          const int t = key0 + gid + (e & 2) * 4;
+          const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
+          if (!vis) s[nr][e] = neg_inf();
+        }
+    }
+    // the reference moves only when a score lies 2^15 above it, so most units need no exchange between
+    // lanes; it is then set 2^7 below the new maximum
+    bool over = false;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = fmaxf(s[nr][h], s[nr][2 + h]);
+        over |= x != neg_inf() && x > m_run[nr][h] + kRescaleLog2;
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = fmaxf(s[nr][h], s[nr][2 + h]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = x == neg_inf() ? m_run[nr][h] : fmaxf(m_run[nr][h], x - kHeadroomLog2);
+          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - mn);
+          m_run[nr][h] = mn;
+          l_run[nr][h] *= f[h];
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          o[nr][ks][0] *= f[0];
+          o[nr][ks][1] *= f[1];
+          o[nr][ks][2] *= f[0];
+          o[nr][ks][3] *= f[1];
+        }
+      }
+    }
+    uint32_t pf[NR][2];  // P^T as the B operand: 16 keys x 8 rows
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      float e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float m = m_run[nr][i & 1];
+        e[i] = ex2_approx(s[nr][i] - (m == neg_inf() ? 0.f : m));
+      }
+      l_run[nr][0] = fmaf(e[0], vinv[0], fmaf(e[2], vinv[1], l_run[nr][0]));
+      l_run[nr][1] = fmaf(e[1], vinv[0], fmaf(e[3], vinv[1], l_run[nr][1]));
+      pf[nr][0] = movmatrix_trans(pack_f16(e[0], e[1]));
+      pf[nr][1] = movmatrix_trans(pack_f16(e[2], e[3]));
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      uint32_t w[4];
+      ldmatrix_x4_trans(ks_u32 + 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t a[4];
+        e4m3x4_to_f16x4(__byte_perm(w[2 * i], 0, 0x3120), a[0], a[1]);
+        e4m3x4_to_f16x4(__byte_perm(w[2 * i + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][ks + i], a, pf[nr][0], pf[nr][1]);
+      }
+    }
+    __syncwarp();  // every lane has read the stage before it is refilled
+    stage = stage == NS - 1 ? 0 : stage + 1;
+
+    // ---- end of the part: join the warps' states
+    const bool last = cw.left == 1;
+    if (cw.u + 1 == cw.nu || last) {
+      const bool whole = part_u0 == 0 && cw.u + 1 == cw.nu;
+      const int64_t rec = 2 * (int64_t)cta + (starts_at_begin ? 0 : 1);
+      starts_at_begin = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float l = l_run[nr][h];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (gid == 0) s_ml[warp][nr * 8 + tq * 2 + h] = make_float2(m_run[nr][h], l);
+        }
+      __syncthreads();
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        if (nr * 8 >= rows) break;
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = nr * 8 + tq * 2 + h;
+          float M = neg_inf();
+#pragma unroll
+          for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - M);
+        }
+        // the warps' columns of 8 rows x 64 columns through shared memory; then a warp per row adds
+        // them up, two columns per lane
+        const int r = nr * 8 + warp, col = lane * 2;
+        float M = neg_inf(), L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) {
+          const float2 v = s_ml[w][r];
+          L += v.x == neg_inf() ? 0.f : ex2_approx(v.x - M) * v.y;
+        }
+        const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+        if (!whole && r < rows && lane == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M, L);
+#pragma unroll
+        for (int c4 = 0; c4 < D / 64; ++c4) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float* dst = cmb + (warp * 8 + tq * 2) * kMmaCmbStride + x * 16 + gid * 2;
+            const float* v = o[nr][c4 * 4 + x];
+            *reinterpret_cast<float2*>(dst) = make_float2(v[0] * f[0], v[2] * f[0]);
+            *reinterpret_cast<float2*>(dst + kMmaCmbStride) = make_float2(v[1] * f[1], v[3] * f[1]);
+          }
+          __syncthreads();
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kMmaWarps; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(cmb + (w * 8 + warp) * kMmaCmbStride + col);
+            sum.x += v.x;
+            sum.y += v.y;
+          }
+          if (r < rows) {
+            if (whole) {
+              const int64_t off = o_offset(p, cw.s, cw.g, r) + c4 * 64 + col;
+              if (p.o_bf16) {
+                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off;
+                const uint32_t v = pack_bf16(sum.x * inv, sum.y * inv);
+                if ((reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+                  *reinterpret_cast<uint32_t*>(dst) = v;
+                } else {
+                  reinterpret_cast<uint16_t*>(dst)[0] = (uint16_t)v;
+                  reinterpret_cast<uint16_t*>(dst)[1] = (uint16_t)(v >> 16);
+                }
+              } else {
+                float* dst = reinterpret_cast<float*>(p.o) + off;
+                dst[0] = sum.x * inv;
+                dst[1] = sum.y * inv;
+              }
+            } else {
+              *reinterpret_cast<float2*>(p.part_o + (rec * kMmaMaxRows + r) * D + c4 * 64 + col) = sum;
+            }
+          }
+          __syncthreads();
+        }
+      }
+      fresh_part = true;
+    }
+    if (last) break;
+    cw.step(p);
+  }
+  cp_async_wait<0>();
+}
+
+template <int D, int NR>
+static cudaError_t launch_mma8(const Kv8Params& p, cudaStream_t stream) {
+  const size_t smem = Mma8<D>::kSmem;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(paged8_mma<D, NR>), (int)smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.direct ? p.B * p.Hkv : p.grid);
+  if (p.first) {
+    paged8_mma<D, NR><<<grid, kMmaThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
+  } else {
+    e = launch_dependent(paged8_mma<D, NR>, grid, dim3(kMmaThreads), smem, stream, 0u, p);
+  }
+  return e != cudaSuccess || p.direct ? e : launch_paged_mma_merge(p, stream);
+}
+
+template <int D>
+static cudaError_t launch_mma8_d(const Kv8Params& p, cudaStream_t stream) {
+  switch ((p.max_q * p.G + 7) / 8) {  // tiles of 8 query rows
+    case 1: return launch_mma8<D, 1>(p, stream);
+    case 2: return launch_mma8<D, 2>(p, stream);
+    case 3: return launch_mma8<D, 3>(p, stream);
+    default: return launch_mma8<D, 4>(p, stream);
+  }
+}
+
+cudaError_t launch_paged8_mma(const Kv8Params& p, cudaStream_t stream) {
+  return p.D == 128 ? launch_mma8_d<128>(p, stream) : launch_mma8_d<64>(p, stream);
+}
+
+}  // namespace specv

@@ -25,63 +25,19 @@
 
 #include "common.cuh"
 #include "launch_cache.h"
+#include "mma_walk.cuh"
 #include "serve_common.cuh"
 #include "serve_internal.h"
 
 namespace specv {
 
-constexpr int kMmaWarps = 8;
-constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaStages = 3;
-constexpr int kMmaCmbStride = 68;  // floats per row of the 64-column join buffer (conflict-free)
 constexpr float kMmaRescaleLog2 = 8.0f;
 
 __host__ __device__ constexpr int mma_stage_bytes(int D) { return 16 * D * 2 * 2; }  // a warp's K and V
-constexpr int kMmaCmbBytes = kMmaWarps * 8 * kMmaCmbStride * 4;
 __host__ __device__ constexpr size_t mma_smem_bytes(int D) {
   return (size_t)kMmaWarps * kMmaStages * mma_stage_bytes(D) + kMmaCmbBytes;
 }
-
-// Units of a segment of sequence s; its first unit starts at key lo rounded down to 16.
-__device__ __forceinline__ int mma_units(const SeqInfo& s) {
-  return s.len > 0 ? (s.len - (s.lo & ~15) + kMmaUnit - 1) / kMmaUnit : 0;
-}
-
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sm) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane == 0) sm[warp] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < kMmaWarps; ++w) t += sm[w];
-  return t;
-}
-
-__device__ __forceinline__ int64_t mma_per_cta(int64_t total, int grid) {
-  const int64_t per = (total + grid - 1) / grid;
-  return per < 1 ? 1 : per;
-}
-
-// Position in the walk over a CTA's units: unit u of nu of segment (b, g), `left` units to go.
-struct MmaWalk {
-  int b, g, u, nu;
-  int64_t left;
-  SeqInfo s;
-  __device__ __forceinline__ void step(const ServeAttnParams& p) {
-    if (--left <= 0) return;
-    if (++u < nu) return;
-    u = 0;
-    if (++g < p.Hkv) return;
-    g = 0;
-    do {
-      s = seq_info(p, ++b);
-      nu = mma_units(s);
-    } while (nu == 0);
-  }
-};
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constant__ ServeAttnParams p) {
@@ -102,71 +58,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
 
   // ---- this CTA's units
   MmaWalk ld;
-  int64_t begin = 0;
-  if (p.direct) {
-    ld.b = cta / p.Hkv;
-    ld.g = cta % p.Hkv;
-    ld.u = 0;
-    ld.s = seq_info(p, ld.b);
-    ld.nu = mma_units(ld.s);
-    ld.left = ld.nu;
-    if (ld.s.bad && ld.g == 0 && tid == 0) status_report(p.status, ld.s.bad);
-    if (ld.nu == 0) {  // no keys: zeros for the rows of a bad length
-      for (int i = tid; i < ld.s.n * p.G * D; i += kMmaThreads) {
-        const int64_t off = o_offset(p, ld.s, ld.g, i / D) + i % D;
-        if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(0.f);
-        else reinterpret_cast<float*>(p.o)[off] = 0.f;
-      }
-      return;
-    }
-  } else {
-    int64_t mine = 0;
-    for (int b = tid; b < p.B; b += kMmaThreads) {
-      const SeqInfo s = seq_info(p, b);
-      mine += mma_units(s);
-      if (s.bad && cta == 0) status_report(p.status, s.bad);
-    }
-    const int64_t total = block_sum(mine, s_scan) * p.Hkv;
-    const int64_t per = mma_per_cta(total, p.grid);
-    begin = (int64_t)cta * per;
-    if (begin >= total) return;
-    ld.left = min(per, total - begin);
-    // the sequence whose units hold `begin`
-    int64_t run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kMmaThreads) {
-      const int b = b0 + tid;
-      const int64_t n = b < p.B ? (int64_t)mma_units(seq_info(p, b)) * p.Hkv : 0;
-      int64_t x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = x;
-      __syncthreads();
-      int64_t pre = run, all = 0;
-#pragma unroll
-      for (int w = 0; w < kMmaWarps; ++w) {
-        if (w < warp) pre += s_scan[w];
-        all += s_scan[w];
-      }
-      const int64_t excl = pre + x - n;
-      if (n > 0 && begin >= excl && begin < excl + n) {
-        s_b = b;
-        s_cum = excl;
-      }
-      run += all;
-      if (begin < run) break;  // the same for all threads
-    }
-    __syncthreads();
-    ld.b = s_b;
-    ld.s = seq_info(p, ld.b);
-    ld.nu = mma_units(ld.s);
-    const int64_t rel = begin - s_cum;
-    ld.g = (int)(rel / ld.nu);
-    ld.u = (int)(rel % ld.nu);
-  }
+  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, [&](uint32_t bits) { status_report(p.status, bits); })) return;
 
   // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
   uint8_t* ring = smem + (size_t)warp * kMmaStages * STAGE;
@@ -553,6 +445,12 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p) {
   p->part_o = reinterpret_cast<float*>(b + 256 + 2 * (size_t)kServeMaxGrid * kMmaMaxRows * sizeof(float2));
 }
 
+cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, cudaStream_t stream) {
+  const dim3 grid(p.B * p.Hkv, (unsigned)(p.max_q * p.G + kMmaWarps - 1) / kMmaWarps);
+  if (p.D == 128) return launch_dependent(paged_mma_merge<128>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+  return launch_dependent(paged_mma_merge<64>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+}
+
 template <int D, int NR>
 static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   const size_t smem = mma_smem_bytes(D);
@@ -562,8 +460,7 @@ static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.direct) return e;
-  const unsigned rows = (unsigned)(p.max_q * p.G + kMmaWarps - 1) / kMmaWarps;
-  return launch_dependent(paged_mma_merge<D>, dim3(p.B * p.Hkv, rows), dim3(kMmaThreads), 0, stream, 0u, p);
+  return launch_paged_mma_merge(p, stream);
 }
 
 template <int D>

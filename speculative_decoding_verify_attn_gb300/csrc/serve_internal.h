@@ -105,6 +105,8 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p);
 void chunk_workspace_carve(void* ws, ServeAttnParams* p);
 
 cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream);
+// joins the records of segments that several CTAs share
+cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, cudaStream_t stream);
 // plan and append, attention, merge
 cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,

@@ -36,6 +36,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn_major, 
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The same with A and B in fp16 (bits 7 and 10 clear).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {
+  return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
 // Whole warp: allocate `ncols` TMEM columns (power of two >= 32); the base address is written to
 // shared memory at `dst`.
 __device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {
