@@ -34,7 +34,8 @@ namespace specv {
 constexpr int kC8Threads = 256 + 2 * 128;
 constexpr uint32_t kC8TmemCols = 512;
 constexpr int kC8Half = 128 * 128;  // 128 rows of one 64-column half: 16 KB
-constexpr int kC8Loaders = 4;       // warps, 32 keys each
+constexpr int kC8Issuer = 4;        // the warp among the first eight that issues the products
+constexpr int kC8Loaders = 7;       // the others
 // A row's sum over one tile up to which its reference stays, and where the reference is set below a maximum.
 constexpr float kC8MaxSum = 65504.f;
 constexpr float kC8HeadroomLog2 = 8.f;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], kC8Loaders);
+      mbar_init(&full[i], 4);  // the groups of a tile
       mbar_init(&empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 4) tc::alloc(&tmem_base, kC8TmemCols);
+  if (warp == kC8Issuer) tc::alloc(&tmem_base, kC8TmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -118,82 +119,91 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_TIMEOUT);
   };
 
-  // registers: 256 x 56 + 256 x 200 = 512 x 128, what the block was launched with
-  if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-
-  if (warp < kC8Loaders) {
+  // registers: 256 x 72 + 256 x 184 = 512 x 128, what the block was launched with
+  if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp != kC8Issuer) {
     // ------------------------------------------------------------------ loaders
-    // lane: chunk lane & 3 (16 values) of a half of row i * 8 + lane / 4 of the warp's 32.  Eight lanes then store
+    // A group is 32 rows of a tile: 0-3 of a unit are K's, 4-7 V's, dealt to the warps in turn, so that a warp
+    // has the time of seven groups for one group's loads.
+    // lane: chunk lane & 3 (16 values) of a half of row i * 8 + lane / 4 of the group's 32.  Eight lanes then store
     // to eight different groups of banks: even chunks of an even row, odd ones of an odd row.
     constexpr int NH = C::kHalves;
     const int rl = lane >> 2, cl = lane & 3;
-    int step = 0, unit = 0;
-    bool ok = true;
-    // the unit that is looked up: a piece of the list and a unit in it
-    int round = 0, u = 0;
-    PieceRaw raw_piece = list.fetch(p, 0);
-    auto settle = [&]() {  // on to the next piece that has units; false at the end
-      while (round < rounds) {
-        if (u < raw_piece.a.w) return true;
-        raw_piece = list.fetch(p, ++round);
-        u = raw_piece.a.z;
+    // the group that is looked up
+    int grp = warp < kC8Issuer ? warp : warp - 1, unit = 0, round = 0;
+    int u = 0, u1 = 0, b = 0, g = 0, lo = 0, len = 0;
+    auto open = [&]() {  // the next piece that has units; false at the end
+      for (; round < rounds; ++round) {
+        const PieceItem it = piece_item(list.fetch(p, round));
+        if (it.u0 >= it.u1) continue;
+        u = it.u0; u1 = it.u1; b = it.b; g = it.g; lo = it.s.lo; len = it.s.len;
+        return true;
       }
       return false;
     };
-    u = raw_piece.a.z;
-    bool have = settle();
-    int page = -1, slot = 0;
-    auto look_up = [&]() {  // of this lane's key
-      const PieceItem it = piece_item(raw_piece);
-      const int t = u * kTcKeys + warp * 32 + lane;
-      page = -2;
-      if (t >= it.s.lo && t < it.s.len) page_slot(p, it.b, t, page, slot);
+    auto advance = [&]() {
+      grp += kC8Loaders;
+      if (grp < 8) return true;
+      grp -= 8;
+      ++unit;
+      if (++u < u1) return true;
+      ++round;
+      return open();
     };
-    int64_t off[4];       // of this lane's four rows; -1 where zeros go
-    uint32_t k_byte = 0, v_byte = 0;  // of this lane's key
-    bool live = false;                // its page is good
+    int page = -2, slot = 0;
+    auto look_up = [&]() {  // of this lane's key
+      const int t = u * kTcKeys + (grp & 3) * 32 + lane;
+      page = -2;
+      if (t >= lo && t < len) page_slot(p, b, t, page, slot);
+    };
+    // the group whose values are on their way
     uint4 raw[4 * NH];
-    auto resolve = [&]() {
-      const int g = raw_piece.c.y;
+    int now = 0;                      // unit * 8 + group
+    bool live = false;                // this lane's key has a page
+    uint32_t byte = 0, v_byte = 0;    // its exponent; a K group also looks after V's
+    auto load = [&]() {
       if (page == -1) chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_BAD_PAGE);
       __syncwarp();
-      const int64_t mine = page >= 0 ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)g * p.kv_sh : -1;
+      now = unit * 8 + grp;
       live = page >= 0;
-      if (live) {
-        const int64_t at = (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
-        k_byte = p.k_exp[at];
-        v_byte = p.v_exp[at];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
-    };
-    auto load = [&](const void* base) {
-      const uint8_t* b = reinterpret_cast<const uint8_t*>(base);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-          raw[i * NH + h] = off[i] >= 0 ? __ldcg(reinterpret_cast<const uint4*>(b + off[i] + h * 64 + cl * 16))
-                                        : make_uint4(0u, 0u, 0u, 0u);
-    };
-    // the tile in `raw` to its stage; returns the warp's exponent byte, false in `ok` after a wait that ran out
-    auto store = [&](int mine) -> int {  // the lane's clamped byte, 0 where zeros went
-      const int top = __reduce_max_sync(0xffffffffu, mine);
-      const bool uneven = __any_sync(0xffffffffu, mine != 0 && mine != top);
-      const int s = step % NS;
-      const bool got = mbar_wait_spin(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
-      if (!__all_sync(0xffffffffu, got)) {
-        fail();
-        ok = false;
-        return 0;
-      }
-      const uint32_t dst = stages_u32 + s * C::kTile + warp * 32 * 128;
+      const int64_t mine = live ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)g * p.kv_sh : -1;
+      const uint8_t* base = reinterpret_cast<const uint8_t*>(grp < 4 ? p.k : p.v) + cl * 16;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + rl;
-        const int down = uneven ? max(__shfl_sync(0xffffffffu, mine, r) - top, -24) : 0;
-        const __half2 f = __float2half2_rn(exp2_whole(down));
+        const int64_t off = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          raw[i * NH + h] = off >= 0 ? __ldcg(reinterpret_cast<const uint4*>(base + off + h * 64)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (live) {
+        const int64_t at = (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
+        v_byte = p.v_exp[at];
+        byte = grp < 4 ? p.k_exp[at] : v_byte;
+      }
+    };
+    // the values in `raw` to their stage, at the group's largest exponent; false after a wait that ran out
+    auto store = [&]() -> bool {
+      const int mine = live ? clamp_exp((int)byte) : 0;
+      const int top = __reduce_max_sync(0xffffffffu, mine);
+      const bool uneven = __any_sync(0xffffffffu, live && mine != top);
+      const int step = now >> 2, s = step % NS;
+      if ((now & 7) < 4) {
+        // both exponents go out with K, before the scores that need them exist
+        const int vtop = __reduce_max_sync(0xffffffffu, live ? clamp_exp((int)v_byte) : 0);
+        if (lane == 0) {
+          const int at = (now >> 3) % kC8Units;
+          reinterpret_cast<uint8_t*>(&s_kexp[at])[now & 3] = (uint8_t)(top ? top : 127);
+          reinterpret_cast<uint8_t*>(&s_vexp[at])[now & 3] = (uint8_t)(vtop ? vtop : 127);
+        }
+      }
+      const bool got = mbar_wait_spin(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      const uint32_t dst = stages_u32 + s * C::kTile + ((now & 3) * 32 + rl) * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __half2 f = __float2half2_rn(1.f);
+        if (uneven) f = __float2half2_rn(exp2_whole(max(__shfl_sync(0xffffffffu, mine, i * 8 + rl) - top, -24)));
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const uint32_t w[4] = {raw[i * NH + h].x, raw[i * NH + h].y, raw[i * NH + h].z, raw[i * NH + h].w};
@@ -207,52 +217,30 @@ __global__ void __launch_bounds__(kC8Threads, 1)
               v[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
-          const uint32_t row = dst + h * kC8Half + r * 128;
-          sts128(row + (((2 * cl) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
-          sts128(row + (((2 * cl + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
+          const uint32_t row = dst + h * kC8Half + i * 1024;  // (row & 7) == rl
+          sts128(row + (((2 * cl) ^ rl) << 4), v[0], v[1], v[2], v[3]);
+          sts128(row + (((2 * cl + 1) ^ rl) << 4), v[4], v[5], v[6], v[7]);
         }
       }
-      return top;
-    };
-    auto arrive = [&]() {
       tc::fence_proxy_async_smem();  // every lane's stores, for the tensor core
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[step % NS]);
-      ++step;
+      if (lane == 0) mbar_arrive(&full[s]);
+      return true;
     };
-    if (have) {
-      look_up();
-      resolve();
-      load(p.k);
-    }
-    while (have && ok) {
-      const int kb = live ? clamp_exp((int)k_byte) : 0, vb = live ? clamp_exp((int)v_byte) : 0;
-      ++u;
-      const bool more = settle();
-      if (more) look_up();
-      // both exponents go out with K, before the scores that need them exist
-      const int vtop = __reduce_max_sync(0xffffffffu, vb);
-      const int ktop = store(kb);
-      if (!ok) break;
-      if (lane == 0) {
-        reinterpret_cast<uint8_t*>(&s_kexp[unit % kC8Units])[warp] = (uint8_t)(ktop ? ktop : 127);
-        reinterpret_cast<uint8_t*>(&s_vexp[unit % kC8Units])[warp] = (uint8_t)(vtop ? vtop : 127);
+    bool have = open();  // a group is looked up
+    if (have) look_up();
+    while (have) {
+      load();
+      have = advance();
+      if (have) look_up();
+      if (!store()) {
+        fail();
+        break;
       }
-      load(p.v);
-      arrive();
-      store(vb);
-      if (!ok) break;
-      if (more) {
-        resolve();
-        load(p.k);
-      }
-      arrive();
-      ++unit;
-      have = more;
     }
-  } else if (warp < 8) {
+    } else {
     // ------------------------------------------------------------------ MMA issuer (one lane)
-    if (warp == kC8Loaders && elect_one()) {
+    if (elect_one()) {
       int step = 0, part[2] = {0, 0}, t[2] = {0, 0};  // pieces and tiles so far, by block
       bool ok = true;
       // S_w = Q_w K^T (behind P_w V of the tile before, whose P it overwrites)
@@ -322,7 +310,9 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         mbar_wait_spin(&drain, 0, nullptr);
       }
     }
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------------ softmax warpgroups
     const int w = (warp - 8) >> 2;
     const int sub = warp & 3;        // TMEM sub-partition of this warp
@@ -635,7 +625,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 
   tc::fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kC8Issuer) {
     __syncwarp();
     tc::fence_after();
     tc::dealloc(tmem, kC8TmemCols);
