@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
   __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ uchar4 s_kexp[kC8Units], s_vexp[kC8Units];  // of a unit's four groups of 32 keys
+  __shared__ uint32_t s_kexp[kC8Units], s_vexp[kC8Units];  // a byte for each of a unit's four groups of 32 keys
   __shared__ LightSeqs s_light;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* qs = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // [block][half][128 rows][128 B]
@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_TIMEOUT);
   };
 
-  // registers: 256 x 72 + 256 x 184 = 512 x 128, what the block was launched with
+  // registers: 256 x 96 + 256 x 160 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp != kC8Issuer) {
     // ------------------------------------------------------------------ loaders
     // A group is 32 rows of a tile: 0-3 of a unit are K's, 4-7 V's, dealt to the warps in turn, so that a warp
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ------------------------------------------------------------------ softmax warpgroups
     const int w = (warp - 8) >> 2;
     const int sub = warp & 3;        // TMEM sub-partition of this warp
@@ -420,55 +420,50 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         if (u == b1 - 1 && have_next) start_q(nx, ntok, nhead);  // the piece's last Q K^T has read its rows
         const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
-        // P = 2^(s * scale - mu) against the present reference, as bf16 pairs; only where a row's sum
-        // says that a score lies far above it (or nothing has been seen yet) is the tile's maximum
-        // taken, O rescaled and the tile done again
+        // what the scores of 32 columns are multiplied by, and the exponent of V's values there
+        const uint32_t kx = s_kexp[(base + u) % kC8Units], vx = s_vexp[(base + u) % kC8Units];
+        auto k_scale = [&](int c) {
+          return fmaxf(qscale * exp2_whole((int)(kx >> (8 * c) & 255u) - 127), 1.17549435e-38f);  // hidden scores stay -inf
+        };
+        auto v_exponent = [&](int c) { return (int)(vx >> (8 * c) & 255u) - 127; };
+        // The usual tile is straight code of a few hundred instructions, 32 columns at a time with the next ones on
+        // their way (with all 128 in registers beside P the kernel spills, and what spills goes to L2, because
+        // shared memory leaves L1 nothing).  What is rare goes over S in TMEM before it, in loops: hidden
+        // scores become -inf there, and the maximum is taken there.
+        if (edge) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int h = hi - c * 32, l = lo - c * 32;  // visible [l, h]
+            const uint32_t vis = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) & (l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l);
+            if (__all_sync(0xffffffffu, vis == ~0u)) continue;
+            uint32_t v[32];
+            tc::ld32(sbuf + c * 32, v);
+            tc::ld_wait(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xff800000u;
+            tc::st32(sbuf + c * 32, v);
+          }
+          tc::st_wait();
+        }
+        // P = 2^(s + ev - mu) against the present reference, as fp16 pairs; only where a row's sum says that a
+        // score lies far above it (or nothing has been seen yet) is the tile's maximum taken, O rescaled and
+        // the tile done again
         uint32_t pk[64];
         float sum, lsum;
         bool exact = u == b0;
         for (;;) {
-          uint32_t s0[32], s1[32], s2[32], s3[32];
-          tc::ld32(sbuf, s0);
-          tc::ld32(sbuf + 32, s1);
-          tc::ld32(sbuf + 64, s2);
-          tc::ld32(sbuf + 96, s3);
-          tc::ld_wait(s0);
-          tc::ld_wait(s1);
-          tc::ld_wait(s2);
-          tc::ld_wait(s3);
-          if (edge) {
-            auto hide = [&](uint32_t(&v)[32], int c0) {
-              const int h = hi - c0, l = lo - c0;  // visible [l, h]
-              const uint32_t vis = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) & (l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xff800000u;
-            };
-            hide(s0, 0);
-            hide(s1, 32);
-            hide(s2, 64);
-            hide(s3, 96);
-          }
-          const uchar4 kx = s_kexp[(base + u) % kC8Units], vx = s_vexp[(base + u) % kC8Units];
-          const uint8_t ke[4] = {kx.x, kx.y, kx.z, kx.w}, ve[4] = {vx.x, vx.y, vx.z, vx.w};
-          float scq[4], evq[4];  // of 32 columns each
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            scq[c] = fmaxf(qscale * exp2_whole((int)ke[c] - 127), 1.17549435e-38f);  // hidden scores stay -inf
-            evq[c] = (float)((int)ve[c] - 127);
-          }
           if (exact) {
-            float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              mx[0] = fmax3(mx[0], __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
-              mx[1] = fmax3(mx[1], __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
-              mx[2] = fmax3(mx[2], __uint_as_float(s2[e]), __uint_as_float(s2[e + 1]));
-              mx[3] = fmax3(mx[3], __uint_as_float(s3[e]), __uint_as_float(s3[e + 1]));
-            }
             float top = neg_inf();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tc::ld32(sbuf + c * 32, v);
+              tc::ld_wait(v);
+              float mx = neg_inf();
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (mx[c] != neg_inf()) top = fmaxf(top, fmaf(mx[c], scq[c], evq[c]));
+              for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              if (mx != neg_inf()) top = fmaxf(top, fmaf(mx, k_scale(c), (float)v_exponent(c)));
+            }
             const float m_new = top == neg_inf() ? m_run : fmaxf(m_run, top - kC8HeadroomLog2);
             const float alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - m_new);
             l *= alpha;
@@ -490,24 +485,33 @@ __global__ void __launch_bounds__(kC8Threads, 1)
           const float mu = m_run == neg_inf() ? 0.f : m_run;
           sum = lsum = 0.f;
           auto chunk = [&](const uint32_t(&v)[32], int c) {
-            const float nmu = evq[c] - mu;
+            const float scale = k_scale(c), nmu = (float)v_exponent(c) - mu;
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float x0, x1;
-              fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), scq[c], nmu, x0, x1);
+              fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), scale, nmu, x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               add2(sums[e & 2], sums[(e & 2) + 1], p0, p1);
               pk[c * 16 + e / 2] = pack_f16(p0, p1);
             }
             const float part = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             sum += part;
-            lsum = fmaf(part, exp2_whole(127 - (int)ve[c]), lsum);
+            lsum = fmaf(part, exp2_whole(-v_exponent(c)), lsum);
           };
-          chunk(s0, 0);
-          chunk(s1, 1);
-          chunk(s2, 2);
-          chunk(s3, 3);
+          uint32_t sa[32], sb[32];
+          tc::ld32(sbuf, sa);
+          tc::ld_wait(sa);
+          tc::ld32(sbuf + 32, sb);
+          chunk(sa, 0);
+          tc::ld_wait(sb);
+          tc::ld32(sbuf + 64, sa);
+          chunk(sb, 1);
+          tc::ld_wait(sa);
+          tc::ld32(sbuf + 96, sb);
+          chunk(sa, 2);
+          tc::ld_wait(sb);
+          chunk(sb, 3);
           if (exact || !__any_sync(0xffffffffu, !(sum <= kC8MaxSum) || m_run == neg_inf())) break;
           exact = true;
         }
