@@ -21,6 +21,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "cache_internal.h"
 #include "common.cuh"
 #include "kv8_common.cuh"
@@ -47,7 +49,7 @@ template <int D>
 struct C8 {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kC8Half;       // a K or V tile, or a Q block
-  static constexpr int kStages = D == 128 ? 5 : 10;     // 160 KB
+  static constexpr int kStages = D == 128 ? 4 : 8;      // 128 KB; what is left is L1's (5 stages: 881 us instead of 855)
   static constexpr size_t kSmem = 1024 + 2 * (size_t)kTile + (size_t)kStages * kTile;
   static_assert(kSmem + 2048 <= 227 * 1024, "with the statically allocated part");
   static constexpr uint32_t kIdescQK = tc::idesc_f16(128, 128, 0, 0);
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
   __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ uint32_t s_kexp[kC8Units], s_vexp[kC8Units];  // a byte for each of a unit's four groups of 32 keys
+  __shared__ float4 s_scale[kC8Units][4];  // of a unit's four groups of 32 keys: K's scale, V's exponent, 1 / V's scale
   __shared__ LightSeqs s_light;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* qs = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // [block][half][128 rows][128 B]
@@ -192,36 +194,40 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         // both exponents go out with K, before the scores that need them exist
         const int vtop = __reduce_max_sync(0xffffffffu, live ? clamp_exp((int)v_byte) : 0);
         if (lane == 0) {
-          const int at = (now >> 3) % kC8Units;
-          reinterpret_cast<uint8_t*>(&s_kexp[at])[now & 3] = (uint8_t)(top ? top : 127);
-          reinterpret_cast<uint8_t*>(&s_vexp[at])[now & 3] = (uint8_t)(vtop ? vtop : 127);
+          const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0;
+          s_scale[(now >> 3) % kC8Units][now & 3] = make_float4(exp2_whole(ke), (float)ve, exp2_whole(-ve), 0.f);
         }
       }
       const bool got = mbar_wait_spin(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
       if (!__all_sync(0xffffffffu, got)) return false;
       const uint32_t dst = stages_u32 + s * C::kTile + ((now & 3) * 32 + rl) * 128;
+      // two straight pieces of code: with the choice inside, each chunk's stores wait for its conversions
+      auto rows = [&](auto scaled) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __half2 f = __float2half2_rn(1.f);
-        if (uneven) f = __float2half2_rn(exp2_whole(max(__shfl_sync(0xffffffffu, mine, i * 8 + rl) - top, -24)));
+        for (int i = 0; i < 4; ++i) {
+          __half2 f;
+          if constexpr (scaled.value) f = __float2half2_rn(exp2_whole(max(__shfl_sync(0xffffffffu, mine, i * 8 + rl) - top, -24)));
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const uint32_t w[4] = {raw[i * NH + h].x, raw[i * NH + h].y, raw[i * NH + h].z, raw[i * NH + h].w};
-          uint32_t v[8];
+          for (int h = 0; h < NH; ++h) {
+            const uint32_t w[4] = {raw[i * NH + h].x, raw[i * NH + h].y, raw[i * NH + h].z, raw[i * NH + h].w};
+            uint32_t v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(w[e], v[2 * e], v[2 * e + 1]);
-          if (uneven) {
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(w[e], v[2 * e], v[2 * e + 1]);
+            if constexpr (scaled.value) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&v[e]), f);
-              v[e] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int e = 0; e < 8; ++e) {
+                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&v[e]), f);
+                v[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
             }
+            const uint32_t row = dst + h * kC8Half + i * 1024;  // (row & 7) == rl
+            sts128(row + (((2 * cl) ^ rl) << 4), v[0], v[1], v[2], v[3]);
+            sts128(row + (((2 * cl + 1) ^ rl) << 4), v[4], v[5], v[6], v[7]);
           }
-          const uint32_t row = dst + h * kC8Half + i * 1024;  // (row & 7) == rl
-          sts128(row + (((2 * cl) ^ rl) << 4), v[0], v[1], v[2], v[3]);
-          sts128(row + (((2 * cl + 1) ^ rl) << 4), v[4], v[5], v[6], v[7]);
         }
-      }
+      };
+      if (uneven) rows(std::true_type{});
+      else rows(std::false_type{});
       tc::fence_proxy_async_smem();  // every lane's stores, for the tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
@@ -420,12 +426,9 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         if (u == b1 - 1 && have_next) start_q(nx, ntok, nhead);  // the piece's last Q K^T has read its rows
         const int hi = pos - u * kTcKeys, lo = wlo - u * kTcKeys;  // visible columns [lo, hi]
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
-        // what the scores of 32 columns are multiplied by, and the exponent of V's values there
-        const uint32_t kx = s_kexp[(base + u) % kC8Units], vx = s_vexp[(base + u) % kC8Units];
-        auto k_scale = [&](int c) {
-          return fmaxf(qscale * exp2_whole((int)(kx >> (8 * c) & 255u) - 127), 1.17549435e-38f);  // hidden scores stay -inf
-        };
-        auto v_exponent = [&](int c) { return (int)(vx >> (8 * c) & 255u) - 127; };
+        // what the scores of 32 columns are multiplied by; hidden scores stay -inf
+        const float4* scales = s_scale[(base + u) % kC8Units];
+        auto k_scale = [&](const float4& x) { return fmaxf(qscale * x.x, 1.17549435e-38f); };
         // The usual tile is straight code of a few hundred instructions, 32 columns at a time with the next ones on
         // their way (with all 128 in registers beside P the kernel spills, and what spills goes to L2, because
         // shared memory leaves L1 nothing).  What is rare goes over S in TMEM before it, in loops: hidden
@@ -462,7 +465,8 @@ __global__ void __launch_bounds__(kC8Threads, 1)
               float mx = neg_inf();
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-              if (mx != neg_inf()) top = fmaxf(top, fmaf(mx, k_scale(c), (float)v_exponent(c)));
+              const float4 x = scales[c];
+              if (mx != neg_inf()) top = fmaxf(top, fmaf(mx, k_scale(x), x.y));
             }
             const float m_new = top == neg_inf() ? m_run : fmaxf(m_run, top - kC8HeadroomLog2);
             const float alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - m_new);
@@ -485,7 +489,8 @@ __global__ void __launch_bounds__(kC8Threads, 1)
           const float mu = m_run == neg_inf() ? 0.f : m_run;
           sum = lsum = 0.f;
           auto chunk = [&](const uint32_t(&v)[32], int c) {
-            const float scale = k_scale(c), nmu = (float)v_exponent(c) - mu;
+            const float4 x = scales[c];
+            const float scale = k_scale(x), nmu = x.y - mu;
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
             }
             const float part = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             sum += part;
-            lsum = fmaf(part, exp2_whole(-v_exponent(c)), lsum);
+            lsum = fmaf(part, x.z, lsum);
           };
           uint32_t sa[32], sb[32];
           tc::ld32(sbuf, sa);
