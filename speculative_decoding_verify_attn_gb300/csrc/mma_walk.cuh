@@ -1,5 +1,5 @@
-// Shared by the kernels of small chunks over paged caches (paged_mma.cu, paged8_mma.cu): the walk over units of
-// 128 keys, laid end to end over all (sequence, kv head) segments and dealt to the CTAs in equal ranges.
+// Shared by the kernels of small chunks over paged caches (paged_mma.cu, paged8_mma.cu): the walk over units
+// of keys, laid end to end over all (sequence, kv head) segments and dealt to the CTAs in equal ranges.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -16,9 +16,15 @@ constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaCmbStride = 68;  // floats per row of the 64-column join buffer (conflict-free)
 constexpr int kMmaCmbBytes = kMmaWarps * 8 * kMmaCmbStride * 4;
 
-// Units of a segment of sequence s; its first unit starts at key lo rounded down to 16.
+// Units (of UNIT keys, an eighth of them per warp) of a segment of sequence s; its first unit starts at key lo
+// rounded down to a warp's keys.
+template <int UNIT>
+__device__ __forceinline__ int mma_first(const SeqInfo& s) {
+  return s.lo & ~(UNIT / kMmaWarps - 1);
+}
+template <int UNIT>
 __device__ __forceinline__ int mma_units(const SeqInfo& s) {
-  return s.len > 0 ? (s.len - (s.lo & ~15) + kMmaUnit - 1) / kMmaUnit : 0;
+  return s.len > 0 ? (s.len - mma_first<UNIT>(s) + UNIT - 1) / UNIT : 0;
 }
 
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sm) {
@@ -40,6 +46,7 @@ __device__ __forceinline__ int64_t mma_per_cta(int64_t total, int grid) {
 }
 
 // Position in the walk over a CTA's units: unit u of nu of segment (b, g), `left` units to go.
+template <int UNIT>
 struct MmaWalk {
   int b, g, u, nu;
   int64_t left;
@@ -52,15 +59,15 @@ struct MmaWalk {
     g = 0;
     do {
       s = seq_info(p, ++b);
-      nu = mma_units(s);
+      nu = mma_units<UNIT>(s);
     } while (nu == 0);
   }
 };
 
 // This CTA's units: the walk's start in `ld`, false if there are none.  Whole CTA; the s_ arguments are shared
 // memory, `report` takes the flags of bad sequences.  Direct mode: the rows of a bad length become zero.
-template <int D, typename Report>
-__device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk& ld, int64_t* s_scan, int& s_b, int64_t& s_cum,
+template <int D, int UNIT, typename Report>
+__device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk<UNIT>& ld, int64_t* s_scan, int& s_b, int64_t& s_cum,
                                           Report report) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -69,7 +76,7 @@ __device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk& ld,
     ld.g = cta % p.Hkv;
     ld.u = 0;
     ld.s = seq_info(p, ld.b);
-    ld.nu = mma_units(ld.s);
+    ld.nu = mma_units<UNIT>(ld.s);
     ld.left = ld.nu;
     if (ld.s.bad && ld.g == 0 && tid == 0) report(ld.s.bad);
     if (ld.nu == 0) {  // no keys: zeros for the rows of a bad length
@@ -84,7 +91,7 @@ __device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk& ld,
     int64_t mine = 0;
     for (int b = tid; b < p.B; b += kMmaThreads) {
       const SeqInfo s = seq_info(p, b);
-      mine += mma_units(s);
+      mine += mma_units<UNIT>(s);
       if (s.bad && cta == 0) report(s.bad);
     }
     const int64_t total = block_sum(mine, s_scan) * p.Hkv;
@@ -96,7 +103,7 @@ __device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk& ld,
     int64_t run = 0;
     for (int b0 = 0; b0 < p.B; b0 += kMmaThreads) {
       const int b = b0 + tid;
-      const int64_t n = b < p.B ? (int64_t)mma_units(seq_info(p, b)) * p.Hkv : 0;
+      const int64_t n = b < p.B ? (int64_t)mma_units<UNIT>(seq_info(p, b)) * p.Hkv : 0;
       int64_t x = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -123,7 +130,7 @@ __device__ __forceinline__ bool mma_start(const ServeAttnParams& p, MmaWalk& ld,
     __syncthreads();
     ld.b = s_b;
     ld.s = seq_info(p, ld.b);
-    ld.nu = mma_units(ld.s);
+    ld.nu = mma_units<UNIT>(ld.s);
     const int64_t rel = begin - s_cum;
     ld.g = (int)(rel / ld.nu);
     ld.u = (int)(rel % ld.nu);

@@ -11,6 +11,8 @@
 //   2 t + 9 of a step of 16, and the query is laid out alike.
 //   V: a transposed ldmatrix brings two neighbouring columns of two keys; one byte permutation pairs the keys,
 //   and columns 2 r, 2 r + 1 take the places r and r + 8 of the 16 rows of the product.
+//   A warp takes 32 keys of a unit at a time, two tiles side by side: twice the independent work per warp, and half
+//   the bookkeeping per key.
 //   A block's K scale multiplies the tile's scores.  Its V scale 2^ev goes into the exponent of the
 //   probabilities, p' = 2^(s + ev - R), with R kept near the largest s + ev: p' then fits fp16 for whatever
 //   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev.
@@ -30,11 +32,15 @@ namespace specv {
 // How far a score may lie above the reference, and where the reference is set below the maximum.
 constexpr float kRescaleLog2 = 15.0f;
 constexpr float kHeadroomLog2 = 7.0f;
+// The reference of a row that has seen no key: every score lies above it, and 2^(-inf - it) is 0.
+constexpr float kNoReference = -3.402823466e38f;
+
+constexpr int kMma8Keys = kMma8Unit / kMmaWarps;  // a warp's keys of a unit
 
 template <int D>
 struct Mma8 {
-  static constexpr int kStage = 16 * D * 2;             // a warp's K and V
-  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr int kStage = kMma8Keys * D * 2;      // a warp's K and V
+  static constexpr int kStages = D == 128 ? 3 : 5;
   static constexpr size_t kSmem = (size_t)kMmaWarps * kStages * kStage + kMmaCmbBytes;
   // Place of chunk c (16 bytes) of row r: eight rows' chunks c lie in eight different groups of banks.
   static __device__ __forceinline__ uint32_t at(int r, int c) {
@@ -47,14 +53,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     paged8_mma(const __grid_constant__ Kv8Params p) {
   pdl_launch_dependents();
   if (!p.first) pdl_wait();  // the append
-  constexpr int KS = D / 16;        // k steps of K Q^T, m tiles of V^T P^T, 16-byte chunks of a row
-  constexpr int RPI = 32 / KS;      // rows one cp.async instruction of the warp covers
+  constexpr int KS = D / 16;          // k steps of K Q^T, m tiles of V^T P^T, 16-byte chunks of a row
+  constexpr int RPI = 32 / KS;        // rows one cp.async instruction of the warp covers
   constexpr int NS = Mma8<D>::kStages;
   constexpr int STAGE = Mma8<D>::kStage;
+  constexpr int KT = NR <= 3 ? 2 : 1; // tiles of 16 keys at a time: two, as far as the registers go
   extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int64_t s_scan[kMmaWarps];
   __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
-  __shared__ uint16_t s_exp[kMmaWarps][NS][16];  // K and V exponent bytes of a stage's keys
+  __shared__ float4 s_scale[kMmaWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent, 1 / V's scale
   __shared__ int s_b;
   __shared__ int64_t s_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -66,37 +73,46 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     else atomicOr(p.status, bits);
   };
 
-  MmaWalk ld;
+  MmaWalk<kMma8Unit> ld;
   if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) return;
 
-  // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
+  // ---- loads: the warp's 32 keys of the unit at `ld`, a lane each for page ids (fetched one unit ahead) and scales
   const uint32_t ring_u32 = smem_u32(smem + (size_t)warp * NS * STAGE);
   const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k);
   const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v);
-  MmaWalk cw = ld;  // the unit in compute
+  MmaWalk<kMma8Unit> cw = ld;  // the unit in compute
+  auto first_key = [&](const MmaWalk<kMma8Unit>& w) {
+    return mma_first<kMma8Unit>(w.s) + w.u * kMma8Unit + warp * kMma8Keys;
+  };
   int page = -1;
-  auto look_up = [&]() {  // page id of this lane's key (lanes 16-31 repeat lanes 0-15)
-    const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
+  auto look_up = [&]() {
+    const int t = first_key(ld) + lane;
     page = -1;
     if (ld.left > 0 && t >= ld.s.lo && t < ld.s.len)
       page = __ldg(p.table + (int64_t)ld.b * p.table_stride + page_of(p, t));
   };
-  // for rows i * RPI + lane / KS the lane's part of the place is constant and i changes it by XOR and offset
   const int c = lane % KS, rl = lane / KS;
-  uint8_t k_byte = 127, v_byte = 127;  // of this lane's key of the unit issued last; they reach s_exp one unit later
-  int exps_stage = -1;
+  const uint32_t lane_at = Mma8<D>::at(rl, c);
+  const bool whole_pages = (p.page_size & (kMma8Keys - 1)) == 0;
+  uint8_t k_byte = 127, v_byte = 127;  // of this lane's key of the unit issued last; they reach s_scale one unit later
+  bool seen = false;                   // whether that key lies in [lo, len)
+  int scale_stage = -1;
   auto issue = [&](int stage) {
-    if (exps_stage >= 0 && lane < 16) s_exp[warp][exps_stage][lane] = (uint16_t)(k_byte | v_byte << 8);
-    exps_stage = -1;
+    if (scale_stage >= 0) {
+      const int ve = clamp_exp(v_byte) - 127;
+      s_scale[warp][scale_stage][lane] = make_float4(exp2_whole(clamp_exp(k_byte) - 127), seen ? (float)ve : neg_inf(), exp2_whole(-ve), 0.f);
+    }
+    scale_stage = -1;
     if (ld.left > 0) {
-      const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
-      const uint32_t dst = ring_u32 + stage * STAGE;
+      const int t0 = first_key(ld), t = t0 + lane;
+      const uint32_t dst = ring_u32 + stage * STAGE + lane_at;
       const bool in = t >= ld.s.lo && t < ld.s.len;
       const bool good = in && page >= 0 && page < p.num_pages;
       const int slot = t - page_of(p, t) * p.page_size;
-      const int64_t row = good ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)ld.g * p.kv_sh : -1;
+      const int64_t row = (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)ld.g * p.kv_sh;
       k_byte = v_byte = 127;
-      exps_stage = stage;
+      seen = in;
+      scale_stage = stage;
       if (good) {
         const int64_t at = (int64_t)page * p.exp_sp + (int64_t)ld.g * p.exp_sh + block_of(p, slot);
         k_byte = p.k_exp[at];
@@ -104,14 +120,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       } else if (in) {
         report((uint32_t)SPEC_STATUS_BAD_PAGE);
       }
-      __syncwarp();
+      const bool all = __all_sync(0xffffffffu, good);
+      // for rows i * RPI + rl the lane's part of the place is constant and i changes it by an offset and an XOR
+      if (whole_pages && all) {  // the usual case: 32 cached tokens of one page
+        int64_t off = __shfl_sync(0xffffffffu, row, 0) + (int64_t)rl * p.kv_st + c * 16;
+        const int64_t step = p.kv_st * RPI;
 #pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = i * RPI + rl;
-        const int64_t so = __shfl_sync(0xffffffffu, row, r);
-        const uint32_t at = dst + Mma8<D>::at(r, c);
-        cp_async16(at, kb + (so < 0 ? 0 : so) + c * 16, so >= 0);
-        cp_async16(at + 16 * D, vb + (so < 0 ? 0 : so) + c * 16, so >= 0);
+        for (int i = 0; i < kMma8Keys / RPI; ++i) {
+          const uint32_t at = (dst + i * RPI * D) ^ (D == 128 ? ((i * RPI) & 7) << 4 : 0);
+          cp_async16(at, kb + off);
+          cp_async16(at + kMma8Keys * D, vb + off);
+          off += step;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kMma8Keys / RPI; ++i) {
+          const int64_t so = __shfl_sync(0xffffffffu, good ? row : -1, i * RPI + rl);
+          const uint32_t at = (dst + i * RPI * D) ^ (D == 128 ? ((i * RPI) & 7) << 4 : 0);
+          cp_async16(at, kb + (so < 0 ? 0 : so + c * 16), so >= 0);
+          cp_async16(at + kMma8Keys * D, vb + (so < 0 ? 0 : so + c * 16), so >= 0);
+        }
       }
       ld.step(p);
       look_up();
@@ -129,6 +157,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   uint32_t qf[NR][KS][2];
   float o[NR][KS][4];  // columns d = ks * 16 + 2 gid (e < 2), + 1 (e >= 2) of rows nr * 8 + 2 tq + (e & 1)
   float qs[NR][2];     // what the scores of those rows are multiplied by
+  int pos[NR][2];      // their positions
   float m_run[NR][2], l_run[NR][2];  // the reference R, and the sum of 2^(s - R)
   int stage = 0;
   bool fresh_part = true;
@@ -136,7 +165,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   int part_u0 = cw.u;
   while (true) {
     const int rows = cw.s.n * p.G;
-    if (fresh_part) {
+    if (__builtin_expect(fresh_part, 0)) {
       fresh_part = false;
       part_u0 = cw.u;
 #pragma unroll
@@ -173,7 +202,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          m_run[nr][h] = neg_inf();
+          pos[nr][h] = cw.s.len - cw.s.n + (nr * 8 + tq * 2 + h) / p.G;
+          m_run[nr][h] = kNoReference;
           l_run[nr][h] = 0.f;
         }
       }
@@ -181,117 +211,133 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     issue(stage == 0 ? NS - 1 : stage - 1);  // NS - 1 units ahead
     cp_async_wait<NS - 1>();
     __syncwarp();
-    const uint32_t ks_u32 = ring_u32 + stage * STAGE;
-    const int key0 = (cw.s.lo & ~15) + cw.u * kMmaUnit + warp * 16;
-
-    // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
-    // few query rows are padded to 8 instead of 16
-    float s[NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nr][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      uint32_t w[4];
-      ldmatrix_x4(ks_u32 + Mma8<D>::at(frag_row, ks + frag_chunk), w[0], w[1], w[2], w[3]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a[4];
-        e4m3x4_to_f16x4(w[2 * i], a[0], a[2]);
-        e4m3x4_to_f16x4(w[2 * i + 1], a[1], a[3]);
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) mma_f16_16816(s[nr], a, qf[nr][ks + i][0], qf[nr][ks + i][1]);
-      }
-    }
-    // the scales of keys gid and gid + 8: the scores become s + ev, to the base of 2
-    float kscale[2], ev[2], vinv[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = s_exp[warp][stage][gid + 8 * i];
-      const int ke = clamp_exp(e & 255), ve = clamp_exp(e >> 8);
-      kscale[i] = exp2_whole(ke - 127);
-      ev[i] = (float)(ve - 127);
-      vinv[i] = exp2_whole(127 - ve);
-    }
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nr][e] = fmaf(s[nr][e], qs[nr][e & 1] * kscale[e >> 1], ev[e >> 1]);
-    // keys some row must not see: past the first new token, below the last row's window, or slots
-    // outside [lo, len)
     const int first_new = cw.s.len - cw.s.n;
-    if (key0 + 16 > first_new || key0 < cw.s.lo || (p.window > 0 && key0 < cw.s.len - p.window)) {
+#pragma unroll
+    for (int half = 0; half < 2 / KT; ++half) {
+      const uint32_t ks_u32 = ring_u32 + stage * STAGE + half * 16 * D, vs_u32 = ks_u32 + kMma8Keys * D;
+      const int key0 = first_key(cw) + half * 16;
+
+      // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
+      // few query rows are padded to 8 instead of 16
+      float s[KT][NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[kt][nr][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t w[KT][4];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+          ldmatrix_x4(ks_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t a[4];
+            e4m3x4_to_f16x4(w[kt][2 * i], a[0], a[2]);
+            e4m3x4_to_f16x4(w[kt][2 * i + 1], a[1], a[3]);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(s[kt][nr], a, qf[nr][ks + i][0], qf[nr][ks + i][1]);
+          }
+      }
+      // the scores s + ev to the base of 2 (keys outside [lo, len) have ev = -inf).  What is rare below is kept
+      // short and out of the way: the loop's instructions do not stay in the nearest cache, and jumps over long
+      // pieces of code cost more than the pieces (24 rows: 183 us with them unrolled in place)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const float4 a = s_scale[warp][stage][half * 16 + kt * 16 + gid], b = s_scale[warp][stage][half * 16 + kt * 16 + gid + 8];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[kt][nr][e] = fmaf(s[kt][nr][e], qs[nr][e & 1] * (e < 2 ? a.x : b.x), e < 2 ? a.y : b.y);
+      }
+      // some row must not see some of these keys: past the first new token, or below the last row's window
+      if (__builtin_expect(key0 + 16 * KT > first_new + 1 || (p.window > 0 && key0 < cw.s.len - p.window), 0)) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int last = pos[nr][h], before = p.window > 0 ? last - p.window : -1;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int t = key0 + kt * 16 + i * 8 + gid;
+                if (t > last || t <= before) s[kt][nr][2 * i + h] = neg_inf();
+              }
+          }
+      }
+      // the reference moves only when a score lies 2^15 above it, so most units need no exchange between
+      // lanes; it is then set 2^7 below the new maximum
+      bool over = false;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int pos = first_new + (nr * 8 + tq * 2 + (e & 1)) / p.G;
-          const int t = key0 + gid + (e & 2) * 4;
-          const bool vis = t <= pos && t < cw.s.len && t >= cw.s.lo && (p.window <= 0 || t > pos - p.window);
-          if (!vis) s[nr][e] = neg_inf();
-        }
-    }
-    // the reference moves only when a score lies 2^15 above it, so most units need no exchange between
-    // lanes; it is then set 2^7 below the new maximum
-    bool over = false;
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float x = fmaxf(s[nr][h], s[nr][2 + h]);
-        over |= x != neg_inf() && x > m_run[nr][h] + kRescaleLog2;
-      }
-    if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        float f[2];
-#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float x = fmaxf(s[nr][h], s[nr][2 + h]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = x == neg_inf() ? m_run[nr][h] : fmaxf(m_run[nr][h], x - kHeadroomLog2);
-          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - mn);
-          m_run[nr][h] = mn;
-          l_run[nr][h] *= f[h];
+          float x = fmaxf(s[0][nr][h], s[0][nr][2 + h]);
+          if constexpr (KT == 2) x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
+          over |= x > m_run[nr][h] + kRescaleLog2;
         }
+      if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          o[nr][ks][0] *= f[0];
-          o[nr][ks][1] *= f[1];
-          o[nr][ks][2] *= f[0];
-          o[nr][ks][3] *= f[1];
+        for (int nr = 0; nr < NR; ++nr) {
+          float f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = fmaxf(s[0][nr][h], s[0][nr][2 + h]);
+            if constexpr (KT == 2) x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m_run[nr][h], x - kHeadroomLog2);
+            f[h] = ex2_approx(m_run[nr][h] - mn);
+            m_run[nr][h] = mn;
+            l_run[nr][h] *= f[h];
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            o[nr][ks][0] *= f[0];
+            o[nr][ks][1] *= f[1];
+            o[nr][ks][2] *= f[0];
+            o[nr][ks][3] *= f[1];
+          }
         }
       }
-    }
-    uint32_t pf[NR][2];  // P^T as the B operand: 16 keys x 8 rows
+      uint32_t pf[KT][NR][2];  // P^T as the B operand: 16 keys x 8 rows
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      float e[4];
+      for (int kt = 0; kt < KT; ++kt) {
+        const float ia = s_scale[warp][stage][half * 16 + kt * 16 + gid].z, ib = s_scale[warp][stage][half * 16 + kt * 16 + gid + 8].z;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float m = m_run[nr][i & 1];
-        e[i] = ex2_approx(s[nr][i] - (m == neg_inf() ? 0.f : m));
+        for (int nr = 0; nr < NR; ++nr) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2_approx(s[kt][nr][i] - m_run[nr][i & 1]);
+          l_run[nr][0] = fmaf(e[0], ia, fmaf(e[2], ib, l_run[nr][0]));
+          l_run[nr][1] = fmaf(e[1], ia, fmaf(e[3], ib, l_run[nr][1]));
+          pf[kt][nr][0] = movmatrix_trans(pack_f16(e[0], e[1]));
+          pf[kt][nr][1] = movmatrix_trans(pack_f16(e[2], e[3]));
+        }
       }
-      l_run[nr][0] = fmaf(e[0], vinv[0], fmaf(e[2], vinv[1], l_run[nr][0]));
-      l_run[nr][1] = fmaf(e[1], vinv[0], fmaf(e[3], vinv[1], l_run[nr][1]));
-      pf[nr][0] = movmatrix_trans(pack_f16(e[0], e[1]));
-      pf[nr][1] = movmatrix_trans(pack_f16(e[2], e[3]));
-    }
-    // O^T += V^T P^T
+      // O^T += V^T P^T
 #pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      uint32_t w[4];
-      ldmatrix_x4_trans(ks_u32 + 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[0], w[1], w[2], w[3]);
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t w[KT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a[4];
-        e4m3x4_to_f16x4(__byte_perm(w[2 * i], 0, 0x3120), a[0], a[1]);
-        e4m3x4_to_f16x4(__byte_perm(w[2 * i + 1], 0, 0x3120), a[2], a[3]);
+        for (int kt = 0; kt < KT; ++kt)
+          ldmatrix_x4_trans(vs_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][ks + i], a, pf[nr][0], pf[nr][1]);
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[4];
+            e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][ks + i], a, pf[kt][nr][0], pf[kt][nr][1]);
+          }
       }
     }
     __syncwarp();  // every lane has read the stage before it is refilled
@@ -299,7 +345,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
     // ---- end of the part: join the warps' states
     const bool last = cw.left == 1;
-    if (cw.u + 1 == cw.nu || last) {
+    if (__builtin_expect(cw.u + 1 == cw.nu || last, 0)) {
       const bool whole = part_u0 == 0 && cw.u + 1 == cw.nu;
       const int64_t rec = 2 * (int64_t)cta + (starts_at_begin ? 0 : 1);
       starts_at_begin = false;
@@ -324,7 +370,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           float M = neg_inf();
 #pragma unroll
           for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
-          f[h] = m_run[nr][h] == neg_inf() ? 0.f : ex2_approx(m_run[nr][h] - M);
+          f[h] = ex2_approx(m_run[nr][h] - M);
         }
         // the warps' columns of 8 rows x 64 columns through shared memory; then a warp per row adds
         // them up, two columns per lane
@@ -335,10 +381,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
         for (int w = 0; w < kMmaWarps; ++w) {
           const float2 v = s_ml[w][r];
-          L += v.x == neg_inf() ? 0.f : ex2_approx(v.x - M) * v.y;
+          L += ex2_approx(v.x - M) * v.y;
         }
         const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-        if (!whole && r < rows && lane == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M, L);
+        if (!whole && r < rows && lane == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M == kNoReference ? neg_inf() : M, L);
 #pragma unroll
         for (int c4 = 0; c4 < D / 64; ++c4) {
 #pragma unroll
@@ -400,7 +446,7 @@ static cudaError_t launch_mma8(const Kv8Params& p, cudaStream_t stream) {
   } else {
     e = launch_dependent(paged8_mma<D, NR>, grid, dim3(kMmaThreads), smem, stream, 0u, p);
   }
-  return e != cudaSuccess || p.direct ? e : launch_paged_mma_merge(p, stream);
+  return e != cudaSuccess || p.direct ? e : launch_paged_mma_merge(p, kMma8Unit, stream);
 }
 
 template <int D>

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   if (cta == 0 && tid == 0) status_clear_for_launch(p.status);
 
   // ---- this CTA's units
-  MmaWalk ld;
+  MmaWalk<kMmaUnit> ld;
   if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, [&](uint32_t bits) { status_report(p.status, bits); })) return;
 
   // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   const __nv_bfloat16* vb = reinterpret_cast<const __nv_bfloat16*>(p.v);
   const __nv_bfloat16* knew = reinterpret_cast<const __nv_bfloat16*>(p.k_new);
   const __nv_bfloat16* vnew = reinterpret_cast<const __nv_bfloat16*>(p.v_new);
-  MmaWalk cw = ld;  // the unit in compute
+  MmaWalk<kMmaUnit> cw = ld;  // the unit in compute
   int page = -1;
   auto look_up = [&]() {  // page id of this lane's key (lanes 16-31 repeat lanes 0-15)
     const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
@@ -367,21 +367,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
 // grid (segments, rows / 8), a warp per row; a batch of records' statistics and values are all in flight
 // at once.
 constexpr int kMmaMergeBatch = 4;
-template <int D>
+template <int D, int UNIT>
 __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_constant__ ServeAttnParams p) {
   __shared__ int64_t s_scan[kMmaWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv, r = blockIdx.y * kMmaWarps + warp;
   int64_t before = 0, all = 0;
   for (int i = tid; i < p.B; i += kMmaThreads) {
-    const int u = mma_units(seq_info(p, i));
+    const int u = mma_units<UNIT>(seq_info(p, i));
     all += u;
     if (i < b) before += u;
   }
   const int64_t total = block_sum(all, s_scan) * p.Hkv;
   before = block_sum(before, s_scan) * p.Hkv;
   const SeqInfo s = seq_info(p, b);
-  const int nu = mma_units(s);
+  const int nu = mma_units<UNIT>(s);
   const int64_t per = mma_per_cta(total, p.grid);
   const int64_t start = before + (int64_t)g * nu;
   const int64_t c0 = start / per;
@@ -445,10 +445,14 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p) {
   p->part_o = reinterpret_cast<float*>(b + 256 + 2 * (size_t)kServeMaxGrid * kMmaMaxRows * sizeof(float2));
 }
 
-cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, cudaStream_t stream) {
+template <int UNIT>
+static cudaError_t launch_merge(const ServeAttnParams& p, cudaStream_t stream) {
   const dim3 grid(p.B * p.Hkv, (unsigned)(p.max_q * p.G + kMmaWarps - 1) / kMmaWarps);
-  if (p.D == 128) return launch_dependent(paged_mma_merge<128>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
-  return launch_dependent(paged_mma_merge<64>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+  if (p.D == 128) return launch_dependent(paged_mma_merge<128, UNIT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+  return launch_dependent(paged_mma_merge<64, UNIT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+}
+cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, int unit, cudaStream_t stream) {
+  return unit == kMmaUnit ? launch_merge<kMmaUnit>(p, stream) : launch_merge<kMma8Unit>(p, stream);
 }
 
 template <int D, int NR>
@@ -460,7 +464,7 @@ static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.direct) return e;
-  return launch_paged_mma_merge(p, stream);
+  return launch_merge<kMmaUnit>(p, stream);
 }
 
 template <int D>
