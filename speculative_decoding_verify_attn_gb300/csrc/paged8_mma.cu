@@ -57,11 +57,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   constexpr int RPI = 32 / KS;        // rows one cp.async instruction of the warp covers
   constexpr int NS = Mma8<D>::kStages;
   constexpr int STAGE = Mma8<D>::kStage;
-  constexpr int KT = NR <= 3 ? 2 : 1; // tiles of 16 keys at a time: two, as far as the registers go
+  constexpr int KT = 2;               // tiles of 16 keys at a time
   extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int64_t s_scan[kMmaWarps];
   __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
-  __shared__ float4 s_scale[kMmaWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent, 1 / V's scale
+  __shared__ float2 s_scale[kMmaWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent
+  __shared__ uint2 s_q[NR][KS][32];  // the query's fragments
+  __shared__ float s_undo[NR * 8];   // what a row's scores are multiplied by
+  __shared__ int s_pos[NR * 8];      // its position
   __shared__ int s_b;
   __shared__ int64_t s_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,8 +102,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   int scale_stage = -1;
   auto issue = [&](int stage) {
     if (scale_stage >= 0) {
-      const int ve = clamp_exp(v_byte) - 127;
-      s_scale[warp][scale_stage][lane] = make_float4(exp2_whole(clamp_exp(k_byte) - 127), seen ? (float)ve : neg_inf(), exp2_whole(-ve), 0.f);
+      s_scale[warp][scale_stage][lane] = make_float2(exp2_whole(clamp_exp(k_byte) - 127), seen ? (float)(clamp_exp(v_byte) - 127) : neg_inf());
     }
     scale_stage = -1;
     if (ld.left > 0) {
@@ -154,10 +156,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const int gid = lane >> 2, tq = lane & 3;
   // places of the fragments' rows: K: matrices (keys 0-7, 8-15) x (chunk, chunk + 1); V alike
   const int frag_row = lane & 15, frag_chunk = lane >> 4;
-  uint32_t qf[NR][KS][2];
   float o[NR][KS][4];  // columns d = ks * 16 + 2 gid (e < 2), + 1 (e >= 2) of rows nr * 8 + 2 tq + (e & 1)
   float qs[NR][2];     // what the scores of those rows are multiplied by
-  int pos[NR][2];      // their positions
   float m_run[NR][2], l_run[NR][2];  // the reference R, and the sum of 2^(s - R)
   int stage = 0;
   bool fresh_part = true;
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (__builtin_expect(fresh_part, 0)) {
       fresh_part = false;
       part_u0 = cw.u;
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
+      // the query's fragments, the same for all warps: each makes some of the tiles of 8 rows
+      for (int nr = warp; nr < NR; nr += kMmaWarps) {
         const int r = nr * 8 + gid;
         const bool real = r < rows;
         // four neighbouring values of each step of 16, as K's rows come
@@ -189,20 +189,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float undo;
         const float up = f16_row_scale(amax, undo);
-        qs[nr][0] = q_factor(__shfl_sync(0xffffffffu, undo, tq * 8), p.scale_log2);
-        qs[nr][1] = q_factor(__shfl_sync(0xffffffffu, undo, tq * 8 + 4), p.scale_log2);
+        if (tq == 0) {
+          s_undo[r] = q_factor(undo, p.scale_log2);
+          s_pos[r] = cw.s.len - cw.s.n + r / p.G;
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+          uint32_t f[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            qf[nr][ks][i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+            f[i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+          s_q[nr][ks][lane] = make_uint2(f[0], f[1]);
+        }
+      }
+      __syncthreads();  // the part before has ended with one, too
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nr][ks][e] = 0.f;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          pos[nr][h] = cw.s.len - cw.s.n + (nr * 8 + tq * 2 + h) / p.G;
+          qs[nr][h] = s_undo[nr * 8 + tq * 2 + h];
           m_run[nr][h] = kNoReference;
           l_run[nr][h] = 0.f;
         }
@@ -212,133 +222,136 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     cp_async_wait<NS - 1>();
     __syncwarp();
     const int first_new = cw.s.len - cw.s.n;
-#pragma unroll
-    for (int half = 0; half < 2 / KT; ++half) {
-      const uint32_t ks_u32 = ring_u32 + stage * STAGE + half * 16 * D, vs_u32 = ks_u32 + kMma8Keys * D;
-      const int key0 = first_key(cw) + half * 16;
+    const uint32_t ks_u32 = ring_u32 + stage * STAGE, vs_u32 = ks_u32 + kMma8Keys * D;
+    const int key0 = first_key(cw);
 
-      // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
-      // few query rows are padded to 8 instead of 16
-      float s[KT][NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
+    // S^T = K Q^T: 16 keys x 8 rows per tile, the keys on the matrix instruction's 16-row side, so
+    // few query rows are padded to 8 instead of 16
+    float s[KT][NR][4];  // keys gid (e = 0, 1), gid + 8 (e = 2, 3); rows nr * 8 + 2 tq + (e & 1)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kt][nr][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      uint32_t w[KT][4];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
+        ldmatrix_x4(ks_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+      for (int i = 0; i < 2; ++i) {
+        uint2 q[NR];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[kt][nr][e] = 0.f;
+        for (int nr = 0; nr < NR; ++nr) q[nr] = s_q[nr][ks + i][lane];
 #pragma unroll
-      for (int ks = 0; ks < KS; ks += 2) {
-        uint32_t w[KT][4];
+        for (int kt = 0; kt < KT; ++kt) {
+          uint32_t a[4];
+          e4m3x4_to_f16x4(w[kt][2 * i], a[0], a[2]);
+          e4m3x4_to_f16x4(w[kt][2 * i + 1], a[1], a[3]);
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-          ldmatrix_x4(ks_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            uint32_t a[4];
-            e4m3x4_to_f16x4(w[kt][2 * i], a[0], a[2]);
-            e4m3x4_to_f16x4(w[kt][2 * i + 1], a[1], a[3]);
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(s[kt][nr], a, qf[nr][ks + i][0], qf[nr][ks + i][1]);
-          }
+          for (int nr = 0; nr < NR; ++nr) mma_f16_16816(s[kt][nr], a, q[nr].x, q[nr].y);
+        }
       }
-      // the scores s + ev to the base of 2 (keys outside [lo, len) have ev = -inf).  What is rare below is kept
-      // short and out of the way: the loop's instructions do not stay in the nearest cache, and jumps over long
-      // pieces of code cost more than the pieces (24 rows: 183 us with them unrolled in place)
+    }
+    // the scores s + ev to the base of 2 (keys outside [lo, len) have ev = -inf).  What is rare below is kept
+    // short and out of the way: the loop's instructions do not stay in the nearest cache, and jumps over long
+    // pieces of code cost more than the pieces (24 rows: 183 us with them unrolled in place)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const float4 a = s_scale[warp][stage][half * 16 + kt * 16 + gid], b = s_scale[warp][stage][half * 16 + kt * 16 + gid + 8];
+    for (int kt = 0; kt < KT; ++kt) {
+      const float2 a = s_scale[warp][stage][kt * 16 + gid], b = s_scale[warp][stage][kt * 16 + gid + 8];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[kt][nr][e] = fmaf(s[kt][nr][e], qs[nr][e & 1] * (e < 2 ? a.x : b.x), e < 2 ? a.y : b.y);
-      }
-      // some row must not see some of these keys: past the first new token, or below the last row's window
-      if (__builtin_expect(key0 + 16 * KT > first_new + 1 || (p.window > 0 && key0 < cw.s.len - p.window), 0)) {
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int last = pos[nr][h], before = p.window > 0 ? last - p.window : -1;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int t = key0 + kt * 16 + i * 8 + gid;
-                if (t > last || t <= before) s[kt][nr][2 * i + h] = neg_inf();
-              }
-          }
-      }
-      // the reference moves only when a score lies 2^15 above it, so most units need no exchange between
-      // lanes; it is then set 2^7 below the new maximum
-      bool over = false;
+        for (int e = 0; e < 4; ++e) s[kt][nr][e] = fmaf(s[kt][nr][e], qs[nr][e & 1] * (e < 2 ? a.x : b.x), e < 2 ? a.y : b.y);
+    }
+    // some row must not see some of these keys: past the first new token, or below the last row's window
+    if (__builtin_expect(key0 + 16 * KT > first_new + 1 || (p.window > 0 && key0 < cw.s.len - p.window), 0)) {
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const int last = s_pos[nr * 8 + tq * 2 + h], before = p.window > 0 ? last - p.window : -1;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int t = key0 + kt * 16 + i * 8 + gid;
+              if (t > last || t <= before) s[kt][nr][2 * i + h] = neg_inf();
+            }
+        }
+    }
+    // the reference moves only when a score lies 2^15 above it, so most units need no exchange between
+    // lanes; it is then set 2^7 below the new maximum
+    bool over = false;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = fmaxf(s[0][nr][h], s[0][nr][2 + h]);
+        x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
+        over |= x > m_run[nr][h] + kRescaleLog2;
+      }
+    if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           float x = fmaxf(s[0][nr][h], s[0][nr][2 + h]);
-          if constexpr (KT == 2) x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
-          over |= x > m_run[nr][h] + kRescaleLog2;
+          x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m_run[nr][h], x - kHeadroomLog2);
+          f[h] = ex2_approx(m_run[nr][h] - mn);
+          m_run[nr][h] = mn;
+          l_run[nr][h] *= f[h];
         }
-      if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          float f[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(s[0][nr][h], s[0][nr][2 + h]);
-            if constexpr (KT == 2) x = fmax3(x, s[1][nr][h], s[1][nr][2 + h]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m_run[nr][h], x - kHeadroomLog2);
-            f[h] = ex2_approx(m_run[nr][h] - mn);
-            m_run[nr][h] = mn;
-            l_run[nr][h] *= f[h];
-          }
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            o[nr][ks][0] *= f[0];
-            o[nr][ks][1] *= f[1];
-            o[nr][ks][2] *= f[0];
-            o[nr][ks][3] *= f[1];
-          }
+        for (int ks = 0; ks < KS; ++ks) {
+          o[nr][ks][0] *= f[0];
+          o[nr][ks][1] *= f[1];
+          o[nr][ks][2] *= f[0];
+          o[nr][ks][3] *= f[1];
         }
       }
-      uint32_t pf[KT][NR][2];  // P^T as the B operand: 16 keys x 8 rows
+    }
+    uint32_t pf[KT][NR][2];  // P^T as the B operand: 16 keys x 8 rows
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const float ia = s_scale[warp][stage][half * 16 + kt * 16 + gid].z, ib = s_scale[warp][stage][half * 16 + kt * 16 + gid + 8].z;
+    for (int kt = 0; kt < KT; ++kt) {
+      // 2^-ev; finite where ev is -inf, whose e is 0
+      const float ia = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid].y), -kNoReference);
+      const float ib = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid + 8].y), -kNoReference);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          float e[4];
+      for (int nr = 0; nr < NR; ++nr) {
+        float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2_approx(s[kt][nr][i] - m_run[nr][i & 1]);
-          l_run[nr][0] = fmaf(e[0], ia, fmaf(e[2], ib, l_run[nr][0]));
-          l_run[nr][1] = fmaf(e[1], ia, fmaf(e[3], ib, l_run[nr][1]));
-          pf[kt][nr][0] = movmatrix_trans(pack_f16(e[0], e[1]));
-          pf[kt][nr][1] = movmatrix_trans(pack_f16(e[2], e[3]));
+        for (int i = 0; i < 4; ++i) e[i] = ex2_approx(s[kt][nr][i] - m_run[nr][i & 1]);
+        l_run[nr][0] = fmaf(e[0], ia, fmaf(e[2], ib, l_run[nr][0]));
+        l_run[nr][1] = fmaf(e[1], ia, fmaf(e[3], ib, l_run[nr][1]));
+        pf[kt][nr][0] = movmatrix_trans(pack_f16(e[0], e[1]));
+        pf[kt][nr][1] = movmatrix_trans(pack_f16(e[2], e[3]));
+      }
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      uint32_t w[KT][4];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+        ldmatrix_x4_trans(vs_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a[4];
+          e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i], 0, 0x3120), a[0], a[1]);
+          e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][ks + i], a, pf[kt][nr][0], pf[kt][nr][1]);
         }
-      }
-      // O^T += V^T P^T
-#pragma unroll
-      for (int ks = 0; ks < KS; ks += 2) {
-        uint32_t w[KT][4];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-          ldmatrix_x4_trans(vs_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t a[4];
-            e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i], 0, 0x3120), a[0], a[1]);
-            e4m3x4_to_f16x4(__byte_perm(w[kt][2 * i + 1], 0, 0x3120), a[2], a[3]);
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][ks + i], a, pf[kt][nr][0], pf[kt][nr][1]);
-          }
-      }
     }
     __syncwarp();  // every lane has read the stage before it is refilled
     stage = stage == NS - 1 ? 0 : stage + 1;
