@@ -201,8 +201,6 @@ int spec_rotary(const spec_rotary_args* a, spec_stream_t stream) {
   p.f32 = a->dtype == SPEC_F32;
   p.negate = a->inverse;
   p.amplitude = a->amplitude != 0.f ? a->amplitude : 1.f;
-  const int per = 16 / elem;
-  p.vec = p.pairs ? a->rot % per == 0 : a->rot / 2 % per == 0;
   p.q = a->q; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;
   p.k = a->k; p.k_st = a->k_stride_t; p.k_sh = a->k_stride_h;
   p.qo = a->q_out; p.qo_st = a->qo_stride_t; p.qo_sh = a->qo_stride_h;

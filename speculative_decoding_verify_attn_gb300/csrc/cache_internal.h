@@ -14,7 +14,6 @@ namespace specv {
 // ------------------------------------------------------------------ rotary positions
 struct RotaryParams {
   int T, Hq, Hkv, D, rot, pairs, f32, B, negate;
-  int vec;                // 16-byte accesses suit rot and the layout
   int tile;               // tokens per CTA
   float amplitude;
   const void* q;

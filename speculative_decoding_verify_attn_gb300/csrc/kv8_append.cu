@@ -5,7 +5,8 @@
 // its own, and where that grows the earlier rows are brought to it; then the new rows are scaled
 // (exactly: a power of two), rounded and stored.  A block's rows are therefore in one warp's hands, and
 // nothing has to be ordered between warps.
-// A lane holds 16 values of a row, so that a store is 16 bytes; the second pass over the rows reads L1.
+// A lane holds 16 values of a row, so that a store is 16 bytes.  Up to 32 rows of 128 values (bf16) stay in
+// registers between the two steps, all loads of them in flight at once; larger blocks are read twice.
 // Bound: HBM for prompts (2 or 4 bytes read and 1 written per value), latency for a round's few rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -19,32 +20,55 @@ namespace specv {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendWarps = kAppendThreads / 32;
 
+// 16 values of a row as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ void load16(const void* src, int64_t at, float (&v)[16]) {
-  if constexpr (F32) {
-    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(src) + at);
+struct Raw16 {
+  static constexpr int W = F32 ? 4 : 2;
+  uint4 w[W];
+  __device__ __forceinline__ void load(const void* src, int64_t at) {
+    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(src) + at * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 w = __ldg(s + i);
-      v[4 * i] = __uint_as_float(w.x);
-      v[4 * i + 1] = __uint_as_float(w.y);
-      v[4 * i + 2] = __uint_as_float(w.z);
-      v[4 * i + 3] = __uint_as_float(w.w);
-    }
-  } else {
-    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + at);
+    for (int i = 0; i < W; ++i) w[i] = __ldg(s + i);
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 w = __ldg(s + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
-        v[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-      }
+    for (int i = 0; i < W; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // value 4 j + i of the 16
+  __device__ __forceinline__ void four(int j, float (&v)[4]) const {
+    if constexpr (F32) {
+      v[0] = __uint_as_float(w[j].x); v[1] = __uint_as_float(w[j].y); v[2] = __uint_as_float(w[j].z); v[3] = __uint_as_float(w[j].w);
+    } else {
+      const uint32_t a = j & 1 ? w[j >> 1].z : w[j >> 1].x, b = j & 1 ? w[j >> 1].w : w[j >> 1].y;
+      v[0] = __uint_as_float(a << 16); v[1] = __uint_as_float(a & 0xffff0000u);
+      v[2] = __uint_as_float(b << 16); v[3] = __uint_as_float(b & 0xffff0000u);
     }
   }
-}
+  // the largest finite magnitude, and `amax`
+  __device__ __forceinline__ float magnitude(float amax) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+      four(j, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = fabsf(v[i]);
+        amax = fmaxf(amax, a <= 3.402823466e38f ? a : 0.f);
+      }
+    }
+    return amax;
+  }
+  __device__ __forceinline__ uint4 encode(float scale) const {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+      four(j, v);
+      u[j] = f32x4_to_e4m3x4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
 
 // Blocks that get new tokens.
 __device__ __forceinline__ int touched_blocks(const Kv8Params& p, const SeqInfo& s) {
@@ -55,14 +79,18 @@ template <bool F32, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_constant__ Kv8Params p, int first) {
   pdl_launch_dependents();
   constexpr int LANES = D / 16, ROWS = 32 / LANES;  // lanes of a row, rows of an instruction
+  constexpr int HELD = F32 ? 4 : 8;                 // of a lane's rows that registers hold (64)
   extern __shared__ int s_pre[];  // [B + 1] blocks before each sequence
   __shared__ int s_sum[kAppendWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (!first) pdl_wait();
   if (first && blockIdx.x == 0 && tid == 0) status_clear_for_launch(p.status);
   auto report = [&](uint32_t bits) {
-    if (first) status_report(p.status, bits);
-    else atomicOr(p.status, bits);
+    if (first) {
+      status_report(p.status, bits);
+    } else {
+      pdl_wait();  // the kernel before clears the status
+      atomicOr(p.status, bits);
+    }
   };
   // prefix sums over the sequences: T rows make at most T blocks, but sequences that overlap can claim more
   int run = 0;
@@ -122,14 +150,24 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_consta
     uint8_t* exp = (is_v ? p.v_exp : p.k_exp) + (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
     uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? p.v : p.k) + (int64_t)page * p.kv_sp + (int64_t)g * p.kv_sh + c * 16;
     const int old = begin > t0 ? clamp_exp(*exp) : 0;
+    const int rows = end - begin;
+    const bool held = rows <= HELD * ROWS;
+    Raw16<F32> x[HELD];
     float amax = 0.f;
-    for (int r = rl; r < end - begin; r += ROWS) {
-      float v[16];
-      load16<F32>(src, from + (int64_t)r * p.new_st, v);
+    if (held) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a = fabsf(v[i]);
-        amax = fmaxf(amax, a <= 3.402823466e38f ? a : 0.f);
+      for (int i = 0; i < HELD; ++i) {
+        if (i * ROWS + rl < rows) x[i].load(src, from + (int64_t)(i * ROWS + rl) * p.new_st);
+        else x[i].clear();
+      }
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) amax = x[i].magnitude(amax);
+    } else {
+#pragma unroll 4
+      for (int r = rl; r < rows; r += ROWS) {
+        Raw16<F32> y;
+        y.load(src, from + (int64_t)r * p.new_st);
+        amax = y.magnitude(amax);
       }
     }
     amax = warp_max(amax);
@@ -151,20 +189,25 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_consta
       }
     }
     const float scale = exp2_whole(127 - e);
-    for (int r = rl; r < end - begin; r += ROWS) {
-      float v[16];
-      load16<F32>(src, from + (int64_t)r * p.new_st, v);
-      uint4 w;
-      uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+    uint8_t* to = dst + (int64_t)(slot + begin - t0) * p.kv_st;
+    if (held) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        u[i] = f32x4_to_e4m3x4(v[4 * i] * scale, v[4 * i + 1] * scale, v[4 * i + 2] * scale, v[4 * i + 3] * scale);
-      *reinterpret_cast<uint4*>(dst + (int64_t)(slot + begin - t0 + r) * p.kv_st) = w;
+      for (int i = 0; i < HELD; ++i)
+        if (i * ROWS + rl < rows) *reinterpret_cast<uint4*>(to + (int64_t)(i * ROWS + rl) * p.kv_st) = x[i].encode(scale);
+    } else {
+#pragma unroll 4
+      for (int r = rl; r < rows; r += ROWS) {
+        Raw16<F32> y;
+        y.load(src, from + (int64_t)r * p.new_st);
+        *reinterpret_cast<uint4*>(to + (int64_t)r * p.kv_st) = y.encode(scale);
+      }
     }
     __syncwarp();
     if (lane == 0) *exp = (uint8_t)e;
   }
-  // see pdl_wait above: a grid that is not the call's first has waited in every CTA
+  // the kernel before (a plan) is none of the append's business but for the status; what follows is ordered behind
+  // this grid alone, so it is not over before that kernel
+  if (!first) pdl_wait();
 }
 
 template <bool F32, int D>

@@ -52,7 +52,6 @@ template <int D, int NR>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     paged8_mma(const __grid_constant__ Kv8Params p) {
   pdl_launch_dependents();
-  if (!p.first) pdl_wait();  // the append
   constexpr int KS = D / 16;          // k steps of K Q^T, m tiles of V^T P^T, 16-byte chunks of a row
   constexpr int RPI = 32 / KS;        // rows one cp.async instruction of the warp covers
   constexpr int NS = Mma8<D>::kStages;
@@ -71,13 +70,27 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const int cta = blockIdx.x;
   float* cmb = reinterpret_cast<float*>(smem + (size_t)kMmaWarps * NS * STAGE);
   if (p.first && cta == 0 && tid == 0) status_clear_for_launch(p.status);
+  // Behind an append only its own tokens, and the block that the first of them lies in, have to be waited for: the
+  // earlier keys are on their way meanwhile.  `waited`: this warp has
+  bool waited = p.first;
+  auto wait = [&]() {
+    if (!waited) pdl_wait();
+    waited = true;
+  };
   auto report = [&](uint32_t bits) {
-    if (p.first) status_report(p.status, bits);
-    else atomicOr(p.status, bits);
+    if (p.first) {
+      status_report(p.status, bits);
+    } else {
+      pdl_wait();  // the append clears the status
+      atomicOr(p.status, bits);
+    }
   };
 
   MmaWalk<kMma8Unit> ld;
-  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) return;
+  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) {
+    wait();  // what follows in the stream is ordered behind this grid alone
+    return;
+  }
 
   // ---- loads: the warp's 32 keys of the unit at `ld`, a lane each for page ids (fetched one unit ahead) and scales
   const uint32_t ring_u32 = smem_u32(smem + (size_t)warp * NS * STAGE);
@@ -108,6 +121,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (ld.left > 0) {
       const int t0 = first_key(ld), t = t0 + lane;
       const uint32_t dst = ring_u32 + stage * STAGE + lane_at;
+      if (!waited && t0 + kMma8Keys > (ld.s.len - ld.s.n) / p.block * p.block) wait();
       const bool in = t >= ld.s.lo && t < ld.s.len;
       const bool good = in && page >= 0 && page < p.num_pages;
       const int slot = t - page_of(p, t) * p.page_size;
@@ -445,6 +459,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     cw.step(p);
   }
   cp_async_wait<0>();
+  wait();
 }
 
 template <int D, int NR>

@@ -61,7 +61,8 @@ def turns_to_frequencies(steps):
     (1, 1, 1, 8, 2, "bf16", 10), (5, 4, 1, 64, 64, "f32", 500), (3, 32, 8, 128, 128, "bf16", 32768),
     (17, 5, 3, 128, 116, "bf16", 1 << 20), (9, 2, 2, 64, 20, "f32", 1 << 24), (700, 3, 1, 128, 32, "bf16", 2 ** 31 - 1),
     (1300, 2, 1, 64, 64, "f32", 100000), (5000, 4, 2, 128, 64, "bf16", 4096), (4, 1, 1, 1024, 1024, "bf16", 1000),
-    (4, 2, 0, 256, 256, "f32", 1000), (6, 0, 2, 80, 48, "bf16", 1000)])
+    (4, 2, 0, 256, 256, "f32", 1000), (6, 0, 2, 80, 48, "bf16", 1000), (9, 2, 2, 64, 24, "bf16", 1000), (9, 2, 2, 64, 10, "f32", 1000),
+    (3, 2, 1, 1024, 1022, "bf16", 1000), (30, 7, 5, 64, 6, "bf16", 1000)])
 def test_rotary_parity(sv, T, Hq, Hkv, D, rot, dtype, far, pairs):
     torch = torch_mod()
     rng = np.random.default_rng(T + D + rot)
