@@ -9,6 +9,7 @@ them into the argument struct and calls the library on the current stream of the
 from __future__ import annotations
 
 import ctypes
+from array import array
 from ctypes import POINTER, Structure, byref, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 from . import serving as _s
@@ -158,26 +159,27 @@ def spec_rotary_steps(rot: int, base: float = 10000.0, *, kind: int = SPEC_ROTAR
     return steps.to(device), amplitude.value
 
 
+_NONE = (0, None, 0, 0, None, 0, 0)
+
+
 def _heads(name, x, out, T, D, dtype):
-    """Pointers and strides of q or k and its output: ten zeros where it is missing."""
+    """Heads of q or k, its pointer and strides and its output's."""
     if x is None:
         if out is not None:
             raise ValueError(f"{name}_out without {name}")
-        return 0, (None, 0, 0), (None, 0, 0)
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.dtype is not dtype:
+        return _NONE
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or x.dtype is not dtype:
         raise ValueError(f"{name} must be [{T}, heads, {D}] of {dtype}")
-    if out is None:
-        out = x
-    elif out.shape != x.shape or out.dtype is not dtype:
+    H, st = shape[1], _rows(name, x)
+    # the stride of a dimension of one element may be anything: D stands in its place
+    ptr, s0, s1 = x.data_ptr(), st[0] if T > 1 else D, st[1] if H > 1 else D
+    if out is None or out is x:
+        return H, ptr, s0, s1, ptr, s0, s1
+    if out.shape != shape or out.dtype is not dtype:
         raise ValueError(f"{name}_out must be like {name}")
-    H = x.shape[1]
-
-    def three(t):
-        st = _rows(name, t)
-        # the stride of a dimension of one element may be anything: D stands in its place
-        return t.data_ptr(), st[0] if T > 1 else D, st[1] if H > 1 else D
-
-    return H, three(x), three(out)
+    st = _rows(name + "_out", out)
+    return H, ptr, s0, s1, out.data_ptr(), st[0] if T > 1 else D, st[1] if H > 1 else D
 
 
 def rotary_args(q, k, steps, *, positions=None, q_start=None, kv_len=None, q_out=None, k_out=None,
@@ -188,8 +190,9 @@ def rotary_args(q, k, steps, *, positions=None, q_start=None, kv_len=None, q_out
     if x is None:
         raise ValueError("neither q nor k")
     T, _, D = x.shape
-    Hq, qi, qo = _heads("q", q, q_out, T, D, x.dtype)
-    Hkv, ki, ko = _heads("k", k, k_out, T, D, x.dtype)
+    dtype = x.dtype
+    Hq, q_ptr, q0, q1, qo_ptr, qo0, qo1 = _heads("q", q, q_out, T, D, dtype)
+    Hkv, k_ptr, k0, k1, ko_ptr, ko0, ko1 = _heads("k", k, k_out, T, D, dtype)
     if steps.dim() != 1 or steps.dtype is not torch.int64 or not steps.is_contiguous():
         raise ValueError("steps must be a contiguous int64 vector")
     B = 0
@@ -209,8 +212,11 @@ def rotary_args(q, k, steps, *, positions=None, q_start=None, kv_len=None, q_out
     amplitude = float(amplitude)
     if not c_float(amplitude).value > 0:  # the struct's 0 stands for 1
         raise ValueError(f"amplitude must be above 0, got {amplitude}")
-    return SpecRotaryArgs(_size(T), Hq, Hkv, _size(D), _size(2 * steps.shape[0]), _whole(layout), _dtype_code(x),
-                          1 if inverse else 0, _size(B), amplitude, *qi, *ki, *qo, *ko, steps.data_ptr(), ps, st, kl, None, 0)
+    rot = 2 * steps.shape[0]
+    if T > _TOP or D > _TOP or B > _TOP or rot > _TOP:
+        raise ValueError("sizes past 32 bits")
+    return SpecRotaryArgs(T, Hq, Hkv, D, rot, _whole(layout), _dtype_code(x), 1 if inverse else 0, B, amplitude, q_ptr, q0, q1,
+                          k_ptr, k0, k1, qo_ptr, qo0, qo1, ko_ptr, ko0, ko1, steps.data_ptr(), ps, st, kl, None, 0)
 
 
 def spec_rotary_workspace(q, k, steps) -> int:
@@ -231,7 +237,7 @@ def spec_rotary(q, k, steps, *, positions=None, q_start=None, kv_len=None, q_out
     positions [T] int32, or q_start [B + 1] and kv_len [B] as in spec_paged_attn (rows of no sequence are left
     as they were).  q_out, k_out: outputs, None for in place.  inverse turns back, which is also what gradients
     take.  Returns (q_out, k_out)."""
-    index = _check([t for t in (q, k, steps, positions, q_start, kv_len, q_out, k_out) if t is not None])
+    index = _check((steps, q, k, positions, q_start, kv_len, q_out, k_out))
     a = rotary_args(q, k, steps, positions=positions, q_start=q_start, kv_len=kv_len, q_out=q_out, k_out=k_out,
                     layout=layout, amplitude=amplitude, inverse=inverse)
     _run("spec_rotary", a, (a.T, a.Hq, a.Hkv, a.D, a.rot, a.layout, a.dtype, "rotary"), index, workspace, stream)
@@ -239,28 +245,44 @@ def spec_rotary(q, k, steps, *, positions=None, q_start=None, kv_len=None, q_out
 
 
 # ---------------------------------------------------------------------------- the cache in 8 bits
+_e4m3 = _u8 = None
+
+
+def _types():
+    global _e4m3, _u8
+    torch = _t()
+    _e4m3, _u8 = torch.float8_e4m3fn, torch.uint8
+
+
 def _cache8(k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_len, D):
     """Checks the cache and the tables; (B, Hkv, page_size, pages, cols, block, pointers and strides)."""
-    torch = _t()
-    if k_pages.dim() != 4 or k_pages.dtype is not torch.float8_e4m3fn or v_pages.dtype is not torch.float8_e4m3fn:
+    _e4m3 or _types()
+    shape, ks = k_pages.shape, k_pages.stride()
+    if k_pages.dtype is not _e4m3 or v_pages.dtype is not _e4m3 or len(shape) != 4:
         raise TypeError("k_pages, v_pages must be [pages, Hkv, page_size, D] of float8_e4m3fn")
-    pages, Hkv, page_size, D2 = k_pages.shape
-    ks = _rows("k_pages", k_pages)
-    if D2 != D or v_pages.shape != k_pages.shape or not (v_pages.stride() == ks or _equal(v_pages, k_pages)):
+    pages, Hkv, page_size, D2 = shape
+    if D2 != D or v_pages.shape != shape or not (v_pages.stride() == ks or _equal(v_pages, k_pages)):
         raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D] with equal strides")
-    if k_exp.dtype is not torch.uint8 or v_exp.dtype is not torch.uint8:
+    if ks[3] != 1:
+        _rows("k_pages", k_pages)
+    if k_exp.dtype is not _u8 or v_exp.dtype is not _u8:
         raise TypeError("k_exp, v_exp must be uint8")
-    if k_exp.dim() != 3 or k_exp.shape[:2] != (pages, Hkv) or v_exp.shape != k_exp.shape or not _equal(v_exp, k_exp):
+    eshape, es = k_exp.shape, k_exp.stride()
+    blocks = eshape[-1]
+    if eshape != (pages, Hkv, blocks) or v_exp.shape != eshape or not (v_exp.stride() == es or _equal(v_exp, k_exp)):
         raise ValueError("k_exp and v_exp must be [pages, Hkv, blocks] with equal strides")
-    es, blocks = _rows("k_exp", k_exp), k_exp.shape[2]
+    if es[2] != 1:
+        _rows("k_exp", k_exp)
     if blocks < 1 or page_size % blocks:
         raise ValueError(f"{blocks} blocks do not divide a page of {page_size} tokens")
     B, cols = page_table.shape
-    ts = _rows("page_table", page_table)
+    ts = page_table.stride()
+    if ts[1] != 1:
+        _rows("page_table", page_table)
     if page_table.dtype is not _s._i32:
         raise ValueError(f"page_table must be int32, got {page_table.dtype}")
-    _ints("q_start", q_start, B + 1)
-    _ints("kv_len", kv_len, B)
+    _vector("q_start", q_start, B + 1, _s._i32)
+    _vector("kv_len", kv_len, B, _s._i32)
     if B > _TOP or page_size > _TOP or pages > _TOP or cols > _TOP:
         raise ValueError("sizes past 32 bits")
     # the stride of a dimension of one element may be anything: D (or 1) stands in its place
@@ -272,11 +294,13 @@ def _cache8(k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_len, D):
 
 def _new_rows(k_new, v_new, T, Hkv, D):
     """Pointers and strides of the new rows."""
-    if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or not _equal(v_new, k_new):
+    shape, ns = k_new.shape, k_new.stride()
+    if shape != (T, Hkv, D) or v_new.shape != shape or not (v_new.stride() == ns or _equal(v_new, k_new)):
         raise ValueError("k_new, v_new must be [T, Hkv, D] with equal strides")
     if v_new.dtype is not k_new.dtype:
         raise TypeError("k_new and v_new must share a dtype")
-    ns = _rows("k_new", k_new)
+    if ns[2] != 1:
+        _rows("k_new", k_new)
     return k_new.data_ptr(), v_new.data_ptr(), ns[0] if T > 1 else D, ns[1] if Hkv > 1 else D
 
 
@@ -314,11 +338,11 @@ def spec_kv8_append(k_new, v_new, k_pages, v_pages, k_exp, v_exp, page_table, q_
 def paged_attn8_args(q, k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_len, o, *, max_q, k_new=None, v_new=None,
                      window: int = 0, scale: float = 0.0) -> SpecPaged8Args:
     """Fill SpecPaged8Args from tensors (no workspace yet)."""
-    _t()
-    T, Hq, D = q.shape
+    q_shape = q.shape
+    T, Hq, D = q_shape
     B, Hkv, page_size, pages, cols, block, layout = _cache8(k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_len, D)
     qs, os_ = _rows("q", q), _rows("o", o)
-    if o.shape != q.shape:
+    if o.shape != q_shape:
         raise ValueError("o must have q's shape")
     new = (None, None, 0, 0)
     if k_new is not None or v_new is not None:
@@ -327,12 +351,14 @@ def paged_attn8_args(q, k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_
         if k_new.dtype is not q.dtype:
             raise TypeError("k_new, v_new must have q's dtype")
         new = _new_rows(k_new, v_new, T, Hkv, D)
+    if T > _TOP:
+        raise ValueError("sizes past 32 bits")
     if max_q.__class__ is not int or not 0 <= max_q <= _TOP:
         max_q = _whole(max_q)
     if window.__class__ is not int or not 0 <= window <= _TOP:
         window = _whole(window)
     return SpecPaged8Args(
-        B, Hq, Hkv, D, _size(T), max_q, _dtype_code(q), _dtype_code(o), page_size, pages, cols, window, block,
+        B, Hq, Hkv, D, T, max_q, _dtype_code(q), _dtype_code(o), page_size, pages, cols, window, block,
         _scale(scale) if scale else 0.0, q.data_ptr(), qs[0] if T > 1 else D, qs[1] if Hq > 1 else D, *layout, *new,
         o.data_ptr(), os_[0], os_[1], None, 0)
 
@@ -363,55 +389,71 @@ def spec_paged_attn8(q, k_pages, v_pages, k_exp, v_exp, page_table, q_start, kv_
 def _page_arrays(caches, pages):
     """The caches [pages, ...] as the library takes them.  A page has to be one run of bytes, in any order of
     its dimensions."""
-    arrays = (SpecPageArray * max(len(caches), 1))()
-    for x, t in zip(arrays, caches):
-        shape, st = t.shape, t.stride()
-        if t.dim() < 1 or shape[0] != pages:
+    words = array("q")  # SpecPageArray is three of them
+    for t in caches:
+        shape = t.shape
+        if not shape or shape[0] != pages:
             raise ValueError(f"a cache must be [pages, ...] with {pages} pages, got {tuple(shape)}")
-        size = t.element_size()
-        run = 1
-        for s, n in sorted(zip(st[1:], shape[1:])):
-            if n != 1:
-                if s != run:
-                    raise ValueError("a page of a cache must be one run of memory (pass the buffer that holds its parts)")
-                run *= n
+        run = stride = t.nbytes // pages if pages else 0
         if run < 1:
             raise ValueError("a cache's pages are empty")
-        x.base, x.page_bytes = t.data_ptr(), run * size
-        x.stride_bytes = st[0] * size if pages > 1 else run * size
-    return arrays
+        if not t.is_contiguous():
+            st, n = t.stride(), 1
+            for s, m in sorted(zip(st[1:], shape[1:])):
+                if m != 1:
+                    if s != n:
+                        raise ValueError("a page of a cache must be one run of memory (pass the buffer that holds its parts)")
+                    n *= m
+            if pages > 1:
+                stride = st[0] * t.element_size()
+        words.extend((t.data_ptr(), stride, run))
+    return words
 
 
 def _table_out(page_table, out):
-    B, cols = page_table.shape
-    _rows("page_table", page_table)
-    out = page_table if out is None else out
-    _rows("table_out", out)
-    if page_table.dtype is not _s._i32 or out.dtype is not _s._i32 or out.shape != page_table.shape:
-        raise ValueError("page_table and table_out must be int32 of one shape")
-    return B, cols, out
+    shape = page_table.shape
+    B, cols = shape
+    if out is None:
+        out = page_table
+    elif out.shape != shape:
+        raise ValueError("page_table and table_out must have one shape")
+    if page_table.dtype is not _s._i32 or out.dtype is not _s._i32:
+        raise ValueError("page_table and table_out must be int32")
+    ts, os_ = _rows("page_table", page_table), _rows("table_out", out)
+    if B > _TOP or cols > _TOP:
+        raise ValueError("sizes past 32 bits")
+    return B, cols, out, ts[0] if B > 1 else cols, os_[0] if B > 1 else cols
+
+
+def _state(n, named):
+    """Checks int32 vectors of n elements, None among them for those not given."""
+    i32, shape = _s._i32, (n,)
+    for name, t in named:
+        if t is not None and (t.dtype is not i32 or t.shape != shape or not t.is_contiguous()):
+            _vector(name, t, n, i32)
 
 
 def page_fork_args(page_table, held, kv_len, refs, parent, *, page_size, grow=None, caches=(), table_out=None, held_out=None,
                    len_out=None, refs_out=None):
     """Fill SpecPageForkArgs from tensors (no workspace yet); the arrays live as long as what is returned."""
     _t()
-    B, cols, table_out = _table_out(page_table, table_out)
+    B, cols, table_out, ts, os_ = _table_out(page_table, table_out)
     pages = refs.shape[0]
-    held_out, len_out, refs_out = (a if b is None else b for a, b in ((held, held_out), (kv_len, len_out), (refs, refs_out)))
-    for name, t, n in (("held", held, B), ("kv_len", kv_len, B), ("parent", parent, B), ("held_out", held_out, B),
-                       ("len_out", len_out, B), ("refs", refs, pages), ("refs_out", refs_out, pages)):
-        _ints(name, t, n)
-    if grow is not None:
-        _ints("grow", grow, B)
-    if B > _TOP or cols > _TOP or pages > _TOP or len(caches) > _TOP:
+    if held_out is None:
+        held_out = held
+    if len_out is None:
+        len_out = kv_len
+    if refs_out is None:
+        refs_out = refs
+    _state(B, (("held", held), ("kv_len", kv_len), ("parent", parent), ("grow", grow), ("held_out", held_out), ("len_out", len_out)))
+    _state(pages, (("refs", refs), ("refs_out", refs_out)))
+    if pages > _TOP or len(caches) > _TOP:
         raise ValueError("sizes past 32 bits")
     arrays = _page_arrays(caches, pages)
     a = SpecPageForkArgs(
-        B, cols, _whole(page_size), pages, len(caches), 0, page_table.data_ptr(), page_table.stride(0) if B > 1 else cols,
-        held.data_ptr(), kv_len.data_ptr(), refs.data_ptr(), parent.data_ptr(), None if grow is None else grow.data_ptr(),
-        table_out.data_ptr(), table_out.stride(0) if B > 1 else cols, held_out.data_ptr(), len_out.data_ptr(),
-        refs_out.data_ptr(), ctypes.cast(arrays, c_void_p), None, 0)
+        B, cols, _whole(page_size), pages, len(caches), 0, page_table.data_ptr(), ts, held.data_ptr(), kv_len.data_ptr(),
+        refs.data_ptr(), parent.data_ptr(), None if grow is None else grow.data_ptr(), table_out.data_ptr(), os_,
+        held_out.data_ptr(), len_out.data_ptr(), refs_out.data_ptr(), arrays.buffer_info()[0] or None, None, 0)
     a.keep = arrays
     return a
 
@@ -433,33 +475,31 @@ def spec_page_fork(page_table, held, kv_len, refs, parent, *, page_size, grow=No
     written to table_out, held_out, len_out and refs_out; the new lengths include grow, as spec_paged_attn's
     do.  With bad data or too few free pages nothing is changed and the status word says why.  Returns
     (table, held, lengths, refs)."""
-    outs = [t for t in (grow, table_out, held_out, len_out, refs_out, *caches) if t is not None]
-    index = _check([page_table, held, kv_len, refs, parent, *outs])
+    index = _check((page_table, held, kv_len, refs, parent, grow, table_out, held_out, len_out, refs_out, *caches))
     a = page_fork_args(page_table, held, kv_len, refs, parent, page_size=page_size, grow=grow, caches=caches,
                        table_out=table_out, held_out=held_out, len_out=len_out, refs_out=refs_out)
     _run("spec_page_fork", a, (a.B, a.table_cols, a.page_size, a.num_pages, "fork"), index, workspace, stream)
-    return tuple(x if y is None else y for x, y in ((page_table, table_out), (held, held_out), (kv_len, len_out),
-                                                    (refs, refs_out)))
+    return (page_table if table_out is None else table_out, held if held_out is None else held_out,
+            kv_len if len_out is None else len_out, refs if refs_out is None else refs_out)
 
 
 def page_compact_args(page_table, held, refs, *, caches=(), table_out=None, refs_out=None, moved=None, num_live=None):
     """Fill SpecPageCompactArgs from tensors (no workspace yet); the arrays live as long as what is returned."""
     _t()
-    B, cols, table_out = _table_out(page_table, table_out)
+    B, cols, table_out, ts, os_ = _table_out(page_table, table_out)
     pages = refs.shape[0]
-    refs_out = refs if refs_out is None else refs_out
-    for name, t, n in (("held", held, B), ("refs", refs, pages), ("refs_out", refs_out, pages), ("moved", moved, pages),
-                       ("num_live", num_live, 1)):
-        if t is not None:
-            _ints(name, t, n)
-    if B > _TOP or cols > _TOP or pages > _TOP or len(caches) > _TOP:
+    if refs_out is None:
+        refs_out = refs
+    _state(B, (("held", held),))
+    _state(pages, (("refs", refs), ("refs_out", refs_out), ("moved", moved)))
+    _state(1, (("num_live", num_live),))
+    if pages > _TOP or len(caches) > _TOP:
         raise ValueError("sizes past 32 bits")
     arrays = _page_arrays(caches, pages)
     a = SpecPageCompactArgs(
-        B, cols, pages, len(caches), page_table.data_ptr(), page_table.stride(0) if B > 1 else cols, held.data_ptr(),
-        refs.data_ptr(), table_out.data_ptr(), table_out.stride(0) if B > 1 else cols, refs_out.data_ptr(),
-        None if moved is None else moved.data_ptr(), None if num_live is None else num_live.data_ptr(),
-        ctypes.cast(arrays, c_void_p), None, 0)
+        B, cols, pages, len(caches), page_table.data_ptr(), ts, held.data_ptr(), refs.data_ptr(), table_out.data_ptr(), os_,
+        refs_out.data_ptr(), None if moved is None else moved.data_ptr(), None if num_live is None else num_live.data_ptr(),
+        arrays.buffer_info()[0] or None, None, 0)
     a.keep = arrays
     return a
 
@@ -477,8 +517,7 @@ def spec_page_compact(page_table, held, refs, *, caches=(), table_out=None, refs
     page_table [B, cols], held [B], refs [pages] int32 as in spec_page_fork; caches: tensors [pages, ...].
     Changed in place, or written to table_out and refs_out.  moved [pages] gets each page's new id (-1: free),
     num_live [1] the number of pages in use; both optional.  Returns (table, refs)."""
-    outs = [t for t in (table_out, refs_out, moved, num_live, *caches) if t is not None]
-    index = _check([page_table, held, refs, *outs])
+    index = _check((page_table, held, refs, table_out, refs_out, moved, num_live, *caches))
     a = page_compact_args(page_table, held, refs, caches=caches, table_out=table_out, refs_out=refs_out, moved=moved,
                           num_live=num_live)
     _run("spec_page_compact", a, (a.B, a.table_cols, a.num_pages, "compact"), index, workspace, stream)

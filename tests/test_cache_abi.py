@@ -236,10 +236,11 @@ def test_page_arguments():
     ok = dict(page_table=i(2, 5), held=i(2), kv_len=i(2), refs=i(7), parent=i(2), page_size=16)
     both = z(7, 16, 2, 2, 64)  # K and V of a page side by side
     a = cache.page_fork_args(**ok, grow=i(2), caches=[both, z(7, 3, dtype=torch.uint8), z(7, 2, 16, 64).permute(0, 2, 1, 3)])
-    assert [(x.stride_bytes, x.page_bytes) for x in a.keep] == [(8192, 8192), (3, 3), (4096, 4096)]
+    assert [tuple(a.keep[3 * i + 1:3 * i + 3]) for i in range(3)] == [(8192, 8192), (3, 3), (4096, 4096)]
+    assert a.keep[0] == both.data_ptr() and ctypes.sizeof(cache.SpecPageArray) == 3 * a.keep.itemsize
     assert a.num_arrays == 3 and a.table_out == a.page_table and a.refs_out == a.refs and a.table_out_stride == 5
     a = cache.page_fork_args(**ok, caches=[z(14, 8)[::2]])
-    assert (a.keep[0].stride_bytes, a.keep[0].page_bytes, a.grow) == (32, 16, None)
+    assert (*a.keep[1:3], a.grow) == (32, 16, None)
     for bad in (dict(caches=[both[:, :, 0]]), dict(caches=[z(6, 4)]), dict(caches=[z(7, 0)]), dict(caches=[z(7, 4).expand(7, 4)[:, :1].expand(7, 4)]),
                 dict(held=i(3)), dict(refs=z(7)), dict(grow=i(1)), dict(table_out=i(2, 6)), dict(page_table=z(2, 5)),
                 dict(parent=z(2, dtype=torch.int64))):
