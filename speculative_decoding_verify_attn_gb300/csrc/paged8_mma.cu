@@ -12,7 +12,8 @@
 //   V: a transposed ldmatrix brings two neighbouring columns of two keys; one byte permutation pairs the keys,
 //   and columns 2 r, 2 r + 1 take the places r and r + 8 of the 16 rows of the product.
 //   A warp takes 32 keys of a unit at a time, two tiles side by side: twice the independent work per warp, and half
-//   the bookkeeping per key.
+//   the bookkeeping per key.  The query's fragments, the same for all warps, are read from shared memory: in
+//   registers they left too few (32 rows of 128: 304 us with them, 115 without).
 //   A block's K scale multiplies the tile's scores.  Its V scale 2^ev goes into the exponent of the
 //   probabilities, p' = 2^(s + ev - R), with R kept near the largest s + ev: p' then fits fp16 for whatever
 //   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev.
@@ -35,13 +36,18 @@ constexpr float kHeadroomLog2 = 7.0f;
 // The reference of a row that has seen no key: every score lies above it, and 2^(-inf - it) is 0.
 constexpr float kNoReference = -3.402823466e38f;
 
-constexpr int kMma8Keys = kMma8Unit / kMmaWarps;  // a warp's keys of a unit
-
-template <int D>
+template <int D, int NR>
 struct Mma8 {
+  // 8 sequences of 16K-32K: 8 and 12 warps 47 and 41 us for 4 rows of 64, 75 and 71 for 20; for rows of 128 the
+  // registers of 12 do not suffice beyond 16 rows, and up to there make no difference (71 us)
+  static constexpr int kWarps = D == 64 ? kMma8WideWarps : kMma8Warps;
+  using Cut = MmaCut<kWarps, kMma8Keys>;
   static constexpr int kStage = kMma8Keys * D * 2;      // a warp's K and V
-  static constexpr int kStages = D == 128 ? 3 : 5;
-  static constexpr size_t kSmem = (size_t)kMmaWarps * kStages * kStage + kMmaCmbBytes;
+  static constexpr int kStages = (D == 128 ? 24 : 40) / kWarps;
+  // the join buffer: a round's columns of 8 rows of every warp (strides without bank conflicts)
+  static constexpr int kCols = D == 64 ? 32 : 64;
+  static constexpr int kCmbStride = kCols + 4;
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + (size_t)kWarps * 8 * kCmbStride * 4;
   // Place of chunk c (16 bytes) of row r: eight rows' chunks c lie in eight different groups of banks.
   static __device__ __forceinline__ uint32_t at(int r, int c) {
     return r * D + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4);
@@ -49,18 +55,21 @@ struct Mma8 {
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
     paged8_mma(const __grid_constant__ Kv8Params p) {
   pdl_launch_dependents();
+  using M = Mma8<D, NR>;
+  using Cut = typename M::Cut;
+  constexpr int kWarps = M::kWarps;
   constexpr int KS = D / 16;          // k steps of K Q^T, m tiles of V^T P^T, 16-byte chunks of a row
   constexpr int RPI = 32 / KS;        // rows one cp.async instruction of the warp covers
-  constexpr int NS = Mma8<D>::kStages;
-  constexpr int STAGE = Mma8<D>::kStage;
-  constexpr int KT = 2;               // tiles of 16 keys at a time
+  constexpr int NS = M::kStages;
+  constexpr int STAGE = M::kStage;
+  constexpr int KT = kMma8Keys / 16;  // tiles of 16 keys, side by side
   extern __shared__ __align__(256) uint8_t smem[];
-  __shared__ int64_t s_scan[kMmaWarps];
-  __shared__ float2 s_ml[kMmaWarps][kMmaMaxRows];
-  __shared__ float2 s_scale[kMmaWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ float2 s_ml[kWarps][kMmaMaxRows];
+  __shared__ float2 s_scale[kWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent
   __shared__ uint2 s_q[NR][KS][32];  // the query's fragments
   __shared__ float s_undo[NR * 8];   // what a row's scores are multiplied by
   __shared__ int s_pos[NR * 8];      // its position
@@ -68,7 +77,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   __shared__ int64_t s_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  float* cmb = reinterpret_cast<float*>(smem + (size_t)kMmaWarps * NS * STAGE);
+  float* cmb = reinterpret_cast<float*>(smem + (size_t)kWarps * NS * STAGE);
   if (p.first && cta == 0 && tid == 0) status_clear_for_launch(p.status);
   // Behind an append only its own tokens, and the block that the first of them lies in, have to be waited for: the
   // earlier keys are on their way meanwhile.  `waited`: this warp has
@@ -86,7 +95,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
   };
 
-  MmaWalk<kMma8Unit> ld;
+  MmaWalk<Cut> ld;
   if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) {
     wait();  // what follows in the stream is ordered behind this grid alone
     return;
@@ -96,9 +105,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const uint32_t ring_u32 = smem_u32(smem + (size_t)warp * NS * STAGE);
   const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k);
   const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v);
-  MmaWalk<kMma8Unit> cw = ld;  // the unit in compute
-  auto first_key = [&](const MmaWalk<kMma8Unit>& w) {
-    return mma_first<kMma8Unit>(w.s) + w.u * kMma8Unit + warp * kMma8Keys;
+  MmaWalk<Cut> cw = ld;  // the unit in compute
+  auto first_key = [&](const MmaWalk<Cut>& w) {
+    return mma_first<Cut>(w.s) + w.u * Cut::UNIT + warp * kMma8Keys;
   };
   int page = -1;
   auto look_up = [&]() {
@@ -108,7 +117,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       page = __ldg(p.table + (int64_t)ld.b * p.table_stride + page_of(p, t));
   };
   const int c = lane % KS, rl = lane / KS;
-  const uint32_t lane_at = Mma8<D>::at(rl, c);
+  const uint32_t lane_at = M::at(rl, c);
   const bool whole_pages = (p.page_size & (kMma8Keys - 1)) == 0;
   uint8_t k_byte = 127, v_byte = 127;  // of this lane's key of the unit issued last; they reach s_scale one unit later
   bool seen = false;                   // whether that key lies in [lo, len)
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       fresh_part = false;
       part_u0 = cw.u;
       // the query's fragments, the same for all warps: each makes some of the tiles of 8 rows
-      for (int nr = warp; nr < NR; nr += kMmaWarps) {
+      for (int nr = warp; nr < NR; nr += kWarps) {
         const int r = nr * 8 + gid;
         const bool real = r < rows;
         // four neighbouring values of each step of 16, as K's rows come
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       uint32_t w[KT][4];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-        ldmatrix_x4(ks_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
+        ldmatrix_x4(ks_u32 + kt * 16 * D + M::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint2 q[NR];
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       uint32_t w[KT][4];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-        ldmatrix_x4_trans(vs_u32 + kt * 16 * D + Mma8<D>::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
+        ldmatrix_x4_trans(vs_u32 + kt * 16 * D + M::at(frag_row, ks + frag_chunk), w[kt][0], w[kt][1], w[kt][2], w[kt][3]);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -394,60 +403,52 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = nr * 8 + tq * 2 + h;
-          float M = neg_inf();
+          float top = neg_inf();
 #pragma unroll
-          for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
-          f[h] = ex2_approx(m_run[nr][h] - M);
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
+          f[h] = ex2_approx(m_run[nr][h] - top);
         }
-        // the warps' columns of 8 rows x 64 columns through shared memory; then a warp per row adds
-        // them up, two columns per lane
-        const int r = nr * 8 + warp, col = lane * 2;
-        float M = neg_inf(), L = 0.f;
+        // the warps' columns of 8 rows through shared memory; then a warp per row adds them up
+        constexpr int E = M::kCols / 32;
+        const int r = nr * 8 + (warp & 7), col = lane * E;
+        float top = neg_inf(), L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           const float2 v = s_ml[w][r];
-          L += ex2_approx(v.x - M) * v.y;
+          L += ex2_approx(v.x - top) * v.y;
         }
         const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-        if (!whole && r < rows && lane == 0) p.part_ml[rec * kMmaMaxRows + r] = make_float2(M == kNoReference ? neg_inf() : M, L);
+        if (!whole && r < rows && warp < 8 && lane == 0)
+          p.part_ml[rec * kMmaMaxRows + r] = make_float2(top == kNoReference ? neg_inf() : top, L);
 #pragma unroll
-        for (int c4 = 0; c4 < D / 64; ++c4) {
+        for (int c0 = 0; c0 < D; c0 += M::kCols) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float* dst = cmb + (warp * 8 + tq * 2) * kMmaCmbStride + x * 16 + gid * 2;
-            const float* v = o[nr][c4 * 4 + x];
+          for (int x = 0; x < M::kCols / 16; ++x) {
+            float* dst = cmb + (warp * 8 + tq * 2) * M::kCmbStride + x * 16 + gid * 2;
+            const float* v = o[nr][c0 / 16 + x];
             *reinterpret_cast<float2*>(dst) = make_float2(v[0] * f[0], v[2] * f[0]);
-            *reinterpret_cast<float2*>(dst + kMmaCmbStride) = make_float2(v[1] * f[1], v[3] * f[1]);
+            *reinterpret_cast<float2*>(dst + M::kCmbStride) = make_float2(v[1] * f[1], v[3] * f[1]);
           }
           __syncthreads();
-          float2 sum = make_float2(0.f, 0.f);
+          if (r < rows && warp < 8) {
+            float sum[E];
 #pragma unroll
-          for (int w = 0; w < kMmaWarps; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(cmb + (w * 8 + warp) * kMmaCmbStride + col);
-            sum.x += v.x;
-            sum.y += v.y;
-          }
-          if (r < rows) {
-            if (whole) {
-              const int64_t off = o_offset(p, cw.s, cw.g, r) + c4 * 64 + col;
-              if (p.o_bf16) {
-                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + off;
-                const uint32_t v = pack_bf16(sum.x * inv, sum.y * inv);
-                if ((reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
-                  *reinterpret_cast<uint32_t*>(dst) = v;
-                } else {
-                  reinterpret_cast<uint16_t*>(dst)[0] = (uint16_t)v;
-                  reinterpret_cast<uint16_t*>(dst)[1] = (uint16_t)(v >> 16);
-                }
-              } else {
-                float* dst = reinterpret_cast<float*>(p.o) + off;
-                dst[0] = sum.x * inv;
-                dst[1] = sum.y * inv;
+            for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+              for (int e = 0; e < E; ++e) sum[e] += cmb[(w * 8 + warp) * M::kCmbStride + col + e];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if (!whole) {
+                p.part_o[(rec * kMmaMaxRows + r) * D + c0 + col + e] = sum[e];
+                continue;
               }
-            } else {
-              *reinterpret_cast<float2*>(p.part_o + (rec * kMmaMaxRows + r) * D + c4 * 64 + col) = sum;
+              const int64_t off = o_offset(p, cw.s, cw.g, r) + c0 + col + e;
+              if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(sum[e] * inv);
+              else reinterpret_cast<float*>(p.o)[off] = sum[e] * inv;
             }
           }
           __syncthreads();
@@ -464,17 +465,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
 template <int D, int NR>
 static cudaError_t launch_mma8(const Kv8Params& p, cudaStream_t stream) {
-  const size_t smem = Mma8<D>::kSmem;
+  using M = Mma8<D, NR>;
+  const size_t smem = M::kSmem;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(paged8_mma<D, NR>), (int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.direct ? p.B * p.Hkv : p.grid);
   if (p.first) {
-    paged8_mma<D, NR><<<grid, kMmaThreads, smem, stream>>>(p);
+    paged8_mma<D, NR><<<grid, M::Cut::THREADS, smem, stream>>>(p);
     e = cudaGetLastError();
   } else {
-    e = launch_dependent(paged8_mma<D, NR>, grid, dim3(kMmaThreads), smem, stream, 0u, p);
+    e = launch_dependent(paged8_mma<D, NR>, grid, dim3(M::Cut::THREADS), smem, stream, 0u, p);
   }
-  return e != cudaSuccess || p.direct ? e : launch_paged_mma_merge(p, kMma8Unit, stream);
+  return e != cudaSuccess || p.direct ? e : launch_paged8_merge(p, M::kWarps, stream);
 }
 
 template <int D>

@@ -31,7 +31,12 @@
 
 namespace specv {
 
+constexpr int kMmaWarps = 8;
+constexpr int kMmaThreads = kMmaWarps * 32;
+using MmaCut16 = MmaCut<kMmaWarps, kMmaUnit / kMmaWarps>;
 constexpr int kMmaStages = 3;
+constexpr int kMmaCmbStride = 68;  // floats per row of the 64-column join buffer (conflict-free)
+constexpr int kMmaCmbBytes = kMmaWarps * 8 * kMmaCmbStride * 4;
 constexpr float kMmaRescaleLog2 = 8.0f;
 
 __host__ __device__ constexpr int mma_stage_bytes(int D) { return 16 * D * 2 * 2; }  // a warp's K and V
@@ -57,7 +62,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   if (cta == 0 && tid == 0) status_clear_for_launch(p.status);
 
   // ---- this CTA's units
-  MmaWalk<kMmaUnit> ld;
+  MmaWalk<MmaCut16> ld;
   if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, [&](uint32_t bits) { status_report(p.status, bits); })) return;
 
   // ---- loads: the warp's 16 keys of the unit at `ld`, with their page ids fetched one unit ahead
@@ -67,7 +72,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
   const __nv_bfloat16* vb = reinterpret_cast<const __nv_bfloat16*>(p.v);
   const __nv_bfloat16* knew = reinterpret_cast<const __nv_bfloat16*>(p.k_new);
   const __nv_bfloat16* vnew = reinterpret_cast<const __nv_bfloat16*>(p.v_new);
-  MmaWalk<kMmaUnit> cw = ld;  // the unit in compute
+  MmaWalk<MmaCut16> cw = ld;  // the unit in compute
   int page = -1;
   auto look_up = [&]() {  // page id of this lane's key (lanes 16-31 repeat lanes 0-15)
     const int t = (ld.s.lo & ~15) + ld.u * kMmaUnit + warp * 16 + (lane & 15);
@@ -367,21 +372,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma(const __grid_constan
 // grid (segments, rows / 8), a warp per row; a batch of records' statistics and values are all in flight
 // at once.
 constexpr int kMmaMergeBatch = 4;
-template <int D, int UNIT>
+template <int D, typename CUT>
 __global__ void __launch_bounds__(kMmaThreads) paged_mma_merge(const __grid_constant__ ServeAttnParams p) {
   __shared__ int64_t s_scan[kMmaWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv, r = blockIdx.y * kMmaWarps + warp;
   int64_t before = 0, all = 0;
   for (int i = tid; i < p.B; i += kMmaThreads) {
-    const int u = mma_units<UNIT>(seq_info(p, i));
+    const int u = mma_units<CUT>(seq_info(p, i));
     all += u;
     if (i < b) before += u;
   }
-  const int64_t total = block_sum(all, s_scan) * p.Hkv;
-  before = block_sum(before, s_scan) * p.Hkv;
+  const int64_t total = block_sum<kMmaWarps>(all, s_scan) * p.Hkv;
+  before = block_sum<kMmaWarps>(before, s_scan) * p.Hkv;
   const SeqInfo s = seq_info(p, b);
-  const int nu = mma_units<UNIT>(s);
+  const int nu = mma_units<CUT>(s);
   const int64_t per = mma_per_cta(total, p.grid);
   const int64_t start = before + (int64_t)g * nu;
   const int64_t c0 = start / per;
@@ -445,14 +450,15 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p) {
   p->part_o = reinterpret_cast<float*>(b + 256 + 2 * (size_t)kServeMaxGrid * kMmaMaxRows * sizeof(float2));
 }
 
-template <int UNIT>
+template <typename CUT>
 static cudaError_t launch_merge(const ServeAttnParams& p, cudaStream_t stream) {
   const dim3 grid(p.B * p.Hkv, (unsigned)(p.max_q * p.G + kMmaWarps - 1) / kMmaWarps);
-  if (p.D == 128) return launch_dependent(paged_mma_merge<128, UNIT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
-  return launch_dependent(paged_mma_merge<64, UNIT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+  if (p.D == 128) return launch_dependent(paged_mma_merge<128, CUT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
+  return launch_dependent(paged_mma_merge<64, CUT>, grid, dim3(kMmaThreads), 0, stream, 0u, p);
 }
-cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, int unit, cudaStream_t stream) {
-  return unit == kMmaUnit ? launch_merge<kMmaUnit>(p, stream) : launch_merge<kMma8Unit>(p, stream);
+cudaError_t launch_paged8_merge(const ServeAttnParams& p, int warps, cudaStream_t stream) {
+  if (warps == kMma8Warps) return launch_merge<MmaCut<kMma8Warps, kMma8Keys>>(p, stream);
+  return launch_merge<MmaCut<kMma8WideWarps, kMma8Keys>>(p, stream);
 }
 
 template <int D, int NR>
@@ -464,7 +470,7 @@ static cudaError_t launch_mma(const ServeAttnParams& p, cudaStream_t stream) {
   kern<<<p.direct ? p.B * p.Hkv : p.grid, kMmaThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.direct) return e;
-  return launch_merge<kMmaUnit>(p, stream);
+  return launch_merge<MmaCut16>(p, stream);
 }
 
 template <int D>

@@ -31,6 +31,7 @@ constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 constexpr int kPageCluster = 8;
 constexpr int kPageCols = 128;  // entries of a row that a warp takes at a time
+constexpr int kPageRows = 4;    // rows of a thread: 4096 at most over a CTA
 
 // What all passes know of their place.
 struct PageGrid {
@@ -168,18 +169,26 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
 
   // ---- pass 2: every CTA goes through all rows; thread t takes rows t * per .. (so prefixes follow the rows)
   const int per = (p.B + kPageThreads - 1) / kPageThreads;
-  int fresh = 0, copies = 0;
-  for (int i = 0; i < per; ++i) {
+  int4 r0[kPageRows], r1[kPageRows];
+#pragma unroll
+  for (int i = 0; i < kPageRows; ++i) {
     const int b = tid * per + i;
-    if (b >= p.B) break;
-    const int4 r0 = __ldcg(reinterpret_cast<const int4*>(p.rows + b)), r1 = __ldcg(reinterpret_cast<const int4*>(p.rows + b) + 1);
-    int copy = 0;
-    if (r1.y) {
-      const int holders = __ldcg(p.count + r1.x);
-      copy = holders > 1 && !(__ldcg(p.writers + r1.x) == holders && __ldcg(p.lowest + r1.x) == b);
+    const int4* row = reinterpret_cast<const int4*>(p.rows + b);
+    const bool in = i < per && b < p.B;
+    r0[i] = in ? __ldcg(row) : make_int4(0, 0, 0, 0);
+    r1[i] = in ? __ldcg(row + 1) : make_int4(0, 0, 0, 0);
+  }
+  int fresh = 0, copies = 0;
+  bool copy[kPageRows];
+#pragma unroll
+  for (int i = 0; i < kPageRows; ++i) {
+    copy[i] = false;
+    if (r1[i].y) {
+      const int holders = __ldcg(p.count + r1[i].x), writers = __ldcg(p.writers + r1[i].x), lowest = __ldcg(p.lowest + r1[i].x);
+      copy[i] = holders > 1 && !(writers == holders && lowest == tid * per + i);
     }
-    fresh += copy + r0.w - r0.z;
-    copies += copy;
+    fresh += (int)copy[i] + r0[i].w - r0[i].z;
+    copies += copy[i];
   }
   int need_all, copies_all;
   const int fresh0 = block_prefix(fresh, s_sum, need_all);
@@ -226,21 +235,16 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
   // what a row needs, where its pages begin in the list of free ones, and its place among the copies; by one CTA
   if (at.rank == 0) {
     int f = fresh0, c = copy0;
-    for (int i = 0; i < per; ++i) {
+#pragma unroll
+    for (int i = 0; i < kPageRows; ++i) {
       const int b = tid * per + i;
-      if (b >= p.B) break;
+      if (i >= per || b >= p.B) continue;
       int4* row = reinterpret_cast<int4*>(p.rows + b);
-      const int4 r0 = __ldcg(row), r1 = __ldcg(row + 1);
-      int copy = 0;
-      if (r1.y) {
-        const int holders = __ldcg(p.count + r1.x);
-        copy = holders > 1 && !(__ldcg(p.writers + r1.x) == holders && __ldcg(p.lowest + r1.x) == b);
-      }
       // parent, kept, need, first new page; page copied or -1, place of the copy, new length
-      row[0] = make_int4(r0.x, r0.z, r0.w, f);
-      row[1] = make_int4(copy ? r1.x : -1, c, r1.z, 0);
-      f += copy + r0.w - r0.z;
-      c += copy;
+      row[0] = make_int4(r0[i].x, r0[i].z, r0[i].w, f);
+      row[1] = make_int4(copy[i] ? r1[i].x : -1, c, r1[i].z, 0);
+      f += (int)copy[i] + r0[i].w - r0[i].z;
+      c += copy[i];
     }
   }
   cl.sync();

@@ -15,7 +15,10 @@ constexpr int kServeMaxGrid = 160;
 // runs.
 constexpr int kMmaMaxRows = 32;
 constexpr int kMmaUnit = 128;   // keys per unit of work of the mma.sync kernel (16 per warp)
-constexpr int kMma8Unit = 256;  // the same over 8-bit caches (32 per warp)
+// The same over 8-bit caches: keys of a unit that a warp takes, warps of a CTA for rows of 128 and of 64.
+constexpr int kMma8Keys = 32;
+constexpr int kMma8Warps = 8;
+constexpr int kMma8WideWarps = 12;
 // Segments of at most this many keys are one CTA of the mma.sync kernel each (no merge launch).  Device
 // time with and without: 8 segments of 128 keys 5.2 and 6.9 us, 256 segments of 512 keys 15.4 and 17.5;
 // past it 8 segments of 1024 keys take 11.3 and 8.4.
@@ -106,8 +109,8 @@ void mma_workspace_carve(void* ws, ServeAttnParams* p);
 void chunk_workspace_carve(void* ws, ServeAttnParams* p);
 
 cudaError_t launch_paged_mma(const ServeAttnParams& p, cudaStream_t stream);
-// joins the records of segments that several CTAs share, cut in units of `unit` keys (kMmaUnit or kMma8Unit)
-cudaError_t launch_paged_mma_merge(const ServeAttnParams& p, int unit, cudaStream_t stream);
+// joins the records of segments over 8-bit caches that several CTAs of `warps` warps share
+cudaError_t launch_paged8_merge(const ServeAttnParams& p, int warps, cudaStream_t stream);
 // plan and append, attention, merge
 cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ServeAttnParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
