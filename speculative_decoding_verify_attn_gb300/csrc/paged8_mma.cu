@@ -58,6 +58,7 @@ template <int D, int NR>
 __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
     paged8_mma(const __grid_constant__ Kv8Params p) {
   pdl_launch_dependents();
+  if (!p.first) pdl_wait();  // the append
   using M = Mma8<D, NR>;
   using Cut = typename M::Cut;
   constexpr int kWarps = M::kWarps;
@@ -79,27 +80,13 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
   const int cta = blockIdx.x;
   float* cmb = reinterpret_cast<float*>(smem + (size_t)kWarps * NS * STAGE);
   if (p.first && cta == 0 && tid == 0) status_clear_for_launch(p.status);
-  // Behind an append only its own tokens, and the block that the first of them lies in, have to be waited for: the
-  // earlier keys are on their way meanwhile.  `waited`: this warp has
-  bool waited = p.first;
-  auto wait = [&]() {
-    if (!waited) pdl_wait();
-    waited = true;
-  };
   auto report = [&](uint32_t bits) {
-    if (p.first) {
-      status_report(p.status, bits);
-    } else {
-      pdl_wait();  // the append clears the status
-      atomicOr(p.status, bits);
-    }
+    if (p.first) status_report(p.status, bits);
+    else atomicOr(p.status, bits);
   };
 
   MmaWalk<Cut> ld;
-  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) {
-    wait();  // what follows in the stream is ordered behind this grid alone
-    return;
-  }
+  if (!mma_start<D>(p, ld, s_scan, s_b, s_cum, report)) return;
 
   // ---- loads: the warp's 32 keys of the unit at `ld`, a lane each for page ids (fetched one unit ahead) and scales
   const uint32_t ring_u32 = smem_u32(smem + (size_t)warp * NS * STAGE);
@@ -130,7 +117,6 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
     if (ld.left > 0) {
       const int t0 = first_key(ld), t = t0 + lane;
       const uint32_t dst = ring_u32 + stage * STAGE + lane_at;
-      if (!waited && t0 + kMma8Keys > (ld.s.len - ld.s.n) / p.block * p.block) wait();
       const bool in = t >= ld.s.lo && t < ld.s.len;
       const bool good = in && page >= 0 && page < p.num_pages;
       const int slot = t - page_of(p, t) * p.page_size;
@@ -460,7 +446,6 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
     cw.step(p);
   }
   cp_async_wait<0>();
-  wait();
 }
 
 template <int D, int NR>

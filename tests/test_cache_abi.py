@@ -270,9 +270,8 @@ def test_host_tensors_are_refused():
 
 
 def test_dependent_grids_wait_before_they_leave():
-    """As test_dependent_launches.py, for kernels that may wait late: every way out of one that can be launched as a
-    dependent, a return or its end, has a wait right before it."""
-    import re
+    """As test_dependent_launches.py, for kernels that may also be a call's first: what comes before the wait is
+    nothing that could leave; the append, which needs nothing of the kernel before it, waits where it ends."""
     from .test_dependent_launches import kernels, source
     seen = set()
     for name in ("kv8_append.cu", "paged8_mma.cu", "chunk8_tc.cu", "pages.cu"):
@@ -280,11 +279,9 @@ def test_dependent_grids_wait_before_they_leave():
             if kernel in ("page_fork", "page_compact"):  # never launched as dependents
                 continue
             seen.add(kernel)
-            before, wait, _ = body.partition("pdl_wait();")
-            if wait and "return" not in before and kernel not in ("kv8_append", "paged8_mma"):
+            if kernel == "kv8_append":
+                assert "return;" not in body and body.rstrip().endswith("pdl_wait();")
                 continue
-            top = re.sub(r"\[&\][^;{]*\{(?:[^{}]|\{(?:[^{}]|\{[^{}]*\})*\})*\}", "", body)  # lambdas' own returns
-            for out in re.finditer(r"\breturn;", top):
-                assert re.search(r"wait\(\);\s*$", top[:out.start()]), kernel
-            assert re.search(r"wait\(\);\s*$", body), kernel
+            before, wait, _ = body.partition("pdl_wait();")
+            assert wait and "return" not in before, kernel
     assert seen == {"kv8_append", "paged8_mma", "chunk8_attn_tc", "page_copy"}

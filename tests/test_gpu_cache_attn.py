@@ -332,3 +332,44 @@ def test_a_serving_step_end_to_end(sv):
                     x[b] = x[a]
             assert np.array_equal(table.cpu().numpy(), t) and np.array_equal(refs.cpu().numpy(), r)
             assert all(np.array_equal(x, y) for x, y in zip(raw(), state))
+
+
+@pytest.mark.parametrize("q", [3, 50])
+def test_offsets_past_32_bits(sv, q):
+    """Pages that lie more than 2^32 bytes into their arrays: append, attention, a copy of a shared page, a move."""
+    torch = torch_mod()
+    Hkv, D, page, block, pages = 8, 128, 64, 32, 70000  # 4.6 GB each
+    if torch.cuda.mem_get_info()[0] < 12 * 2 ** 30:
+        pytest.skip("not enough memory")
+    kp, vp = (torch.empty(pages, Hkv, page, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ke, ve = (torch.full((pages, Hkv, page // block), 120, dtype=torch.uint8, device="cuda") for _ in range(2))
+    c = Attn([q], [150], G=4, Hkv=Hkv, D=D, page=page, block=block, append=True, seed=1, lead=0, trail=0)
+    c.table[:, :3] = [0, 1, 2]
+    ids = [pages - 1, pages - 2, pages - 5]
+    codes = np.full((3, Hkv, page, D), 0x38, np.uint8)
+    c.codes, c.exps = [codes.copy(), codes.copy()], [np.full((3, Hkv, 2), 120, np.uint8) for _ in range(2)]
+    rng = np.random.default_rng(0)
+    for x in c.codes:
+        x[:] = rng.integers(0, 0x60, x.shape)
+    c.pages = 3
+    for n, i in enumerate(ids):
+        kp.view(torch.uint8)[i], vp.view(torch.uint8)[i] = (torch.from_numpy(x[n]).cuda() for x in c.codes)
+    (ref, A, W, S), state = c.reference()
+    table, lens, refs = i32([ids + [0]]), i32([150]), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[ids] = 1
+    o = torch.empty(q, 4 * Hkv, D, dtype=torch.float32, device="cuda")
+    sv.spec_paged_attn8(c.q.cuda(), kp, vp, ke, ve, table, i32([0, q]), lens, o, max_q=q, k_new=c.new[0].cuda(), v_new=c.new[1].cuda())
+    check(np64(o), ref, A, W, S, D, 150, "f32")
+    got = lambda x, at: x.view(torch.uint8)[at].cpu().numpy()  # noqa: E731
+    for x, want in zip((kp, vp, ke, ve), state):
+        assert np.array_equal(got(x, ids), want)
+    # a second holder of the last page: the row's own copy is the lowest free page, then everything moves down
+    refs[ids[2]] = 2
+    held = i32([3])
+    sv.spec_page_fork(table, held, lens, refs, i32([0]), page_size=page, grow=i32([1]), caches=[kp, vp, ke, ve])
+    assert table[0, :3].tolist() == ids[:2] + [0] and np.array_equal(got(kp, 0), state[0][2])
+    moved = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    sv.spec_page_compact(table, held, refs, caches=[kp, vp, ke, ve], moved=moved)
+    assert table[0, :3].tolist() == [3, 2, 0] and moved[ids[2]] == 1
+    for x, want in zip((kp, vp, ke, ve), state):
+        assert np.array_equal(got(x, [3, 2, 0]), want[[0, 1, 2]])
