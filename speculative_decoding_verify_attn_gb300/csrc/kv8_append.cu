@@ -101,11 +101,13 @@ __device__ __forceinline__ int touched_blocks(const Kv8Params& p, const SeqInfo&
   return s.len > 0 ? (s.len - 1) / p.block - (s.len - s.n) / p.block + 1 : 0;
 }
 
-template <bool F32, int D>
+// HOLD: with the way that keeps rows in registers; without it the kernel is shorter and done sooner (a round of 8
+// sequences with their attention 108 us instead of 110.5).
+template <bool F32, int D, bool HOLD>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_constant__ Kv8Params p, int first) {
   pdl_launch_dependents();
   constexpr int LANES = D / 16, ROWS = 32 / LANES;  // lanes of a row, rows of an instruction
-  constexpr int HELD = F32 ? 4 : 8;                 // of a lane's rows that registers hold (64)
+  constexpr int HELD = HOLD ? (F32 ? 4 : 8) : 1;    // of a lane's rows that registers hold (64)
   extern __shared__ int s_pre[];  // [B + 1] blocks before each sequence
   __shared__ int s_sum[kAppendWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_consta
     uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? p.v : p.k) + (int64_t)page * p.kv_sp + (int64_t)g * p.kv_sh + c * 16;
     const int old = begin > t0 ? clamp_exp(*exp) : 0;
     const int rows = end - begin;
-    const bool held = rows <= HELD * ROWS;
+    const bool held = HOLD && rows <= HELD * ROWS;
     Raw16<F32> x[HELD];
     if (held) {
 #pragma unroll
@@ -242,24 +244,32 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append(const __grid_consta
   if (!first) pdl_wait();
 }
 
-template <bool F32, int D>
-static cudaError_t launch_append(const Kv8Params& p, bool first, cudaStream_t stream) {
+template <bool F32, int D, bool HOLD>
+static cudaError_t launch_append(const Kv8Params& p, bool first, int64_t units, cudaStream_t stream) {
   const int smem = (p.B + 1) * (int)sizeof(int);
-  // at most T / block + 2 per sequence with tokens
-  const int64_t blocks = p.T / p.block + 2 * (int64_t)(p.B < p.T ? p.B : p.T);
-  const int64_t want = (blocks * p.Hkv * 2 + kAppendWarps - 1) / kAppendWarps;
+  const int64_t want = (units + kAppendWarps - 1) / kAppendWarps;
   // one wave (registers leave four CTAs an SM): more CTAs work the sequences out anew, 27 us against 25 for 16K rows
   const unsigned grid = (unsigned)(want < 4 * p.grid ? want : 4 * p.grid);
   if (first) {
-    kv8_append<F32, D><<<grid, kAppendThreads, smem, stream>>>(p, 1);
+    kv8_append<F32, D, HOLD><<<grid, kAppendThreads, smem, stream>>>(p, 1);
     return cudaGetLastError();
   }
-  return launch_dependent(kv8_append<F32, D>, dim3(grid), dim3(kAppendThreads), smem, stream, 0u, p, 0);
+  return launch_dependent(kv8_append<F32, D, HOLD>, dim3(grid), dim3(kAppendThreads), smem, stream, 0u, p, 0);
+}
+
+// Few units (block, head, K or V) are a round's: their latency counts, not their bytes.
+constexpr int64_t kAppendFewUnits = 1024;
+template <bool F32, int D>
+static cudaError_t launch_append_d(const Kv8Params& p, bool first, cudaStream_t stream) {
+  // at most T / block blocks, and two per sequence with tokens
+  const int64_t units = (p.T / p.block + 2 * (int64_t)(p.B < p.T ? p.B : p.T)) * p.Hkv * 2;
+  return units <= kAppendFewUnits ? launch_append<F32, D, false>(p, first, units, stream)
+                                  : launch_append<F32, D, true>(p, first, units, stream);
 }
 
 cudaError_t launch_kv8_append(const Kv8Params& p, bool first, cudaStream_t stream) {
-  if (p.src_f32) return p.D == 128 ? launch_append<true, 128>(p, first, stream) : launch_append<true, 64>(p, first, stream);
-  return p.D == 128 ? launch_append<false, 128>(p, first, stream) : launch_append<false, 64>(p, first, stream);
+  if (p.src_f32) return p.D == 128 ? launch_append_d<true, 128>(p, first, stream) : launch_append_d<true, 64>(p, first, stream);
+  return p.D == 128 ? launch_append_d<false, 128>(p, first, stream) : launch_append_d<false, 64>(p, first, stream);
 }
 
 }  // namespace specv

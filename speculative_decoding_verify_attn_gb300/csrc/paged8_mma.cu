@@ -426,18 +426,27 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < E; ++e) sum[e] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-              for (int e = 0; e < E; ++e) sum[e] += cmb[(w * 8 + warp) * M::kCmbStride + col + e];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              if (!whole) {
-                p.part_o[(rec * kMmaMaxRows + r) * D + c0 + col + e] = sum[e];
-                continue;
+            for (int w = 0; w < kWarps; ++w) {
+              const float* src = cmb + (w * 8 + warp) * M::kCmbStride + col;
+              if constexpr (E == 2) {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                sum[0] += v.x;
+                sum[1] += v.y;
+              } else {
+                sum[0] += src[0];
               }
-              const int64_t off = o_offset(p, cw.s, cw.g, r) + c0 + col + e;
-              if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(sum[e] * inv);
-              else reinterpret_cast<float*>(p.o)[off] = sum[e] * inv;
+            }
+            if (!whole) {
+              float* dst = p.part_o + (rec * kMmaMaxRows + r) * D + c0 + col;
+              if constexpr (E == 2) *reinterpret_cast<float2*>(dst) = make_float2(sum[0], sum[1]);
+              else dst[0] = sum[0];
+            } else {
+              const int64_t off = o_offset(p, cw.s, cw.g, r) + c0 + col;
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[off + e] = __float2bfloat16_rn(sum[e] * inv);
+                else reinterpret_cast<float*>(p.o)[off + e] = sum[e] * inv;
+              }
             }
           }
           __syncthreads();
