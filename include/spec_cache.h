@@ -163,10 +163,11 @@ int spec_kv8_append(const spec_kv8_append_args* args, spec_stream_t stream);
  * Layout of the cache as spec_kv8_append.
  * Finiteness as there; besides, a row's largest |q| times scale is below 2^70.
  * Accumulation is fp32.  K, V and the queries enter the products in fp16, which holds e4m3 values and bf16
- *   queries (scaled row by row by a power of two; parts below 2^-29 of a row's largest lose bits) without
- *   rounding; probabilities are rounded to fp16.  In tiles of several blocks, chunks of more than 32 query
- *   rows also bring a block's scale to the largest of its 32 neighbours in fp16 (values 2^-15 below e4m3's
- *   range there lose bits).
+ *   queries without rounding: queries are scaled by a power of two, one for the rows of a sequence and kv head in
+ *   chunks of up to 32 query rows (tokens x heads of the group), one for each row in larger ones, and only parts
+ *   below 2^-29 of the largest lose bits.  Probabilities are rounded to fp16.  Larger chunks bring V and K of 32
+ *   neighbouring keys to the largest of their blocks' scales; values lose bits there if that is more than 2^15
+ *   above their own, and probabilities count as weights of values of that scale.
  * ---------------------------------------------------------------------------------------- */
 typedef struct spec_paged8_args {
   int32_t B, Hq, Hkv, D, T, max_q;

@@ -107,7 +107,8 @@ def stands_for(codes, exp):
 
 def paged_attn8(q, codes, exps, table, q_start, kv_len, window=0, scale=0.0):
     """o [T, Hq, D], with what the error bound is made of, per row and head: A = sum p |v|, W = (the largest p 2^ev) *
-    sum |v / 2^ev|; and the largest scale * sum |q k|."""
+    sum |v / 2^ev|, and the same with 2^ev replaced by the largest scale among 32 neighbouring keys, together; and the
+    largest scale * sum |q k|."""
     T, Hq, D = q.shape
     scale = scale or D ** -0.5
     size, Hkv = codes[0].shape[2], codes[0].shape[1]
@@ -125,6 +126,8 @@ def paged_attn8(q, codes, exps, table, q_start, kv_len, window=0, scale=0.0):
             ke, ve = (np.clip(x[page, g, slot // block].astype(np.int64), 63, 191) - 127.0 for x in exps)
             k, v8 = VALUES[codes[0][page, g, slot]] * 2.0 ** ke[:, None], VALUES[codes[1][page, g, slot]]
             v = v8 * 2.0 ** ve[:, None]
+            top = np.array([ve[t // 32 == i // 32].max() for i in t])  # of the keys that the chunk sees
+            near = np.abs(v8) * 2.0 ** (ve - top)[:, None]
             for j in range(n):
                 pos = length - n + j
                 seen = (t <= pos) & ((t > pos - window) if window > 0 else True)
@@ -133,7 +136,8 @@ def paged_attn8(q, codes, exps, table, q_start, kv_len, window=0, scale=0.0):
                     p = np.exp(s - s.max())
                     p /= p.sum()
                     o[r0 + j, h], A[r0 + j, h] = p @ v[seen], p @ np.abs(v[seen])
-                    W[r0 + j, h] = (p * 2.0 ** ve[seen]).max() * np.abs(v8[seen]).sum(0)
+                    W[r0 + j, h] = (p * 2.0 ** ve[seen]).max() * np.abs(v8[seen]).sum(0) + \
+                        (p * 2.0 ** top[seen]).max() * near[seen].sum(0)
                     S = max(S, float((np.abs(k[seen]) @ np.abs(q[r0 + j, h])).max()) * abs(scale))
     return o, A, W, S
 

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 #pragma unroll
         for (int x = 1; x < CH; x <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
         float undo;
-        const float up = f16_row_scale(amax, undo);
+        const float up = f16_scale(amax, undo);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[e] = pack_f16(__uint_as_float(v[e] << 16) * up, __uint_as_float(v[e] & 0xffff0000u) * up);

@@ -73,15 +73,15 @@ __device__ __forceinline__ void page_slot(const ServeAttnParams& p, int b, int t
   slot = t - col * p.page_size;
 }
 
-// A query row in fp16: scaled by the power of two that brings its largest value to [2^14, 2^15), so that
-// only parts 2^29 below that lose bits.  `inverse` undoes the scale.
-__device__ __forceinline__ float f16_row_scale(float amax, float& inverse) {
+// Queries in fp16: scaled by the power of two that brings the largest value to [2^14, 2^15), so that only parts
+// 2^29 below that lose bits.  `inverse` undoes the scale.
+__device__ __forceinline__ float f16_scale(float amax, float& inverse) {
   const int k = (int)(__float_as_uint(amax) >> 23) - 127;  // amax in [2^k, 2^(k + 1))
   const int up = amax > 0.f ? min(14 - k, 100) : 0;
   inverse = exp2_whole(-up);
   return exp2_whole(up);
 }
-// What the scores of such a row are multiplied by, kept where a block's 2^64 leaves it finite.
+// What the scores of such queries are multiplied by, kept where a block's 2^64 leaves it finite.
 __device__ __forceinline__ float q_factor(float inverse, float scale_log2) {
   return fminf(inverse * scale_log2, 4.611686018427388e18f);  // 2^62
 }

@@ -19,9 +19,11 @@
 //   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev.
 //   fp16 holds p' <= 2^15 and rounds to steps of 2^-24, so R is set 2^7 below the maximum: what a
 //   probability of the largest key's size loses is then below 2^-32 of it.
-//   Query rows are scaled to fp16 row by row by a power of two, undone on the scores.
+//   The query's rows are scaled into fp16 by one power of two, undone on the scores together with K's scale (a
+//   scale for each row: 20 rows 103 us instead of 98).  Parts below 2^-29 of the largest value lose bits, which
+//   moves a score by at most 2^-39 of what the largest query could reach.
 // Measured (8 sequences of 16K-32K, 32/8 heads of 128, the join included): 4 rows per kv head 65 us (83% of the copy
-// rate), 16 rows 71 us (75%), 20 rows 105 us (66%), 32 rows 115 us; past 16 rows two warps a scheduler leave
+// rate), 16 rows 71 us (75%), 20 rows 98 us (71%), 32 rows 110 us; past 16 rows two warps a scheduler leave
 // its fixed latencies open.  In rows of 64: 41 us for 4 rows (66%), 71 for 20.
 #include <cuda_runtime.h>
 
@@ -75,8 +77,8 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
   __shared__ float2 s_ml[kWarps][kMmaMaxRows];
   __shared__ float2 s_scale[kWarps][NS][kMma8Keys];  // of a stage's keys: K's scale, V's exponent
   __shared__ uint2 s_q[NR][KS][32];  // the query's fragments
-  __shared__ float s_undo[NR * 8];   // what a row's scores are multiplied by
-  __shared__ int s_pos[NR * 8];      // its position
+  __shared__ float s_amax[NR];       // the largest magnitude of 8 rows
+  __shared__ int s_pos[NR * 8];      // a row's position
   __shared__ int s_b;
   __shared__ int64_t s_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
   // places of the fragments' rows: K: matrices (keys 0-7, 8-15) x (chunk, chunk + 1); V alike
   const int frag_row = lane & 15, frag_chunk = lane >> 4;
   float o[NR][KS][4];  // columns d = ks * 16 + 2 gid (e < 2), + 1 (e >= 2) of rows nr * 8 + 2 tq + (e & 1)
-  float qs[NR][2];     // what the scores of those rows are multiplied by
+  float qs = 0.f;      // what the scores are multiplied by
   float m_run[NR][2], l_run[NR][2];  // the reference R, and the sum of 2^(s - R)
   int stage = 0;
   bool fresh_part = true;
@@ -180,14 +182,14 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
     if (__builtin_expect(fresh_part, 0)) {
       fresh_part = false;
       part_u0 = cw.u;
-      // the query's fragments, the same for all warps: each makes some of the tiles of 8 rows
-      for (int nr = warp; nr < NR; nr += kWarps) {
-        const int r = nr * 8 + gid;
-        const bool real = r < rows;
-        // four neighbouring values of each step of 16, as K's rows come
-        const uint2* src = reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                          (real ? q_offset(p, cw.s, cw.g, r) : 0));
-        uint2 raw[KS];
+      // the query's fragments, the same for all warps: warp w makes those of the w-th 8 rows, four neighbouring values
+      // of each step of 16, as K's rows come
+      const int r = warp * 8 + gid;
+      const bool real = warp < NR && r < rows;
+      const uint2* src = reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                        (real ? q_offset(p, cw.s, cw.g, r) : 0));
+      uint2 raw[KS];
+      if (warp < NR) {
         float amax = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -197,14 +199,17 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
           for (int i = 0; i < 2; ++i)
             amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float undo;
-        const float up = f16_row_scale(amax, undo);
-        if (tq == 0) {
-          s_undo[r] = q_factor(undo, p.scale_log2);
-          s_pos[r] = cw.s.len - cw.s.n + r / p.G;
-        }
+        amax = warp_max(amax);
+        if (lane == 0) s_amax[warp] = amax;
+      }
+      __syncthreads();  // the part before has ended with one, too
+      float amax = s_amax[0], undo;
+#pragma unroll
+      for (int nr = 1; nr < NR; ++nr) amax = fmaxf(amax, s_amax[nr]);
+      const float up = f16_scale(amax, undo);
+      qs = q_factor(undo, p.scale_log2);
+      if (warp < NR) {
+        if (tq == 0) s_pos[r] = cw.s.len - cw.s.n + r / p.G;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t w[2] = {raw[ks].x, raw[ks].y};
@@ -212,10 +217,10 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             f[i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-          s_q[nr][ks][lane] = make_uint2(f[0], f[1]);
+          s_q[warp][ks][lane] = make_uint2(f[0], f[1]);
         }
       }
-      __syncthreads();  // the part before has ended with one, too
+      __syncthreads();
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -224,7 +229,6 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
           for (int e = 0; e < 4; ++e) o[nr][ks][e] = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          qs[nr][h] = s_undo[nr * 8 + tq * 2 + h];
           m_run[nr][h] = kNoReference;
           l_run[nr][h] = 0.f;
         }
@@ -273,10 +277,11 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       const float2 a = s_scale[warp][stage][kt * 16 + gid], b = s_scale[warp][stage][kt * 16 + gid + 8];
+      const float ka = qs * a.x, kb = qs * b.x;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[kt][nr][e] = fmaf(s[kt][nr][e], qs[nr][e & 1] * (e < 2 ? a.x : b.x), e < 2 ? a.y : b.y);
+        for (int e = 0; e < 4; ++e) s[kt][nr][e] = fmaf(s[kt][nr][e], e < 2 ? ka : kb, e < 2 ? a.y : b.y);
     }
     // some row must not see some of these keys: past the first new token, or below the last row's window
     if (__builtin_expect(key0 + 16 * KT > first_new + 1 || (p.window > 0 && key0 < cw.s.len - p.window), 0)) {

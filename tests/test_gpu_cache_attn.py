@@ -5,9 +5,11 @@ before its rounding, the numerator's and the normaliser's shares are at most 2 r
 fp32 sum, off by at most (D + 8) 2^-24 S with S the largest scale * sum |q k| (absolutely: it sits in an exponent), the
 exponents up to 64 of V's scales are added to it in fp32 (2^-23 * 64, twice), and 2^-20 for 2^x and the
 running rescales.  Probabilities are rounded to fp16: 2^-11 A, and where they are below 2^-14 by half a step of 2^-24;
-as the largest p' is at least 2^7, that is 2^-32 W, with W = max(p 2^ev) * sum |v / 2^ev|.  The P.V and l sums over L
-keys add L 2^-24 A each; the output's own rounding comes last.  Keys whose scales lie within 2^5 of their
-neighbours' lose nothing in fp16.  Slots past kv_len and pages before the window hold NaN codes."""
+as the largest p' = c p 2^ev is at least 2^7, that moves the output by at most sum 2^-25 |v / 2^ev| / c <= 2^-32 W, with
+W = max(p 2^ev) * sum |v / 2^ev|.  In large chunks 32 neighbouring keys have one ev, the largest of theirs, and the
+values v / 2^ev that go with it; W holds both forms.  The P.V and l sums over L keys add L 2^-24 A each; the output's
+own rounding comes last.  Values brought to a neighbour's scale up to 2^14 above their own lose nothing in fp16
+(e4m3's are multiples of 2^-9, fp16's of 2^-24).  Slots past kv_len and pages before the window hold NaN codes."""
 
 import numpy as np
 import pytest
