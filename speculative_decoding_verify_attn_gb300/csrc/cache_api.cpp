@@ -327,6 +327,7 @@ int spec_paged_attn8(const spec_paged8_args* a, spec_stream_t stream) {
   p.min_units = 2;
   p.piece_cost = 3.f;
   p.cut_cost = 7.f;
+  p.share_piece = 3;
   specv::chunk_workspace_carve(a->workspace, &p);
   if (a->window > 0 && a->window < keys) keys = a->window;
   // a tile's rows see at most `keys` keys and those that its tokens lie apart

@@ -125,7 +125,10 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   longest = __reduce_max_sync(0xffffffffu, lane < kPlanWarps ? s_warp[lane] : 0u);
   const int64_t all = total * p.Hkv;
-  const int per = (int)max((int64_t)p.min_units, (all + p.grid - 1) / p.grid);
+  // Shares are equal with what a piece costs beside its units counted in, in units (0: units alone).  24 mixed
+  // sequences over an 8-bit cache, a piece counting 0, 2, 3, 4 and 5 units: 134.8, 132.1, 131.7, 131.6 and 134.4 us.
+  const int extra = p.share_piece;
+  const int per = (int)max((int64_t)p.min_units, (all + (int64_t)extra * tiles * p.Hkv + p.grid - 1) / p.grid);
   // cut only where an estimate says that it beats dealing whole tiles, in units with piece_cost for every
   // piece: whole tiles take the longest one, or as many average ones as waves; shares take the mean, a second cut
   // tile and the merge.  The dealing leaves its longest CTA somewhat above the estimate (24 mixed sequences:
@@ -150,7 +153,8 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     const bool big = n > 0 && is_big(n);
     if (n > 0 && !big) atomicAdd(&s_bin[bin_of(n)], 1);
     const unsigned mask = __ballot_sync(0xffffffffu, big);
-    int64_t x = big ? n : 0;
+    const int cost = n + extra;
+    int64_t x = big ? cost : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -173,7 +177,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     const int before = n_big + (int)__reduce_add_sync(0xffffffffu, lane < warp ? counts : 0u) + __popc(mask & ((1u << lane) - 1u));
     if (big && before < kMaxBig) {
       s_big[before] = t;
-      s_big_at[before] = big_units + pre_units + x - n;
+      s_big_at[before] = big_units + pre_units + x - cost;
     }
     n_big += (int)__reduce_add_sync(0xffffffffu, counts);
     big_units += sum_units;
@@ -213,6 +217,8 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     ctas = (int)min((int64_t)ctas, (line + p.min_units - 1) / p.min_units);
   }
   const int64_t share = ctas > 0 ? (line + ctas - 1) / ctas : 1;
+  // with extra costs the remainder is spread, too: shares of `share` and one less
+  const int64_t least = extra > 0 && ctas > 0 ? max((int64_t)1, line / ctas) : share;
   // ---- waves of whole tiles: item i (tile i / Hkv, head i % Hkv) to CTA i % ctas
   auto big_size = [&](int j) { return (int)(s_big_at[j + 1] - s_big_at[j]); };
   const int n_items = n_big * p.Hkv;
@@ -221,7 +227,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     int k = 0;
     for (int i = tid; i < n_items; i += ctas, ++k) {
       sum += big_size(i / p.Hkv);
-      if (sum >= share) break;
+      if (sum >= least) break;
     }
     atomicMin(&s_waves, k);
   }
@@ -230,7 +236,7 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
   // what each CTA lacks after them (at least a unit), and its place in the rest of the line
   int64_t lacks = 0;
   if (tid < ctas) {
-    lacks = share;
+    lacks = extra > 0 ? max((int64_t)1, (tid + 1) * line / ctas - tid * line / ctas) : share;
     for (int k = 0; k < waves; ++k) lacks -= big_size((k * ctas + tid) / p.Hkv);
   }
   if (tid < kServeMaxGrid) {  // whole warps
@@ -267,6 +273,18 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
     g = (int)((at - s_big_at[lo] * p.Hkv) / n);
     start = s_big_at[lo] * p.Hkv + (int64_t)g * n;
   };
+  if (extra > 0) {  // no cut in front of a tile's first unit
+    int64_t at = tid < ctas ? s_from[tid] : line;
+    if (at < line) {
+      int j, g, n;
+      int64_t start;
+      place(at, j, g, start, n);
+      if (at - start <= extra) at = start;
+    }
+    __syncthreads();
+    if (tid < ctas) s_from[tid] = at;
+    __syncthreads();
+  }
   auto write_item = [&](ChunkItem* item, const PlanTile& r, int u0, int u1, int slot, int g) {
     const int n = s_n[r.b], len = s_len[r.b];
     int4* dst = reinterpret_cast<int4*>(item);
@@ -281,7 +299,8 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
       const PlanTile r = tile_of(s_big[i / p.Hkv]);
       write_item(p.big + tid * kBigPieces + k, r, r.u0, r.u1, -1, i % p.Hkv);
     }
-    const int64_t begin = s_from[tid], end = min(line, begin + lacks);
+    const int64_t begin = s_from[tid];
+    const int64_t end = min(line, extra == 0 ? begin + lacks : tid + 1 < ctas ? s_from[tid + 1] : line);
     int64_t at = begin;
     while (at < end && k < kBigPieces) {
       int j, g, n;
@@ -289,8 +308,9 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
       place(at, j, g, start, n);
       const PlanTile r = tile_of(s_big[j]);
       const int64_t stop = min(end, start + n);
+      const int from = at == start ? 0 : (int)(at - start) - extra;
       const bool whole = at == start && stop == start + n;
-      write_item(p.big + tid * kBigPieces + k, r, r.u0 + (int)(at - start), r.u0 + (int)(stop - start),
+      write_item(p.big + tid * kBigPieces + k, r, r.u0 + from, r.u0 + (int)(stop - start) - extra,
                  whole ? -1 : 2 * tid + (at == begin ? 0 : 1), g);
       // the tile's first cut lies at the end of this share: it is joined from here on
       if (!whole && at == start) {
@@ -366,6 +386,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_const
 // Merge of cut tiles: a unit of work is (cut tile of a kv head, block of 128 rows, 8 columns),
 // thread m a row; records are column-major, so a warp's loads of one column are one line.  The pieces'
 // weights 2^(m_i - M) are worked out once per row and unit; loads go out several pieces at a time.
+// A unit is a chain of four trips to memory, so eight CTAs an SM take them (24 mixed sequences over an 8-bit cache 134.6
+// us, with four 138.3, with sixteen 134.5).
 // Also zeros the rows of sequences with a bad kv_len.
 constexpr int kChunkMergeCols = 8;
 constexpr int kMergeThreads = 128;
@@ -496,7 +518,7 @@ cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaS
   return cudaGetLastError();
 }
 cudaError_t launch_chunk_merge(const ServeAttnParams& p, cudaStream_t stream) {
-  return launch_dependent(chunk_merge, dim3(4 * p.grid), dim3(kMergeThreads), 0, stream, 0u, p);
+  return launch_dependent(chunk_merge, dim3(8 * p.grid), dim3(kMergeThreads), 0, stream, 0u, p);
 }
 
 }  // namespace specv

@@ -86,6 +86,7 @@ struct ServeAttnParams {
   // chunk kernels: what a piece costs beside its units (its rows, its first maximum, its epilogue), and
   // what cutting costs a CTA (a second cut tile's piece, the merge), in units
   float piece_cost, cut_cost;
+  int share_piece;        // chunk kernels: what a piece counts in the shares of cut tiles beside its units, in units
   int min_units;          // chunk kernels: units a CTA's share of cut tiles has at least
   int use_tma;            // tcgen05 kernel: the tensor maps are valid
   int tma_page_keys;      // keys one copy brings (min(page_size, kTcKeys); packed: kTcKeys)
