@@ -54,6 +54,7 @@ enum {
  *   several sequences belongs to the first of them.
  * Layout: q, q_out [T, Hq, D]; k, k_out [T, Hkv, D]; either may be missing (NULL with 0 heads).  An output
  *   that is its input (same pointer, same strides) is turned in place; otherwise none overlaps an input.
+ *   Rows of an output do not overlap each other, so broadcast rows are not turned in place.
  * Types: dtype SPEC_BF16 or SPEC_F32 for all of them.  Strides are multiples of 16 bytes, pointers
  *   16-byte aligned (steps: 8).  The arithmetic is fp32, rounded once.
  * Limits: rows of 16 to 2048 bytes, a multiple of 16; rot even, 2 <= rot <= D; Hq, Hkv <= 4096;
@@ -122,7 +123,8 @@ int spec_rotary_steps(int32_t rot, int32_t kind, double base, double factor, dou
  *
  * Layout: k_new, v_new [T, Hkv, D] (equal strides), src_dtype SPEC_BF16 or SPEC_F32; k_pages, v_pages with any
  *   strides for page, head and token, equal for both (kv_stride_*; multiples of 16, pointers 16-byte
- *   aligned); k_exp, v_exp with any strides for page and head, equal for both, a head's blocks contiguous.
+ *   aligned); k_exp, v_exp with any strides for page and head, equal for both, a head's blocks contiguous.  K and V, pages, heads and tokens
+ *   do not overlap each other.
  * Limits as spec_paged_attn; block >= 1 divides page_size.
  * Data errors as spec_paged_attn: bad sequences (SPEC_STATUS_BAD_RANGE, SPEC_STATUS_BAD_KV_LEN) and
  *   blocks of a page id out of range (SPEC_STATUS_BAD_PAGE) are not written.

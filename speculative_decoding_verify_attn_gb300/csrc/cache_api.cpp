@@ -76,6 +76,15 @@ bool cache8_layout(const Args* a) {
          a->k_exp && a->v_exp && a->exp_stride_p >= 0 && a->exp_stride_h >= 0 && int_layout(a->page_table) &&
          int_layout(a->q_start) && int_layout(a->kv_len);
 }
+// what the append writes does not overlap, as far as single strides say
+template <typename Args>
+bool cache8_writable(const Args* a) {
+  auto apart = [](int n, int64_t stride, int row) { return n == 1 || stride >= row; };
+  const int blocks = a->page_size / a->block;
+  return a->k_pages != a->v_pages && a->k_exp != a->v_exp && apart(a->num_pages, a->kv_stride_p, a->D) &&
+         apart(a->Hkv, a->kv_stride_h, a->D) && apart(a->page_size, a->kv_stride_t, a->D) &&
+         apart(a->num_pages, a->exp_stride_p, blocks) && apart(a->Hkv, a->exp_stride_h, blocks);
+}
 template <typename Args>
 Kv8Params cache8_params(const Args* a, int max_q) {
   Kv8Params p;
@@ -191,6 +200,11 @@ int spec_rotary(const spec_rotary_args* a, spec_stream_t stream) {
     return SPEC_ERR_INVALID_ARG;
   if (a->Hkv > 0 && k_in && ((a->T > 1 && a->k_stride_t != a->ko_stride_t) || (a->Hkv > 1 && a->k_stride_h != a->ko_stride_h)))
     return SPEC_ERR_INVALID_ARG;
+  // rows of an output do not overlap, as far as single strides say, and q and k have an output each
+  if ((a->T > 1 && ((a->Hq > 0 && a->qo_stride_t < a->D) || (a->Hkv > 0 && a->ko_stride_t < a->D))) ||
+      (a->Hq > 1 && a->qo_stride_h < a->D) || (a->Hkv > 1 && a->ko_stride_h < a->D))
+    return SPEC_ERR_INVALID_ARG;
+  if (a->Hq > 0 && a->Hkv > 0 && (a->q_out == a->k_out || a->q_out == a->k || a->k_out == a->q)) return SPEC_ERR_INVALID_ARG;
   if (!a->steps || !aligned(a->steps, 8)) return SPEC_ERR_INVALID_ARG;
   if (a->positions ? !aligned(a->positions, 4) : !int_layout(a->q_start) || !int_layout(a->kv_len)) return SPEC_ERR_INVALID_ARG;
   if ((st = check_workspace(a->workspace, a->workspace_bytes, kStatusBytes)) != SPEC_OK) return st;
@@ -275,7 +289,8 @@ int spec_kv8_append(const spec_kv8_append_args* a, spec_stream_t stream) {
   if (st != SPEC_OK || (st = check_pages8(append_shape(a), a->table_stride)) != SPEC_OK) return st;
   if (a->T == 0) return SPEC_OK;
   const int elem = a->src_dtype == SPEC_F32 ? 4 : 2;
-  if (!cache8_layout(a) || !vector_layout(a->k_new, elem, a->new_stride_t, a->new_stride_h) || !vector_layout(a->v_new, elem, 0, 0))
+  if (!cache8_layout(a) || !cache8_writable(a) || !vector_layout(a->k_new, elem, a->new_stride_t, a->new_stride_h) ||
+      !vector_layout(a->v_new, elem, 0, 0))
     return SPEC_ERR_INVALID_ARG;
   if ((st = check_workspace(a->workspace, a->workspace_bytes, kStatusBytes)) != SPEC_OK) return st;
   Kv8Params p = cache8_params(a, append_shape(a).max_q);
@@ -301,7 +316,7 @@ int spec_paged_attn8(const spec_paged8_args* a, spec_stream_t stream) {
   if (!cache8_layout(a) || !vector_layout(a->q, 2, a->q_stride_t, a->q_stride_h) || !a->o || a->o_stride_t < 0 ||
       a->o_stride_h < 0 || !aligned(a->o, a->o_dtype == SPEC_F32 ? 4 : 2))
     return SPEC_ERR_INVALID_ARG;
-  if (a->k_new && (!vector_layout(a->k_new, 2, a->new_stride_t, a->new_stride_h) || !vector_layout(a->v_new, 2, 0, 0)))
+  if (a->k_new && (!cache8_writable(a) || !vector_layout(a->k_new, 2, a->new_stride_t, a->new_stride_h) || !vector_layout(a->v_new, 2, 0, 0)))
     return SPEC_ERR_INVALID_ARG;
   if ((st = check_workspace(a->workspace, a->workspace_bytes, spec_paged_attn8_workspace(a))) != SPEC_OK) return st;
 

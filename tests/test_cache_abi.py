@@ -29,7 +29,7 @@ def rotary(**kw):
 
 def cache8(**kw):
     d = dict(B=2, Hkv=2, D=128, T=10, page_size=16, num_pages=64, table_cols=20, block=8, k_new=FAKE, v_new=FAKE,
-             new_stride_t=256, new_stride_h=128, k_pages=FAKE, v_pages=FAKE, kv_stride_p=4096, kv_stride_h=2048,
+             new_stride_t=256, new_stride_h=128, k_pages=FAKE, v_pages=FAKE + (1 << 20), kv_stride_p=4096, kv_stride_h=2048,
              kv_stride_t=128, k_exp=FAKE + 1, v_exp=FAKE + 3, exp_stride_p=4, exp_stride_h=2, page_table=FAKE,
              table_stride=20, q_start=FAKE, kv_len=FAKE, workspace=FAKE, workspace_bytes=1 << 40)
     d.update(kw)
@@ -95,6 +95,23 @@ def test_struct_sizes(L):
 ])
 def test_rotary_refusals(L, kw, status):
     assert L.spec_rotary(ctypes.byref(rotary(**kw)), None) == status
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=FAKE, q_stride_t=0, qo_stride_t=0), dict(qo_stride_t=64), dict(qo_stride_h=0), dict(ko_stride_t=0),
+    dict(ko_stride_h=120), dict(q_out=FAKE + 256, k_out=FAKE + 256), dict(q_out=FAKE + 4096, k=FAKE + 4096),
+])
+def test_rotary_outputs_that_overlap(L, kw):
+    assert L.spec_rotary(ctypes.byref(rotary(**kw)), None) == -1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v_pages=FAKE, k_pages=FAKE), dict(k_exp=FAKE, v_exp=FAKE), dict(kv_stride_p=0), dict(kv_stride_h=0),
+    dict(kv_stride_t=64), dict(exp_stride_p=0), dict(exp_stride_h=0),
+])
+def test_caches_that_overlap_are_not_written(L, kw):
+    assert L.spec_kv8_append(ctypes.byref(append(**kw)), None) == -1
+    assert L.spec_paged_attn8(ctypes.byref(paged8(**kw)), None) == -1
 
 
 CACHE = [
