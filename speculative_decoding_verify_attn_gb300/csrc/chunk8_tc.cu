@@ -5,8 +5,8 @@
 //   and probabilities.  fp16 holds e4m3 exactly and probabilities better than bf16.
 //   warps 0-3, 5-7  loaders: groups of 32 keys of a K or V tile go to them in turn.  A thread reads 16 bytes of a
 //                 key at a time and stores 32 bytes of fp16 where the tensor core wants them; the next group's page
-//                 ids come meanwhile.  Values go through registers: a ring of raw tiles in shared memory would add
-//                 512 cycles of its port to the 1536 that the products' operands take per 128 keys.
+//                 ids come meanwhile.  Values go through registers: raw rows in shared memory would add 512 cycles
+//                 of its port to the 1536 that the products' operands take per 128 keys (810 us instead of 798).
 //   warp 4        MMA issuer (one lane), as there.
 //   warps 8-15    two warpgroups, a thread per query row.
 // Scales: the 32 keys of a group are brought to their largest exponent by an exact fp16 product (nothing is done
@@ -20,7 +20,7 @@
 // Measured (32/8 heads of 128): a 2048-token chunk at 32K 0.79 ms, 1.35 PFLOP/s, 71% of the measured matrix rate.  128
 // keys take 3500 cycles, 2050 of them products: the issuer waits 500 for tiles and 500 for probabilities, and its
 // products run slower beside the loaders' stores.  24 sequences of 0-384 tokens, 16/4 heads of 64, 0.10 ms of 0.13.
-// TMEM columns (512): block w at 256 w: S [0, 128), P over [0, 64), O [128, 128 + D).
+// TMEM columns (512): block w at 256 w: S [0, 128), O [128, 128 + D), P over S's first 64 or, for rows of 64, in the last 64.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -52,6 +52,9 @@ template <int D>
 struct C8 {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kC8Half;       // a K or V tile, or a Q block
+  // P has columns of its own where there are enough, so that S outlives it and the softmax can go over halves in a loop:
+  // nothing spills (24 mixed sequences: 130 us without, 128.5 with)
+  static constexpr bool kApart = D == 64;
   static constexpr int kStages = D == 128 ? 4 : 8;      // 128 KB; what is left is L1's
   static constexpr size_t kSmem = 1024 + 2 * (size_t)kTile + (size_t)kStages * kTile;
   static_assert(kSmem + 2048 <= 227 * 1024, "with the statically allocated part");
@@ -61,6 +64,8 @@ struct C8 {
 
 __device__ __forceinline__ uint32_t c8_col_s(int w) { return 256u * w; }
 __device__ __forceinline__ uint32_t c8_col_o(int w) { return 256u * w + 128u; }
+template <int D>
+__device__ __forceinline__ uint32_t c8_col_p(int w) { return C8<D>::kApart ? c8_col_o(w) + D : c8_col_s(w); }
 
 // Units of the piece that block w's rows see: [b0, b1), empty for a block without rows.
 __device__ __forceinline__ void c8_block_units(const ServeAttnParams& p, const PieceItem& it, int w, int& b0, int& b1) {
@@ -168,47 +173,69 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       slot = t - col * p.page_size;
       page = __ldg(p.table + (int64_t)b * p.table_stride + col);
     };
-    // the group whose values are on their way
-    uint4 raw[4 * NH];
-    int now = 0;                      // unit * 8 + group
+    // the group that comes next: where its rows lie, and its exponents on their way
+    int64_t off[4];
+    const uint8_t* base = nullptr;
+    int coming = 0;                   // unit * 8 + group
     bool live = false;                // this lane's key has a page
     uint32_t byte = 0, v_byte = 0;    // its exponent; a K group also looks after V's
+    // Rows of 64: its addresses are made before the present group is stored, and its loads go out right behind (24 mixed
+    // sequences 133.3 us without, 130.5 with).  Rows of 128 do not wait for memory most (a 2048-token chunk at 32K 789 and 796 us).
+    constexpr bool kEarly = D == 64;
+    uint4 raw[4 * NH];
     auto load = [&]() {
-      now = unit * 8 + grp;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          raw[i * NH + h] = off[i] >= 0 ? __ldcg(reinterpret_cast<const uint4*>(base + off[i] + h * 64)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto prepare = [&]() {
+      coming = unit * 8 + grp;
       live = in && page >= 0 && page < p.num_pages;
       if (in && !live) chunk_report<LIGHT>(p, (uint32_t)SPEC_STATUS_BAD_PAGE);
       __syncwarp();
       const int64_t mine = live ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)g * p.kv_sh : -1;
-      const uint8_t* base = reinterpret_cast<const uint8_t*>(grp < 4 ? p.k : p.v) + cl * 16;
+      base = reinterpret_cast<const uint8_t*>(grp < 4 ? p.k : p.v) + cl * 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t off = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-          raw[i * NH + h] = off >= 0 ? __ldcg(reinterpret_cast<const uint4*>(base + off + h * 64)) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
+      if constexpr (!kEarly) load();
       if (live) {
         const int64_t at = (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
         byte = (grp < 4 ? p.k_exp : p.v_exp)[at];
         if (grp < 4) v_byte = p.v_exp[at];
       }
     };
-    // the values in `raw` to their stage, at the group's largest exponent; false after a wait that ran out
-    auto store = [&]() -> bool {
-      const int mine = live ? clamp_exp((int)byte) : 0;
+    bool have = open();  // a group is looked up
+    if (have) look_up();
+    auto next = [&]() {
+      if (!have) return false;
+      prepare();
+      have = advance();
+      if (have) look_up();
+      return true;
+    };
+    bool more = next();
+    if (kEarly && more) load();
+    while (more) {
+      const int now = coming, mine = live ? clamp_exp((int)byte) : 0, v_mine = live ? clamp_exp((int)v_byte) : 0;
       const int top = __reduce_max_sync(0xffffffffu, mine);
-      const bool uneven = __any_sync(0xffffffffu, live && mine != top);
+      const bool uneven = __any_sync(0xffffffffu, mine != 0 && mine != top);
       const int step = now >> 2, s = step % NS;
       if ((now & 7) < 4) {
         // both exponents go out with K, before the scores that need them exist
-        const int vtop = __reduce_max_sync(0xffffffffu, live ? clamp_exp((int)v_byte) : 0);
+        const int vtop = __reduce_max_sync(0xffffffffu, v_mine);
         if (lane == 0) {
           const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0;
           s_scale[(now >> 3) % kC8Units][now & 3] = make_float4(exp2_whole(ke), (float)ve, exp2_whole(-ve), 0.f);
         }
       }
+      if constexpr (kEarly) more = next();
       const bool got = mbar_wait_spin(&empty[s], ((step / NS) & 1) ^ 1u, &s_abort);
-      if (!__all_sync(0xffffffffu, got)) return false;
+      if (!__all_sync(0xffffffffu, got)) {
+        fail();
+        break;
+      }
       const uint32_t dst = stages_u32 + s * C::kTile + ((now & 3) * 32 + rl) * 128;
       // two straight pieces of code: with the choice inside, each chunk's stores wait for its conversions
       auto rows = [&](auto scaled) {
@@ -240,18 +267,8 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       tc::fence_proxy_async_smem();  // every lane's stores, for the tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
-      return true;
-    };
-    bool have = open();  // a group is looked up
-    if (have) look_up();
-    while (have) {
-      load();
-      have = advance();
-      if (have) look_up();
-      if (!store()) {
-        fail();
-        break;
-      }
+      if constexpr (!kEarly) more = next();
+      else if (more) load();
     }
     } else {
     // ------------------------------------------------------------------ MMA issuer (one lane)
@@ -298,7 +315,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
               const uint32_t vb = v_lo + sv * (C::kTile >> 4);
 #pragma unroll
               for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                tc::mma_ts_lo(tmem + c8_col_o(w), tmem + c8_col_s(w) + ks * 8, vb + ks * (2048 >> 4), C::kIdescPV,
+                tc::mma_ts_lo(tmem + c8_col_o(w), tmem + c8_col_p<D>(w) + ks * 8, vb + ks * (2048 >> 4), C::kIdescPV,
                               (ks > 0 || u > b0[w]) ? 1u : 0u);
               if (u == b1[w] - 1) tc::commit(&pvdone[w]);
               ++t[w];
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     const int sub = warp & 3;        // TMEM sub-partition of this warp
     const int m = sub * 32 + lane;   // TMEM lane = row of the block
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
-    const uint32_t sbuf = tl + c8_col_s(w), obuf = tl + c8_col_o(w);
+    const uint32_t sbuf = tl + c8_col_s(w), pbuf = tl + c8_col_p<D>(w), obuf = tl + c8_col_o(w);
     const uint32_t qblock_u32 = qs_u32 + w * C::kTile;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       const bool got = mbar_wait_spin(bar, parity, &s_abort);
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         // P = 2^(s + ev - mu) against the present reference, as fp16 pairs; only where a row's sum says that a
         // score lies far above it (or nothing has been seen yet) is the tile's maximum taken, O rescaled and
         // the tile done again
-        uint32_t pk[64];
+        uint32_t pk[C::kApart ? 32 : 64];
         float sum, lsum;
         bool exact = u == b0;
         for (;;) {
@@ -497,7 +514,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
           }
           const float mu = m_run == neg_inf() ? 0.f : m_run;
           sum = lsum = 0.f;
-          auto chunk = [&](const uint32_t(&v)[32], int c) {
+          auto chunk = [&](const uint32_t(&v)[32], int c, int at) {  // columns 32 c .. to pk[at ..]
             const float4 x = scales[c];
             const float scale = k_scale(x), nmu = x.y - mu;
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
@@ -507,32 +524,47 @@ __global__ void __launch_bounds__(kC8Threads, 1)
               fma2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), scale, nmu, x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               add2(sums[e & 2], sums[(e & 2) + 1], p0, p1);
-              pk[c * 16 + e / 2] = pack_f16(p0, p1);
+              pk[at + e / 2] = pack_f16(p0, p1);
             }
             const float part = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             sum += part;
             lsum = fmaf(part, x.z, lsum);
           };
           uint32_t sa[32], sb[32];
-          tc::ld32(sbuf, sa);
-          tc::ld_wait(sa);
-          tc::ld32(sbuf + 32, sb);
-          chunk(sa, 0);
-          tc::ld_wait(sb);
-          tc::ld32(sbuf + 64, sa);
-          chunk(sb, 1);
-          tc::ld_wait(sa);
-          tc::ld32(sbuf + 96, sb);
-          chunk(sa, 2);
-          tc::ld_wait(sb);
-          chunk(sb, 3);
+          if constexpr (C::kApart) {
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+              tc::ld32(sbuf + c * 32, sa);
+              tc::ld_wait(sa);
+              tc::ld32(sbuf + c * 32 + 32, sb);
+              chunk(sa, c, 0);
+              tc::ld_wait(sb);
+              chunk(sb, c + 1, 16);
+              tc::st32(pbuf + c * 16, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
+            }
+          } else {
+            tc::ld32(sbuf, sa);
+            tc::ld_wait(sa);
+            tc::ld32(sbuf + 32, sb);
+            chunk(sa, 0, 0);
+            tc::ld_wait(sb);
+            tc::ld32(sbuf + 64, sa);
+            chunk(sb, 1, 16);
+            tc::ld_wait(sa);
+            tc::ld32(sbuf + 96, sb);
+            chunk(sa, 2, 32);
+            tc::ld_wait(sb);
+            chunk(sb, 3, 48);
+          }
           if (exact || !__any_sync(0xffffffffu, !(sum <= kC8MaxSum) || m_run == neg_inf())) break;
           exact = true;
         }
         l += lsum;
         __syncwarp();
-        tc::st32(sbuf, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
-        tc::st32(sbuf + 32, reinterpret_cast<uint32_t(&)[32]>(pk[32]));
+        if constexpr (!C::kApart) {
+          tc::st32(pbuf, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
+          tc::st32(pbuf + 32, reinterpret_cast<uint32_t(&)[32]>(pk[32]));
+        }
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
