@@ -183,12 +183,14 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     // sequences 133.3 us without, 130.5 with).  Rows of 128 do not wait for memory most (a 2048-token chunk at 32K 789 and 796 us).
     constexpr bool kEarly = D == 64;
     uint4 raw[4 * NH];
-    auto load = [&]() {
+    auto load = [&](int i) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int h = 0; h < NH; ++h)
+        raw[i * NH + h] = off[i] >= 0 ? __ldcg(reinterpret_cast<const uint4*>(base + off[i] + h * 64)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_all = [&]() {
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-          raw[i * NH + h] = off[i] >= 0 ? __ldcg(reinterpret_cast<const uint4*>(base + off[i] + h * 64)) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i) load(i);
     };
     auto prepare = [&]() {
       coming = unit * 8 + grp;
@@ -198,8 +200,10 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       const int64_t mine = live ? (int64_t)page * p.kv_sp + (int64_t)slot * p.kv_st + (int64_t)g * p.kv_sh : -1;
       base = reinterpret_cast<const uint8_t*>(grp < 4 ? p.k : p.v) + cl * 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
-      if constexpr (!kEarly) load();
+      for (int i = 0; i < 4; ++i) {
+        off[i] = __shfl_sync(0xffffffffu, mine, i * 8 + rl);
+        if constexpr (!kEarly) load(i);
+      }
       if (live) {
         const int64_t at = (int64_t)page * p.exp_sp + (int64_t)g * p.exp_sh + block_of(p, slot);
         byte = (grp < 4 ? p.k_exp : p.v_exp)[at];
@@ -216,15 +220,15 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       return true;
     };
     bool more = next();
-    if (kEarly && more) load();
+    if (kEarly && more) load_all();
     while (more) {
-      const int now = coming, mine = live ? clamp_exp((int)byte) : 0, v_mine = live ? clamp_exp((int)v_byte) : 0;
+      const int now = coming, mine = live ? clamp_exp((int)byte) : 0;
       const int top = __reduce_max_sync(0xffffffffu, mine);
-      const bool uneven = __any_sync(0xffffffffu, mine != 0 && mine != top);
+      const bool uneven = __any_sync(0xffffffffu, live && mine != top);
       const int step = now >> 2, s = step % NS;
       if ((now & 7) < 4) {
         // both exponents go out with K, before the scores that need them exist
-        const int vtop = __reduce_max_sync(0xffffffffu, v_mine);
+        const int vtop = __reduce_max_sync(0xffffffffu, live ? clamp_exp((int)v_byte) : 0);
         if (lane == 0) {
           const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0;
           s_scale[(now >> 3) % kC8Units][now & 3] = make_float4(exp2_whole(ke), (float)ve, exp2_whole(-ve), 0.f);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
       if constexpr (!kEarly) more = next();
-      else if (more) load();
+      else if (more) load_all();
     }
     } else {
     // ------------------------------------------------------------------ MMA issuer (one lane)
