@@ -167,9 +167,10 @@ int spec_kv8_append(const spec_kv8_append_args* args, spec_stream_t stream);
  * Accumulation is fp32.  K, V and the queries enter the products in fp16, which holds e4m3 values and bf16
  *   queries without rounding: queries are scaled by a power of two, one for the rows of a sequence and kv head in
  *   chunks of up to 32 query rows (tokens x heads of the group), one for each row in larger ones, and only parts
- *   below 2^-29 of the largest lose bits.  Probabilities are rounded to fp16.  Larger chunks bring V and K of 32
- *   neighbouring keys to the largest of their blocks' scales; values lose bits there if that is more than 2^15
- *   above their own, and probabilities count as weights of values of that scale.
+ *   below 2^-29 of the largest lose bits.  Probabilities are rounded to fp16 as weights of V's scales, p 2^ev: those
+ *   below 2^-32 of a row's largest lose bits.  Larger chunks bring V and K of 32 neighbouring keys to the largest of their
+ *   blocks' scales where these lie within 2^15 of each other, which is exact (the largest then counts in p 2^ev); keys
+ *   farther apart keep their own scales, which takes longer.
  * ---------------------------------------------------------------------------------------- */
 typedef struct spec_paged8_args {
   int32_t B, Hq, Hkv, D, T, max_q;

@@ -13,7 +13,10 @@
 // where they share one, as in blocks of 32 tokens or more); K's scale, V's exponent and its inverse scale go to
 // the softmax through shared memory, four of each per tile.  There K's multiplies the scores of its 32
 // columns, and V's is added to the exponent of the probabilities: p' = 2^(s + ev - mu), as in paged8_mma.cu;
-// the sum of the softmax takes p' 2^-ev.
+// the sum of the softmax takes p' 2^-ev.  Keys more than 2^15 apart, which fp16 cannot bring together (a block of zeros
+// has the least scale, one of a rolled back token may have a large one), keep their values as they are, and the softmax
+// scales their scores one by one: in straight loops that the usual tile does not see (it takes 0.80 ms with the code of
+// them and 0.79 without; a chunk with such keys in all tiles 1.4-1.7 ms).
 // mu is 2^8 below the largest s + ev of the piece's first tile: 128 equal scores then stay below 2^15, a sum
 // up to which fp16 holds every p', and steps of 2^-24 are 2^-32 of the largest.
 // Query rows are scaled by powers of two into fp16, in place in shared memory, once per piece.
@@ -47,6 +50,13 @@ constexpr float kC8HeadroomLog2 = 8.f;
 // Units whose exponents are kept: the loaders are at most NS / 2 + 1 units ahead of the issuer, and the issuer
 // one ahead of the softmax that it waits for.
 constexpr int kC8Units = 16;
+// How far the scales of a group's keys may lie apart for their values to be brought to the largest: e4m3's values are
+// multiples of 2^-9, fp16's of 2^-24, so up to there nothing is lost.
+constexpr int kC8Gap = 15;
+// What scores are multiplied by at least: as sums below 2^31, they move by less than 2^-25.  Scores that the softmax has
+// scaled by itself are put back divided by it, at most kC8Most of them.
+constexpr float kC8LeastScale = 1.3877787807814457e-17f;  // 2^-56
+constexpr float kC8Most = 1.1805916207174113e21f;         // 2^70
 
 template <int D>
 struct C8 {
@@ -89,7 +99,9 @@ __global__ void __launch_bounds__(kC8Threads, 1)
   __shared__ uint64_t sfull[2], pfull[2], pvdone[2], ofree[2], qfull[2], drain;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ float4 s_scale[kC8Units][4];  // of a unit's four groups of 32 keys: K's scale, V's exponent, 1 / V's scale
+  // of a unit's four groups of 32 keys: K's scale, V's exponent, 1 / V's scale.  Where scales lie too far apart, V's
+  // exponent is NaN and the last word says which (1 K's, 2 V's) and their largest bytes
+  __shared__ float4 s_scale[kC8Units][4], s_own[8][4];
   __shared__ LightSeqs s_light;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* qs = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // [block][half][128 rows][128 B]
@@ -224,14 +236,19 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     while (more) {
       const int now = coming, mine = live ? clamp_exp((int)byte) : 0;
       const int top = __reduce_max_sync(0xffffffffu, mine);
-      const bool uneven = __any_sync(0xffffffffu, live && mine != top);
+      const bool apart = __any_sync(0xffffffffu, live && mine + kC8Gap < top);
+      const bool uneven = __any_sync(0xffffffffu, live && mine != top) && !apart;
       const int step = now >> 2, s = step % NS;
       if ((now & 7) < 4) {
         // both exponents go out with K, before the scores that need them exist
-        const int vtop = __reduce_max_sync(0xffffffffu, live ? clamp_exp((int)v_byte) : 0);
+        const int v_mine = live ? clamp_exp((int)v_byte) : 0;
+        const int vtop = __reduce_max_sync(0xffffffffu, v_mine);
+        const bool v_apart = __any_sync(0xffffffffu, live && v_mine + kC8Gap < vtop);
         if (lane == 0) {
-          const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0;
-          s_scale[(now >> 3) % kC8Units][now & 3] = make_float4(exp2_whole(ke), (float)ve, exp2_whole(-ve), 0.f);
+          const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0, own = (int)apart | (int)v_apart << 1;
+          s_scale[(now >> 3) % kC8Units][now & 3] =
+              make_float4(exp2_whole(ke), own ? __int_as_float(0x7fffffff) : (float)ve, exp2_whole(-ve),
+                          __int_as_float(own ? own | top << 8 | vtop << 16 : 0));
         }
       }
       if constexpr (kEarly) more = next();
@@ -246,7 +263,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           __half2 f;
-          if constexpr (scaled.value) f = __float2half2_rn(exp2_whole(max(__shfl_sync(0xffffffffu, mine, i * 8 + rl) - top, -24)));
+          if constexpr (scaled.value) f = __float2half2_rn(exp2_whole(max(__shfl_sync(0xffffffffu, mine, i * 8 + rl) - top, -kC8Gap)));
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const uint32_t w[4] = {raw[i * NH + h].x, raw[i * NH + h].y, raw[i * NH + h].z, raw[i * NH + h].w};
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
     PieceItem it;
     int b0 = 0, b1 = 0, tok = -1, head = 0;
     bool have = next_piece(it, b0, b1), ok = true;
-    int base = nbase;
+    int base = nbase, cur = round - 1;  // the piece's place in the list
     float qscale = 0.f;
     if (have) {
       start_q(it, tok, head);
@@ -458,7 +475,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         const bool edge = __any_sync(0xffffffffu, hi < kTcKeys - 1 || lo > 0);
         // what the scores of 32 columns are multiplied by; hidden scores stay -inf
         const float4* scales = s_scale[(base + u) % kC8Units];
-        auto k_scale = [&](const float4& x) { return fmaxf(qscale * x.x, 1.17549435e-38f); };
+        auto k_scale = [&](const float4& x) { return fmaxf(qscale * x.x, kC8LeastScale); };
         // The usual tile is straight code of a few hundred instructions, 32 columns at a time with the next ones on
         // their way (with all 128 in registers beside P the kernel spills, and what spills goes to L2, because
         // shared memory leaves L1 nothing).  What is rare goes over S in TMEM before it, in loops: hidden
@@ -480,13 +497,15 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         }
         // P = 2^(s + ev - mu) against the present reference, as fp16 pairs; only where a row's sum says that a
         // score lies far above it (or nothing has been seen yet) is the tile's maximum taken, O rescaled and
-        // the tile done again
+        // the tile done again.  Keys with scales of their own make the sum a NaN, which comes that way, too: S then
+        // becomes what their scores are, and they are counted apart
         uint32_t pk[C::kApart ? 32 : 64];
         float sum, lsum;
         bool exact = u == b0;
         for (;;) {
           if (exact) {
             float top = neg_inf();
+            uint32_t own = 0u;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
@@ -496,11 +515,56 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               const float4 x = scales[c];
-              if (mx != neg_inf()) top = fmaxf(top, fmaf(mx, k_scale(x), x.y));
+              if (mx != neg_inf()) top = fmaxf(top, fmaf(mx, k_scale(x), x.y));  // not where x.y is NaN
+              own |= __float_as_uint(x.w);
+            }
+            float own_top = -kC8Most, own_sum = 0.f;  // a bound on s, and the sum of 2^(s - it)
+            if (own) {
+              const PieceItem at = piece_item(list.fetch(p, cur));
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t w = __float_as_uint(scales[c].w);
+                if (!w) continue;
+                // the lane's key's bytes, K's below V's, looked up once more (a place for all in shared memory would
+                // leave L1 a step less of it: 830 us instead of 799 for a 2048-token chunk at 32K)
+                uint32_t mine = 0u;
+                const int t = u * kTcKeys + c * 32 + lane;
+                if (t >= at.s.lo && t < at.s.len) {
+                  int page, slot;
+                  page_slot(p, at.b, t, page, slot);
+                  if (page >= 0) {
+                    const int64_t place = (int64_t)page * p.exp_sp + (int64_t)at.g * p.exp_sh + block_of(p, slot);
+                    mine = (uint32_t)clamp_exp(p.k_exp[place]) | (uint32_t)clamp_exp(p.v_exp[place]) << 8;
+                  }
+                }
+                if (!(w & 1u)) mine = (mine & 0xff00u) | (w >> 8 & 0xffu);
+                if (!(w & 2u)) mine = (mine & 0xffu) | (w >> 8 & 0xff00u);
+#pragma unroll 1
+                for (int d = 0; d < 32; d += 8) {
+                  uint32_t v[8];
+                  tc::ld8_wait(sbuf + c * 32 + d, v);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const uint32_t b = __shfl_sync(0xffffffffu, mine, d + e);
+                    const float s = __uint_as_float(v[e]) * fmaxf(qscale * __uint_as_float((b & 0xffu) << 23), 1.17549435e-38f);
+                    const float z = s + (float)((int)(b >> 8) - 127), to = fmaxf(own_top, s);
+                    top = fmaxf(top, z);
+                    own_sum = own_sum * ex2_approx(own_top - to) + ex2_approx(s - to);
+                    own_top = to;
+                    if (s != neg_inf()) v[e] = __float_as_uint(fminf(fmaxf(z, -kC8Most), kC8Most) * (1.f / kC8LeastScale));
+                  }
+                  tc::st8(sbuf + c * 32 + d, v);
+                }
+              }
+              tc::st_wait();
+              if (lane < 4) s_own[warp - 8][lane] = scales[lane].w != 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : scales[lane];
+              __syncwarp();
+              scales = s_own[warp - 8];
             }
             const float m_new = top == neg_inf() ? m_run : fmaxf(m_run, top - kC8HeadroomLog2);
             const float alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - m_new);
             l *= alpha;
+            if (own_sum > 0.f) l = fmaf(own_sum, ex2_approx(own_top - m_new), l);
             m_run = m_new;
             if (u > b0) {
               // the P V before has completed: this tile's Q K^T, issued after it, has
@@ -668,6 +732,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       have = have_next;
       it = nx;
       base = nbase;
+      cur = round - 1;
       qscale = next_scale;
       b0 = nb0;
       b1 = nb1;

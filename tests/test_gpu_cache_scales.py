@@ -1,0 +1,91 @@
+"""spec_paged_attn8 over block scales far apart among 32 neighbouring keys, where the large one may be hidden from a row.
+Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them but through W."""
+
+import numpy as np
+import pytest
+
+from .helpers import torch_mod
+from .test_gpu_cache import i32, np64
+from .test_gpu_cache_attn import SENTINEL, Attn, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verify_attn_gb300 as sv
+    sv.lib()
+    return sv
+
+
+def blocks_of(c, tokens):
+    """Indices (page, block) of these tokens of sequence 0."""
+    tokens = np.asarray(tokens)
+    return c.table[0, tokens // c.page], tokens % c.page // c.block
+
+
+def in_few_rows(sv, c, ref, A, W, S):
+    """The rows of a chunk again, in calls of up to 32 query rows per KV head."""
+    torch = torch_mod()
+    n, length, r0, most = int(c.start[1] - c.start[0]), int(c.kv_len[0]), int(c.start[0]), 32 // c.G
+    for j in range(0, n, most):
+        m = min(most, n - j)
+        o = torch.full(c.q.shape, SENTINEL, device="cuda")
+        sv.spec_paged_attn8(c.d_q, *c.d_codes, *c.d_exps, c.d_table, i32([r0 + j, r0 + j + m]), i32([length - n + j + m]), o,
+                            max_q=m, window=c.window)
+        rows = slice(r0 + j, r0 + j + m)
+        check(np64(o)[rows], ref[rows], A[rows], W[rows], S, c.D, length, "f32", f"few rows from {j}")
+
+
+@pytest.mark.parametrize("where", ["in view", "later", "before the window"])
+@pytest.mark.parametrize("page,block", [(32, 1), (7, 7), (24, 24), (48, 24)])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("gap", [15, 16, 24, 25, 26, 40, 120])
+def test_a_large_neighbour(sv, gap, which, page, block, where):
+    """Blocks 2^gap above their neighbours: once seen by all rows, once the chunk's last token, once the first that its
+    first row sees.  What the other rows get does not depend on it.  Keys differ in a value that queries do not look at,
+    so that the scores stay what they were."""
+    D = 64 if gap % 2 else 128
+    c = Attn([70], [300], G=4, Hkv=1, D=D, page=page, block=block, window=100 if where == "before the window" else 0,
+             seed=gap + page)
+    seen = range(300) if c.window == 0 else range(131, 300)
+    tokens = {"in view": list(seen)[3::37], "later": [299], "before the window": [131]}[where]
+    low = 120 if gap < 60 else 66
+    r0, r1 = c.start[0], c.start[1]
+    for i, e in enumerate(c.exps):
+        far = which in ("kv"[i], "both")
+        e[:] = c.rng.integers(low - 3, low + 1, e.shape) if far else c.rng.integers(117, 121, e.shape)
+        if far:
+            at = blocks_of(c, tokens)
+            e[at[0], :, at[1]] = low + gap
+            if i == 0:
+                c.q[r0:r1] *= 2.0 ** (120 - low)
+                c.q[r0:r1, :, 0] = 0.0
+                big = np.zeros(c.codes[0].shape[2], bool)
+                for page_id, blk in set(zip(*at)):
+                    big[:] = False
+                    big[blk * block:(blk + 1) * block] = True
+                    k = c.codes[0][page_id][:, big]
+                    k[..., 1:] = np.where(k[..., 1:] == 0x7F, 0x7F, 0)
+                    c.codes[0][page_id][:, big] = k
+    ref = c.reference()[0]
+    c.verify(sv)
+    in_few_rows(sv, c, *ref)
+
+
+@pytest.mark.parametrize("q_len", [[5], [64]])
+@pytest.mark.parametrize("seed", range(6))
+def test_random_scales(sv, seed, q_len):
+    """Scales of both kinds drawn per block from 2^-20 to 2^20, some of the blocks empty."""
+    rng = np.random.default_rng(seed)
+    page = int(rng.choice([8, 24, 32, 64]))
+    block = int(rng.choice([b for b in (1, 2, 3, 4, 8, 12, 24, 32) if page % b == 0]))
+    c = Attn(q_len, [int(rng.integers(70, 900))], G=4, Hkv=2, D=int(rng.choice([64, 128])), page=page, block=block,
+             window=int(rng.choice([0, 40])), seed=seed)
+    c.exps[1][:] = c.rng.integers(107, 148, c.exps[1].shape)
+    empty = c.rng.random(c.exps[1].shape) < 0.2
+    for x, e in zip(c.codes, c.exps):
+        e[empty] = 63
+        x[np.repeat(empty, block, axis=-1) & (x[..., 0] != 0x7F)] = 0
+    c.exps[0][~empty] = c.rng.integers(90, 121, c.exps[0].shape)[~empty]
+    c.verify(sv)
