@@ -15,8 +15,9 @@
 // columns, and V's is added to the exponent of the probabilities: p' = 2^(s + ev - mu), as in paged8_mma.cu;
 // the sum of the softmax takes p' 2^-ev.  Keys more than 2^15 apart, which fp16 cannot bring together (a block of zeros
 // has the least scale, one of a rolled back token may have a large one), keep their values as they are, and the softmax
-// scales their scores one by one: in straight loops that the usual tile does not see (it takes 0.80 ms with the code of
-// them and 0.79 without; a chunk with such keys in all tiles 1.4-1.7 ms).
+// scales their scores one by one and counts them without V's scale, as it does where that is far from 1: in loops that the
+// usual tile does not see (it takes 0.80 ms with the code of them and 0.79 without; a chunk with such keys in all tiles
+// 1.4-1.7 ms).
 // mu is 2^8 below the largest s + ev of the piece's first tile: 128 equal scores then stay below 2^15, a sum
 // up to which fp16 holds every p', and steps of 2^-24 are 2^-32 of the largest.
 // Query rows are scaled by powers of two into fp16, in place in shared memory, once per piece.
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   // of a unit's four groups of 32 keys: K's scale, V's exponent, 1 / V's scale.  Where scales lie too far apart, V's
-  // exponent is NaN and the last word says which (1 K's, 2 V's) and their largest bytes
+  // exponent is NaN and the last word says which (1 K's, 2 V's; 4: some of V's are far from 1) and their largest bytes
   __shared__ float4 s_scale[kC8Units][4], s_own[8][4];
   __shared__ LightSeqs s_light;
   const uint32_t raw = smem_u32(smem_raw);
@@ -243,9 +244,10 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         // both exponents go out with K, before the scores that need them exist
         const int v_mine = live ? clamp_exp((int)v_byte) : 0;
         const int vtop = __reduce_max_sync(0xffffffffu, v_mine);
-        const bool v_apart = __any_sync(0xffffffffu, live && v_mine + kC8Gap < vtop);
+        const bool v_own = __any_sync(0xffffffffu, live && (v_mine + kC8Gap < vtop || far_scale(v_mine)));
+        const bool v_apart = v_own && __any_sync(0xffffffffu, live && v_mine + kC8Gap < vtop);
         if (lane == 0) {
-          const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0, own = (int)apart | (int)v_apart << 1;
+          const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0, own = (int)apart | (int)v_apart << 1 | (int)v_own << 2;
           s_scale[(now >> 3) % kC8Units][now & 3] =
               make_float4(exp2_whole(ke), own ? __int_as_float(0x7fffffff) : (float)ve, exp2_whole(-ve),
                           __int_as_float(own ? own | top << 8 | vtop << 16 : 0));
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
             }
             const float m_new = top == neg_inf() ? m_run : fmaxf(m_run, top - kC8HeadroomLog2);
             const float alpha = m_run == neg_inf() ? 0.f : ex2_approx(m_run - m_new);
-            l *= alpha;
+            l = m_run == neg_inf() ? 0.f : scale_sum(l, m_run - m_new, alpha);
             if (own_sum > 0.f) l = fmaf(own_sum, ex2_approx(own_top - m_new), l);
             m_run = m_new;
             if (u > b0) {
@@ -659,6 +661,8 @@ __global__ void __launch_bounds__(kC8Threads, 1)
       tc::fence_after();
       if (it.slot >= 0) {
         const int64_t rec = it.slot;
+        const int up = sum_shift(l);
+        const float f = exp2_whole(-up);
         float* dst = p.part_o + rec * D * kTcRows + w * 128 + m;
         uint32_t v[32];
 #pragma unroll 1
@@ -667,9 +671,9 @@ __global__ void __launch_bounds__(kC8Threads, 1)
           tc::ld32(obuf + c * 32, v);
           tc::ld_wait(v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) dst[(c * 32 + e) * kTcRows] = __uint_as_float(v[e]);
+          for (int e = 0; e < 32; ++e) dst[(c * 32 + e) * kTcRows] = __uint_as_float(v[e]) * f;
         }
-        p.part_ml[rec * kTcRows + w * 128 + m] = make_float2(m_run, l);
+        p.part_ml[rec * kTcRows + w * 128 + m] = make_float2(m_run + up, l * f);
       } else {
         // not unrolled: this code runs once per piece and its instructions come from far; 32 columns'
         // worth of them, fetched once, halve the time of four times as many

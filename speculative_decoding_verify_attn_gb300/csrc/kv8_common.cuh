@@ -86,4 +86,22 @@ __device__ __forceinline__ float q_factor(float inverse, float scale_log2) {
   return fminf(inverse * scale_log2, 4.611686018427388e18f);  // 2^62
 }
 
+// ---- the softmax's sum where V's scales lie far apart.  Probabilities carry V's scale, p' = 2^(s + ev - R), and the
+// sum takes p' 2^-ev.  The p' of a key whose scale is 2^100 below another's can leave the range of floats although
+// the key counts as much as the other.  Where V's scales lie within 2^-28 .. 2^28 that cannot be: a key whose weight is
+// within 2^-30 of the largest has p' > 2^-(28 + 64 + 30), whatever the others' scales.  Elsewhere the sum takes 2^(s - R).
+constexpr int kFarExp = 28;
+__device__ __forceinline__ bool far_scale(int byte) { return byte < 127 - kFarExp || byte > 127 + kFarExp; }
+// l 2^x with f = 2^x, which may be below the range of floats where the product is not.
+__device__ __forceinline__ float scale_sum(float l, float x, float f) {
+  const float h = ex2_approx(0.5f * x);
+  return x > -100.f ? l * f : l * h * h;
+}
+// The power of two by which a record's sum and values are divided (and its reference raised), so that no weight
+// 2^(R_i - R) leaves the range before its sum is multiplied in; 0 for the usual sums.
+__device__ __forceinline__ int sum_shift(float l) {
+  const int k = (int)(__float_as_uint(l) >> 23) - 127;
+  return l > 0.f && (k > 40 || k < -40) ? min(max(k, -100), 100) : 0;
+}
+
 }  // namespace specv

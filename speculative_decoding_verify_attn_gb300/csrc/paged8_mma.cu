@@ -16,7 +16,8 @@
 //   registers they left too few (32 rows of 128: 304 us with them, 115 without).
 //   A block's K scale multiplies the tile's scores.  Its V scale 2^ev goes into the exponent of the
 //   probabilities, p' = 2^(s + ev - R), with R kept near the largest s + ev: p' then fits fp16 for whatever
-//   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev.
+//   scales, and weighs keys as they weigh in the output.  The sum of the softmax takes p' 2^-ev, or, where a unit's scales
+//   are far from 1, 2^(s - R) (kv8_common.cuh says why).
 //   fp16 holds p' <= 2^15 and rounds to steps of 2^-24, so R is set 2^7 below the maximum: what a
 //   probability of the largest key's size loses is then below 2^-32 of it.
 //   The query's rows are scaled into fp16 by one power of two, undone on the scores together with K's scale (a
@@ -114,8 +115,11 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
   uint8_t k_byte = 127, v_byte = 127;  // of this lane's key of the unit issued last; they reach s_scale one unit later
   bool seen = false;                   // whether that key lies in [lo, len)
   int scale_stage = -1;
+  uint32_t far = 0;  // bit of a stage: V's scales are such that the sum is not taken from the probabilities
   auto issue = [&](int stage) {
     if (scale_stage >= 0) {
+      const bool any = __any_sync(0xffffffffu, seen && far_scale(v_byte));
+      far = (far & ~(1u << scale_stage)) | (uint32_t)any << scale_stage;
       s_scale[warp][scale_stage][lane] = make_float2(exp2_whole(clamp_exp(k_byte) - 127), seen ? (float)(clamp_exp(v_byte) - 127) : neg_inf());
     }
     scale_stage = -1;
@@ -323,8 +327,8 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           const float mn = fmaxf(m_run[nr][h], x - kHeadroomLog2);
           f[h] = ex2_approx(m_run[nr][h] - mn);
+          l_run[nr][h] = scale_sum(l_run[nr][h], m_run[nr][h] - mn, f[h]);
           m_run[nr][h] = mn;
-          l_run[nr][h] *= f[h];
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -335,12 +339,26 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
         }
       }
     }
+    const bool far_stage = far >> stage & 1u;
+    if (__builtin_expect(far_stage, 0)) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const float va = fmaxf(s_scale[warp][stage][kt * 16 + gid].y, -64.f);
+        const float vb = fmaxf(s_scale[warp][stage][kt * 16 + gid + 8].y, -64.f);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            l_run[nr][i & 1] += ex2_approx(s[kt][nr][i] - m_run[nr][i & 1] - (i < 2 ? va : vb));
+      }
+    }
     uint32_t pf[KT][NR][2];  // P^T as the B operand: 16 keys x 8 rows
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       // 2^-ev; finite where ev is -inf, whose e is 0
-      const float ia = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid].y), -kNoReference);
-      const float ib = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid + 8].y), -kNoReference);
+      const float most = far_stage ? 0.f : -kNoReference;
+      const float ia = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid].y), most);
+      const float ib = fminf(ex2_approx(-s_scale[warp][stage][kt * 16 + gid + 8].y), most);
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         float e[4];
@@ -411,11 +429,12 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float2 v = s_ml[w][r];
-          L += ex2_approx(v.x - top) * v.y;
+          L += scale_sum(v.y, v.x - top, ex2_approx(v.x - top));
         }
-        const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+        const int up = sum_shift(L);
+        const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : exp2_whole(-up);
         if (!whole && r < rows && warp < 8 && lane == 0)
-          p.part_ml[rec * kMmaMaxRows + r] = make_float2(top == kNoReference ? neg_inf() : top, L);
+          p.part_ml[rec * kMmaMaxRows + r] = make_float2(top == kNoReference ? neg_inf() : top + up, L * inv);
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += M::kCols) {
 #pragma unroll
@@ -443,8 +462,8 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
             }
             if (!whole) {
               float* dst = p.part_o + (rec * kMmaMaxRows + r) * D + c0 + col;
-              if constexpr (E == 2) *reinterpret_cast<float2*>(dst) = make_float2(sum[0], sum[1]);
-              else dst[0] = sum[0];
+              if constexpr (E == 2) *reinterpret_cast<float2*>(dst) = make_float2(sum[0] * inv, sum[1] * inv);
+              else dst[0] = sum[0] * inv;
             } else {
               const int64_t off = o_offset(p, cw.s, cw.g, r) + c0 + col;
 #pragma unroll

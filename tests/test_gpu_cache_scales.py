@@ -1,8 +1,10 @@
-"""spec_paged_attn8 over block scales far apart among 32 neighbouring keys, where the large one may be hidden from a row.
-Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them but through W."""
+"""spec_paged_attn8 over block scales far apart: among 32 neighbouring keys, where the large one may be hidden from a row,
+and from one end of the range to the other, where the normaliser has to count keys whose values hardly matter.  Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them but through W."""
 
 import numpy as np
 import pytest
+
+from oracle import cache as oc
 
 from .helpers import torch_mod
 from .test_gpu_cache import i32, np64
@@ -89,3 +91,51 @@ def test_random_scales(sv, seed, q_len):
         x[np.repeat(empty, block, axis=-1) & (x[..., 0] != 0x7F)] = 0
     c.exps[0][~empty] = c.rng.integers(90, 121, c.exps[0].shape)[~empty]
     c.verify(sv)
+
+
+def rising(c, codes, byte):
+    """Keys of sequence 0 whose score with a row (1, 0, 0, ...) is what `codes` says, times 2^(byte - 127)."""
+    c.q[:] = 0.0
+    c.q[:, :, 0] = 1.0
+    for t, code in enumerate(codes):
+        page, slot = c.table[0, t // c.page], t % c.page
+        c.codes[0][page, :, slot] = 0
+        c.codes[0][page, :, slot, 0] = code
+    c.exps[0][:] = byte
+
+
+@pytest.mark.parametrize("order", ["falling", "rising", "mixed"])
+@pytest.mark.parametrize("q,length", [(2, 300), (3, 9000), (60, 300), (60, 5000)])
+def test_normaliser_over_the_whole_range(sv, q, length, order):
+    """Equal scores, and V's scales from 2^-64 to 2^64: values of the smallest do not show beside the largest, but their
+    keys count as much.  In one tile, in several, in the shares of several CTAs."""
+    c = Attn([q], [length], G=4, Hkv=2, D=64 if q % 2 else 128, page=32, block=32, seed=q)
+    rising(c, [0] * length, 127)
+    t = np.arange(length) // 32
+    last = t[-1]
+    byte = {"falling": np.where(t == 0, 191, 63), "rising": np.where(t == last, 191, 63),
+            "mixed": np.where(t == last // 2, 191, np.where(t % 3 == 1, 66, 63))}[order]
+    c.exps[1][c.table[0, t], :, 0] = byte[:, None]
+    c.verify(sv)
+
+
+@pytest.mark.parametrize("block", [1, 8, 32])
+@pytest.mark.parametrize("q,length", [(2, 700), (60, 700), (64, 4000)])
+@pytest.mark.parametrize("steps", [4, 10, 16])
+def test_normaliser_of_unequal_scores(sv, q, length, block, steps):
+    """The keys of large scale have scores above the others', by up to 2^steps in the weight: what is counted of the small
+    ones lies far below the range of the products."""
+    c = Attn([q], [length], G=2, Hkv=1, D=64, page=32, block=block, seed=q + steps)
+    at, blk = blocks_of(c, np.arange(length))
+    large = c.rng.random(c.exps[1].shape) < 0.03
+    large[c.table[0, 0]] = True
+    big = large[at, 0, blk]
+    rising(c, np.where(big, 0x38, 0), 127)         # scores 1 and 0, times scale
+    c.exps[1][:] = np.where(large, 191, 66)
+    ln2 = float(np.log(2.0))
+    ref, A, W, S = oc.paged_attn8(
+        np64(c.q), c.codes, c.exps, c.table, c.start, c.kv_len, 0, steps * ln2)
+    o, st = c.run(sv, scale=steps * ln2)
+    r0, r1 = c.start[0], c.start[1]
+    assert st == 0
+    check(o[r0:r1], ref[r0:r1], A[r0:r1], W[r0:r1], S, 64, length, "f32")
