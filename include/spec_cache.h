@@ -163,7 +163,7 @@ int spec_kv8_append(const spec_kv8_append_args* args, spec_stream_t stream);
  *   sees the new tokens as the cache holds them.
  * Types: q and k_new / v_new SPEC_BF16; o_dtype SPEC_F32 or SPEC_BF16.
  * Layout of the cache as spec_kv8_append.
- * Finiteness as there; besides, a row's largest |q| times scale is below 2^70.
+ * Finiteness as there; besides, a row's largest |q| times scale is below 2^70 (else that row's o is unspecified).
  * Accumulation is fp32.  K, V and the queries enter the products in fp16, which holds e4m3 values and bf16
  *   queries without rounding: queries are scaled by a power of two, one for the rows of a sequence and kv head in
  *   chunks of up to 32 query rows (tokens x heads of the group), one for each row in larger ones, and only parts

@@ -41,6 +41,8 @@ constexpr float kRescaleLog2 = 15.0f;
 constexpr float kHeadroomLog2 = 7.0f;
 // The reference of a row that has seen no key: every score lies above it, and 2^(-inf - it) is 0.
 constexpr float kNoReference = -3.402823466e38f;
+// A row's largest |q| times scale stays below 2^70; here times log2(e).
+constexpr float kMaxQueryLog2 = 1.1805916207174113e21f * kLog2e;
 
 template <int D, int NR>
 struct Mma8 {
@@ -203,7 +205,17 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
           for (int i = 0; i < 2; ++i)
             amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
         }
-        amax = warp_max(amax);
+        // a row that is not finite, or beyond what a row may be, must not take the others' bits: it counts as zeros
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (!(amax * p.scale_log2 < kMaxQueryLog2)) {
+          amax = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) raw[ks] = make_uint2(0u, 0u);
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
         if (lane == 0) s_amax[warp] = amax;
       }
       __syncthreads();  // the part before has ended with one, too

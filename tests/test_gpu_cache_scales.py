@@ -1,5 +1,7 @@
 """spec_paged_attn8 over block scales far apart: among 32 neighbouring keys, where the large one may be hidden from a row,
-and from one end of the range to the other, where the normaliser has to count keys whose values hardly matter.  Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them but through W."""
+and from one end of the range to the other, where the normaliser has to count keys whose values hardly matter; and over
+query rows that are not finite beside others.  Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them
+but through W."""
 
 import numpy as np
 import pytest
@@ -139,3 +141,18 @@ def test_normaliser_of_unequal_scores(sv, q, length, block, steps):
     r0, r1 = c.start[0], c.start[1]
     assert st == 0
     check(o[r0:r1], ref[r0:r1], A[r0:r1], W[r0:r1], S, 64, length, "f32")
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan"), 2.0 ** 126])
+@pytest.mark.parametrize("q,length", [(1, 200), (5, 200), (5, 9000), (60, 200)])
+def test_a_row_that_is_not_finite_is_alone(sv, q, length, value):
+    """A query row that is not finite, or too large, leaves the other rows as they are, those of its token and KV head too."""
+    c = Attn([q], [length], G=4, Hkv=2, D=64, seed=9)
+    ref, A, W, S = c.reference()[0]
+    r0, r1 = int(c.start[0]), int(c.start[1])
+    c.q[r0 + q // 2, 5, 7] = value
+    o, st = c.run(sv)
+    keep = np.ones((q, 8), bool)
+    keep[q // 2, 5] = False
+    assert st == 0
+    check(o[r0:r1][keep], ref[r0:r1][keep], A[r0:r1][keep], W[r0:r1][keep], S, 64, length, "f32")
