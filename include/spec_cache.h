@@ -206,8 +206,8 @@ int spec_paged_attn8(const spec_paged8_args* args, spec_stream_t stream);
  * spec_page_fork
  *
  * One step of a batch of sequences whose pages may be shared.  Row b holds the pages page_table[b, 0 ..
- * held[b] - 1]; refs[p] counts the holders of page p (rows, and whatever else the caller counts there); a page
- * with refs[p] <= 0 is free.  After the call row b goes on from what row parent[b] was:
+ * held[b] - 1]; refs[p] counts the holders of page p (every row that holds it, and whatever else the caller counts
+ * there; a count above 0 that leaves out rows is not noticed); a page with refs[p] <= 0 is free.  After the call row b goes on from what row parent[b] was:
  *     parent[b] == -1: the row is empty (no tokens, no pages); grow[b] does not matter
  *     else: it has the kv_len[parent[b]] tokens of that row and room for grow[b] more, kv_len_out[b] =
  *     kv_len[parent[b]] + grow[b] (what spec_paged_attn takes for a chunk of grow[b] new tokens), and holds
@@ -219,7 +219,7 @@ int spec_paged_attn8(const spec_paged8_args* args, spec_stream_t stream);
  * this call are free in it.
  * All or nothing: with any data error (SPEC_STATUS_BAD_RANGE: a parent outside [-1, B);
  * SPEC_STATUS_BAD_KV_LEN: a length or held count below 0, more tokens than held pages, grow < 0, or more than
- * table_cols pages; SPEC_STATUS_BAD_PAGE: a page id outside [0, num_pages) that is kept or given back;
+ * table_cols pages; SPEC_STATUS_BAD_PAGE: a held entry that is no page, or a page that refs says is free;
  * SPEC_STATUS_NO_PAGE: too few free pages) nothing is changed.
  *
  * Layout: page_table, table_out [B, table_cols] int32 with row strides; held, kv_len, parent, grow (NULL: 0)

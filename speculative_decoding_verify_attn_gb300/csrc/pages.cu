@@ -87,6 +87,7 @@ struct ForkItem {
   int b, c0, parent, held, before, kept, need, grow, last;
   uint32_t bad;                                 // data errors, the same for the warp
   int mine[kPageCols / 32], from[kPageCols / 32];  // entries: the row's own, those it takes over (0 where there are none)
+  int holders[kPageCols / 32];                     // of the row's own, before the call
   // entries [give(), held) are given back, [0, kept) taken over unless they are the row's already
   __device__ __forceinline__ int give() const { return parent == b ? kept : 0; }
   __device__ __forceinline__ int take() const { return parent == b ? 0 : kept; }
@@ -123,6 +124,8 @@ struct ForkItem {
       mine[i] = !bad && c < held ? own[c] : 0;
       from[i] = !bad && c < take() ? theirs[c] : 0;
     }
+#pragma unroll
+    for (int i = 0; i < kPageCols / 32; ++i) holders[i] = mine[i] >= 0 && mine[i] < p.num_pages ? __ldg(p.refs + mine[i]) : 0;
     if (!bad && c0 == 0 && grow > 0 && before % p.page_size != 0) last = theirs[before / p.page_size];
   }
   // to the counts, and what the row becomes to `rows`
@@ -137,7 +140,10 @@ struct ForkItem {
 #pragma unroll
       for (int i = 0; i < kPageCols / 32; ++i) {
         const int c = c0 + i * 32 + lane;
-        if (c < held && good(mine[i]) && c >= give()) atomicSub(p.count + mine[i], 1);
+        if (c < held && good(mine[i])) {
+          if (holders[i] <= 0) wrong = SPEC_STATUS_BAD_PAGE;  // it would go out again as a free page
+          if (c >= give()) atomicSub(p.count + mine[i], 1);
+        }
         if (c < take()) {
           if (good(from[i])) atomicAdd(p.count + from[i], 1);
           p.stage[(int64_t)b * p.cols + c] = from[i];

@@ -32,3 +32,22 @@ def test_fork_checks_the_pages_of_rows_that_stay(sv, row, col, entry, grow):
         for a, ref in zip(got, (b.table, b.held, b.kv_len, b.refs)):
             assert np.array_equal(a, ref)
         assert all(np.array_equal(x, y) for x, y in zip(before, after))
+
+
+@pytest.mark.parametrize("count", [0, -1])
+@pytest.mark.parametrize("parent", [[0, 1, 2, 3], [0, 2, 2, 3], [0, -1, 2, 3]])
+@pytest.mark.parametrize("col", [0, 2, 3])
+def test_fork_reports_held_pages_that_count_as_free(sv, col, parent, count):
+    """A page of a row that nobody is counted to hold would go out as another row's new page."""
+    b = Beams(4, 16, 100, 50, 3, 5, drop=0.0)
+    b.parent = np.array(parent, np.int32)
+    b.kv_len[:], b.held[:], b.grow[:] = 40, 4, 20
+    b.table[:, :4] = np.arange(16).reshape(4, 4)
+    b.refs[:] = np.arange(b.pages) < 16
+    b.refs[4 + col] = count  # row 1's
+    for in_place in (True, False):
+        got, before, after, status = b.run(sv, in_place)
+        assert status == sv.SPEC_STATUS_BAD_PAGE
+        for a, ref in zip(got, (b.table, b.held, b.kv_len, b.refs)):
+            assert np.array_equal(a, ref)
+        assert all(np.array_equal(x, y) for x, y in zip(before, after))
