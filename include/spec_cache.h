@@ -162,7 +162,7 @@ int spec_kv8_append(const spec_kv8_append_args* args, spec_stream_t stream);
  *   k_new / v_new set (both or neither): the call first does what spec_kv8_append does, and the attention
  *   sees the new tokens as the cache holds them.
  * Types: q and k_new / v_new SPEC_BF16; o_dtype SPEC_F32 or SPEC_BF16.
- * Layout of the cache as spec_kv8_append.
+ * Layout of the cache as spec_kv8_append; rows of o do not overlap each other.
  * Finiteness as there; besides, a row's largest |q| times scale is below 2^70 (else that row's o is unspecified).
  * Accumulation is fp32.  K, V and the queries enter the products in fp16, which holds e4m3 values and bf16
  *   queries without rounding: queries are scaled by a power of two, one for the rows of a sequence and kv head in
@@ -207,7 +207,8 @@ int spec_paged_attn8(const spec_paged8_args* args, spec_stream_t stream);
  *
  * One step of a batch of sequences whose pages may be shared.  Row b holds the pages page_table[b, 0 ..
  * held[b] - 1]; refs[p] counts the holders of page p (every row that holds it, and whatever else the caller counts
- * there; a count above 0 that leaves out rows is not noticed); a page with refs[p] <= 0 is free.  After the call row b goes on from what row parent[b] was:
+ * there; a count above 0 that leaves out rows is not noticed); a page with refs[p] <= 0 is free.  After the
+ * call row b goes on from what row parent[b] was:
  *     parent[b] == -1: the row is empty (no tokens, no pages); grow[b] does not matter
  *     else: it has the kv_len[parent[b]] tokens of that row and room for grow[b] more, kv_len_out[b] =
  *     kv_len[parent[b]] + grow[b] (what spec_paged_attn takes for a chunk of grow[b] new tokens), and holds

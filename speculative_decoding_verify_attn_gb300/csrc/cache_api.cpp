@@ -316,6 +316,8 @@ int spec_paged_attn8(const spec_paged8_args* a, spec_stream_t stream) {
   if (!cache8_layout(a) || !vector_layout(a->q, 2, a->q_stride_t, a->q_stride_h) || !a->o || a->o_stride_t < 0 ||
       a->o_stride_h < 0 || !aligned(a->o, a->o_dtype == SPEC_F32 ? 4 : 2))
     return SPEC_ERR_INVALID_ARG;
+  // rows of o do not overlap, as far as single strides say
+  if ((a->T > 1 && a->o_stride_t < a->D) || (a->Hq > 1 && a->o_stride_h < a->D)) return SPEC_ERR_INVALID_ARG;
   if (a->k_new && (!cache8_writable(a) || !vector_layout(a->k_new, 2, a->new_stride_t, a->new_stride_h) || !vector_layout(a->v_new, 2, 0, 0)))
     return SPEC_ERR_INVALID_ARG;
   if ((st = check_workspace(a->workspace, a->workspace_bytes, spec_paged_attn8_workspace(a))) != SPEC_OK) return st;
