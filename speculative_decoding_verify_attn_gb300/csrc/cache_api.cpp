@@ -343,7 +343,7 @@ int spec_paged_attn8(const spec_paged8_args* a, spec_stream_t stream) {
   p.unit_keys = specv::kTcKeys;
   p.min_units = 2;
   p.piece_cost = 3.f;
-  p.cut_cost = 7.f;
+  p.cut_cost = 7.f;  // 3, 7 and 12: 24 mixed sequences, rows of 64, 125 us each; 16 of up to 700 tokens, rows of 128, 574, 574 and 560
   p.share_piece = 3;
   specv::chunk_workspace_carve(a->workspace, &p);
   if (a->window > 0 && a->window < keys) keys = a->window;

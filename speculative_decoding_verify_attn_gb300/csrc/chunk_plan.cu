@@ -34,6 +34,7 @@ struct PlanTile {
   int b, row0, u0, u1;
 };
 
+template <bool PIECES>
 __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, int* s_n, int* s_len, int* s_q0) {
   __shared__ uint32_t s_warp[32];
   __shared__ int64_t s_sum[32];
@@ -125,9 +126,10 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   longest = __reduce_max_sync(0xffffffffu, lane < kPlanWarps ? s_warp[lane] : 0u);
   const int64_t all = total * p.Hkv;
-  // Shares are equal with what a piece costs beside its units counted in, in units (0: units alone).  24 mixed
-  // sequences over an 8-bit cache, a piece counting 0, 2, 3, 4 and 5 units: 134.8, 132.1, 131.7, 131.6 and 134.4 us.
-  const int extra = p.share_piece;
+  // Shares are equal with what a piece costs beside its units counted in, in units (0: units alone).  Over an 8-bit cache,
+  // a piece counting 0, 2, 3 and 4 units: 24 mixed sequences, rows of 64, 129.7, 125.3, 125.0 and 124.0 us; 16 of up to 700
+  // tokens at up to 16K, rows of 128, 568, 573, 574 and 593; 8 of 40 tokens at 16K-32K 221, 217, 218 and 219.
+  const int extra = PIECES ? p.share_piece : 0;
   const int per = (int)max((int64_t)p.min_units, (all + (int64_t)extra * tiles * p.Hkv + p.grid - 1) / p.grid);
   // cut only where an estimate says that it beats dealing whole tiles, in units with piece_cost for every
   // piece: whole tiles take the longest one, or as many average ones as waves; shares take the mean, a second cut
@@ -347,6 +349,9 @@ __device__ __forceinline__ void plan_body(const ServeAttnParams& p, int* s_pre, 
 
 // CTA 0 makes the plan (but for light calls); the others (if there are new rows) append: CTA 1 + b + B y takes sequence b, a
 // thread per 16-byte chunk of a row.
+// PIECES: shares count what a piece costs.  Calls without pay nothing for it (3 fp32 prompts 33.6 us; as one kernel, which
+// spilled, 35.2).
+template <bool PIECES>
 __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_constant__ ServeAttnParams p, int elem) {
   pdl_launch_dependents();
   extern __shared__ int s_seq[];  // [B + 1], [B], [B], [B]
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_const
     return;
   }
   if (blockIdx.x == 0) {
-    plan_body(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1, s_seq + 3 * p.B + 1);
+    plan_body<PIECES>(p, s_seq, s_seq + p.B + 1, s_seq + 2 * p.B + 1, s_seq + 3 * p.B + 1);
     return;
   }
   const int b = (blockIdx.x - 1) % p.B, y = (blockIdx.x - 1) / p.B, ny = (gridDim.x - 1) / p.B;
@@ -386,8 +391,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_prepare(const __grid_const
 // Merge of cut tiles: a unit of work is (cut tile of a kv head, block of 128 rows, 8 columns),
 // thread m a row; records are column-major, so a warp's loads of one column are one line.  The pieces'
 // weights 2^(m_i - M) are worked out once per row and unit; loads go out several pieces at a time.
-// A unit is a chain of four trips to memory, so eight CTAs an SM take them (24 mixed sequences over an 8-bit cache 134.6
-// us, with four 138.3, with sixteen 134.5).
+// A unit is a chain of four trips to memory, so eight CTAs an SM take them: 24 mixed sequences over an 8-bit cache 129.7 us,
+// with four 132.7; over bf16 a 2048-token chunk at 32K 713 and 719 us, 16 packed prompts 200.7 and 199.9.
 // Also zeros the rows of sequences with a bad kv_len.
 constexpr int kChunkMergeCols = 8;
 constexpr int kMergeThreads = 128;
@@ -504,9 +509,10 @@ void chunk_workspace_carve(void* ws, ServeAttnParams* p) {
   p->max_tiles = (int)chunk_max_tiles(p->T, p->G, p->B, p->row_tile);
 }
 
-cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
+template <bool PIECES>
+static cudaError_t launch_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
   const int smem = (4 * p.B + 1) * (int)sizeof(int);
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(chunk_prepare), smem);
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(chunk_prepare<PIECES>), smem);
   if (e != cudaSuccess) return e;
   unsigned grid = 1;
   if (p.k_new) {  // about 2400 CTAs at most, one per sequence at least
@@ -514,8 +520,11 @@ cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaS
     const int64_t most = (2400 + p.B - 1) / p.B;
     grid += (unsigned)p.B * (unsigned)(want < most ? want : most);
   }
-  chunk_prepare<<<grid, kPlanThreads, smem, stream>>>(p, elem_bytes);
+  chunk_prepare<PIECES><<<grid, kPlanThreads, smem, stream>>>(p, elem_bytes);
   return cudaGetLastError();
+}
+cudaError_t launch_chunk_prepare(const ServeAttnParams& p, int elem_bytes, cudaStream_t stream) {
+  return p.share_piece > 0 ? launch_prepare<true>(p, elem_bytes, stream) : launch_prepare<false>(p, elem_bytes, stream);
 }
 cudaError_t launch_chunk_merge(const ServeAttnParams& p, cudaStream_t stream) {
   return launch_dependent(chunk_merge, dim3(8 * p.grid), dim3(kMergeThreads), 0, stream, 0u, p);
