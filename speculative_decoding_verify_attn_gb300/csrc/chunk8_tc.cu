@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
         // both exponents go out with K, before the scores that need them exist
         const int v_mine = live ? clamp_exp((int)v_byte) : 0;
         const int vtop = __reduce_max_sync(0xffffffffu, v_mine);
-        const bool v_own = __any_sync(0xffffffffu, live && (v_mine + kC8Gap < vtop || far_scale(v_mine)));
+        const bool v_own = __any_sync(0xffffffffu, live && v_mine < max(vtop - kC8Gap, kFarLow)) || vtop > kFarHigh;
         const bool v_apart = v_own && __any_sync(0xffffffffu, live && v_mine + kC8Gap < vtop);
         if (lane == 0) {
           const int ke = top ? top - 127 : 0, ve = vtop ? vtop - 127 : 0, own = (int)apart | (int)v_apart << 1 | (int)v_own << 2;

@@ -90,8 +90,7 @@ __device__ __forceinline__ float q_factor(float inverse, float scale_log2) {
 // sum takes p' 2^-ev.  The p' of a key whose scale is 2^100 below another's can leave the range of floats although
 // the key counts as much as the other.  Where V's scales lie within 2^-28 .. 2^28 that cannot be: a key whose weight is
 // within 2^-30 of the largest has p' > 2^-(28 + 64 + 30), whatever the others' scales.  Elsewhere the sum takes 2^(s - R).
-constexpr int kFarExp = 28;
-__device__ __forceinline__ bool far_scale(int byte) { return byte < 127 - kFarExp || byte > 127 + kFarExp; }
+constexpr int kFarLow = 127 - 28, kFarHigh = 127 + 28;  // bytes below and above are far
 // l 2^x with f = 2^x, which may be below the range of floats where the product is not.
 __device__ __forceinline__ float scale_sum(float l, float x, float f) {
   const float h = ex2_approx(0.5f * x);

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(Mma8<D, NR>::Cut::THREADS, 1)
   uint32_t far = 0;  // bit of a stage: V's scales are such that the sum is not taken from the probabilities
   auto issue = [&](int stage) {
     if (scale_stage >= 0) {
-      const bool any = __any_sync(0xffffffffu, seen && far_scale(v_byte));
+      const bool any = __any_sync(0xffffffffu, seen && (v_byte < kFarLow || v_byte > kFarHigh));
       far = (far & ~(1u << scale_stage)) | (uint32_t)any << scale_stage;
       s_scale[warp][scale_stage][lane] = make_float2(exp2_whole(clamp_exp(k_byte) - 127), seen ? (float)(clamp_exp(v_byte) - 127) : neg_inf());
     }
