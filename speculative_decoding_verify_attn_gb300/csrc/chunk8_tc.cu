@@ -21,7 +21,7 @@
 // mu is 2^8 below the largest s + ev of the piece's first tile: 128 equal scores then stay below 2^15, a sum
 // up to which fp16 holds every p', and steps of 2^-24 are 2^-32 of the largest.
 // Query rows are scaled by powers of two into fp16, in place in shared memory, once per piece.
-// Measured (32/8 heads of 128): a 2048-token chunk at 32K 0.79 ms, 1.35 PFLOP/s, 71% of the measured matrix rate.  128
+// Measured (32/8 heads of 128): a 2048-token chunk at 32K 0.80 ms, 1.34 PFLOP/s, 70% of the measured matrix rate.  128
 // keys take 3500 cycles, 2050 of them products: the issuer waits 500 for tiles and 500 for probabilities, and its
 // products run slower beside the loaders' stores.  24 sequences of 0-384 tokens, 16/4 heads of 64, 0.10 ms of 0.13.
 // TMEM columns (512): block w at 256 w: S [0, 128), O [128, 128 + D), P over S's first 64 or, for rows of 64, in the last 64.

@@ -23,9 +23,10 @@
 //   The query's rows are scaled into fp16 by one power of two, undone on the scores together with K's scale (a
 //   scale for each row: 20 rows 103 us instead of 98).  Parts below 2^-29 of the largest value lose bits, which
 //   moves a score by at most 2^-39 of what the largest query could reach.
-// Measured (8 sequences of 16K-32K, 32/8 heads of 128, the join included): 4 rows per kv head 65 us (83% of the copy
-// rate), 16 rows 71 us (75%), 20 rows 98 us (71%), 32 rows 110 us; past 16 rows two warps a scheduler leave
-// its fixed latencies open.  In rows of 64: 41 us for 4 rows (66%), 71 for 20.
+// Measured (8 sequences of 16K-32K, 32/8 heads of 128, the join included): 4 rows per kv head 63 us (85% of the copy
+// rate), 16 rows 70 us (76%), 20 rows 100 us (70%), 32 rows 109 us; past 16 rows two warps a scheduler leave
+// its fixed latencies open.  In rows of 64: 40 us for 4 rows (67%), 71 for 20.  Sums by themselves for scales far from 1
+// stand in the loop (16 rows of 128 67 us without them, 4 rows of 64 38.6); in a loop of their own, or a function, they cost as much.
 #include <cuda_runtime.h>
 
 #include "cache_internal.h"
