@@ -3,6 +3,8 @@ and from one end of the range to the other, where the normaliser has to count ke
 query rows that are not finite beside others.  Bounds are those of test_gpu_cache_attn.py: no scale of a neighbour enters them
 but through W."""
 
+import os
+
 import numpy as np
 import pytest
 
@@ -93,6 +95,40 @@ def test_random_scales(sv, seed, q_len):
         x[np.repeat(empty, block, axis=-1) & (x[..., 0] != 0x7F)] = 0
     c.exps[0][~empty] = c.rng.integers(90, 121, c.exps[0].shape)[~empty]
     c.verify(sv)
+
+
+CALLS = int(os.environ.get("SPEC_RANDOM_CALLS", "30"))
+SEED = int(os.environ.get("SPEC_RANDOM_SEED", "0"))
+
+
+@pytest.mark.parametrize("seed", range(SEED, SEED + CALLS))
+def test_random_calls_over_the_whole_range(sv, seed):
+    """V's scales from 2^-64 to 2^64: any, a few of them, one far from the rest; K's large blocks differ in a value that
+    queries do not look at."""
+    rng = np.random.default_rng(12000 + seed)
+    page = int(rng.choice([1, 7, 16, 24, 32, 64]))
+    block = int(rng.choice([b for b in range(1, page + 1) if page % b == 0]))
+    most = int(rng.choice([8, 60, 200]))
+    q = [int(rng.integers(1, most + 1)) for _ in range(int(rng.choice([1, 2, 5])))]
+    c = Attn(q, [n + int(2 ** rng.uniform(0, 11)) for n in q], G=int(rng.choice([1, 4])), Hkv=int(rng.choice([1, 2])),
+             D=int(rng.choice([64, 128])), page=page, block=block, window=int(rng.choice([0, 0, 30])),
+             append=bool(rng.random() < 0.3), seed=seed)
+    lo, hi = sorted(int(x) for x in rng.integers(63, 192, 2))
+    e = c.exps[1]
+    e[:] = (c.rng.integers(lo, hi + 1, e.shape) if seed % 4 < 2 else c.rng.choice([63, 127, 191], e.shape) if seed % 4 == 2 else
+            np.where(c.rng.random(e.shape) < 0.05, hi, lo))
+    if seed % 4 != 1 and not c.do_append:
+        r0, r1 = c.start[0], c.start[-1]
+        low = int(rng.integers(66, 130))
+        far = c.rng.random(c.exps[0].shape) < 0.1
+        c.exps[0][:] = np.where(far, min(low + int(rng.integers(0, 120)), 191), low - c.rng.integers(0, 3, far.shape))
+        c.q[r0:r1] *= 2.0 ** (120 - low)
+        c.q[r0:r1, :, 0] = 0.0
+        codes = c.codes[0]
+        hidden = np.repeat(far, block, axis=-1)[..., None] & (codes != 0x7F)
+        hidden[..., 0] = False
+        codes[hidden] = 0
+    c.verify(sv, what=f"seed {seed}", max_q=int(rng.choice([c.max_q, c.max_q + 40])))
 
 
 def rising(c, codes, byte):
